@@ -12,6 +12,10 @@ Entry points (same names as the C ABI):
 ``gdn_replay_state_updates``  replay of captured (decay, key, delta) records
 ``gdn_state_snapshot``        immutable copy of a state set
 ``gdn_prefill_workspace_bytes``
+``gdn_linear_prefill``        linear attention with a decay for each head, whole sequences
+``gdn_linear_step``           the same token by token, with capture
+``gdn_verify_drafts``         drafted tokens against the target's probabilities
+``gdn_block_norm``            norms around a block, fused with gate, residual and scale
 """
 
 from __future__ import annotations
@@ -31,7 +35,8 @@ EXPORTED = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill_chunk
             "gdn_prefill_chunked_states", "gdn_prefill_chunked_ex", "gdn_recurrent_step",
             "gdn_recurrent_step_ex", "gdn_replay_state_updates", "gdn_state_snapshot",
             "gdn_status_string", "gdn_last_error", "gdn_profile_enable", "gdn_profile_collect",
-            "gdn_prefill_chunked_noalloc")
+            "gdn_prefill_chunked_noalloc", "gdn_linear_workspace_bytes", "gdn_linear_prefill", "gdn_linear_step",
+            "gdn_verify_workspace_bytes", "gdn_verify_drafts", "gdn_block_norm")
 GDN_NOALLOC_SCRATCH_BYTES = 128 * 1024 * 1024
 
 
@@ -62,6 +67,16 @@ class gdn_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32),
                 ("Hv", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class gdn_verify_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("target_row_stride", ctypes.c_int64), ("draft_row_stride", ctypes.c_int64)]
+
+
+class gdn_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int32), ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_act", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -106,6 +121,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_replay_state_updates.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.gdn_state_snapshot.restype = i32
     lib.gdn_state_snapshot.argtypes = [vp, vp, i64, i32, i32, i32, vp]
+    lib.gdn_linear_workspace_bytes.restype = sz
+    lib.gdn_linear_workspace_bytes.argtypes = [shp, i32]
+    lib.gdn_linear_prefill.restype = i32
+    lib.gdn_linear_prefill.argtypes = [shp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+    lib.gdn_linear_step.restype = i32
+    lib.gdn_linear_step.argtypes = [shp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, i32, vp, vp, vp]
+    vshp, nshp = ctypes.POINTER(gdn_verify_shape), ctypes.POINTER(gdn_norm_shape)
+    lib.gdn_verify_workspace_bytes.restype = sz
+    lib.gdn_verify_workspace_bytes.argtypes = [vshp]
+    lib.gdn_verify_drafts.restype = i32
+    lib.gdn_verify_drafts.argtypes = [vshp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gdn_block_norm.restype = i32
+    lib.gdn_block_norm.argtypes = [nshp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [i32]
     lib.gdn_last_error.restype = ctypes.c_char_p
@@ -449,6 +477,258 @@ def gdn_state_snapshot(src, dst=None):
     return dst
 
 
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head, draft verification, block norms
+# ---------------------------------------------------------------------------
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_gpu(dev):
+    """The library reads device memory only; a host pointer would fault the GPU."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors are on {dev}, expected a GPU")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _linear_common(q, k, v, g, scale, initial_state, stride, cu_seqlens, o, final_state, output_final_state):
+    """Checks shared by gdn_linear_prefill and gdn_linear_step."""
+    dev, dtype = q.device, q.dtype
+    sh = _shape_from(q, k, v, scale, cu_seqlens)
+    _need(q, "q")
+    _need(k, "k", dtype, dev)
+    _need(v, "v", dtype, dev)
+    _need(g, "g", torch.float32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    _need(initial_state, "initial_state", torch.float32, dev)
+    if sh.Hq <= 0 or sh.Hv % sh.Hq != 0:
+        raise ValueError(f"Hv={sh.Hv} must be a multiple of Hq={sh.Hq}")
+    ntok = sh.T if cu_seqlens is not None else sh.B * sh.T
+    if k.shape != q.shape:
+        raise ValueError(f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
+    if v.dim() != q.dim() or v.shape[:-2] != q.shape[:-2]:
+        raise ValueError(f"v has shape {tuple(v.shape)}; its leading dims must match q's {tuple(q.shape[:-2])}")
+    if g.dim() == 1:
+        g_stride = 0
+        if g.shape[0] != sh.Hv:
+            raise ValueError(f"g has shape {tuple(g.shape)}, expected {(sh.Hv,)} or {tuple(v.shape[:-1])}")
+    else:
+        g_stride = sh.Hv
+        if g.shape != v.shape[:-1]:
+            raise ValueError(f"g has shape {tuple(g.shape)}, expected {(sh.Hv,)} or {tuple(v.shape[:-1])}")
+    if cu_seqlens is not None and cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be 1-D [N+1]")
+    if o is None:
+        o = torch.empty(v.shape, dtype=dtype, device=dev)
+    else:
+        _need(o, "o", dtype, dev)
+        if o.shape != v.shape:
+            raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(v.shape)}")
+    if final_state is None:
+        if output_final_state:
+            final_state = torch.empty((sh.B, sh.Hv, sh.dk, sh.dv), dtype=torch.float32, device=dev)
+    else:
+        _need(final_state, "final_state", torch.float32, dev)
+    per = sh.Hv * sh.dk * sh.dv
+    if stride is None:
+        stride = 0 if (initial_state is not None and initial_state.shape[0] == 1 and sh.B > 1) else per
+    _check_states(sh, initial_state, int(stride), final_state)
+    return sh, ntok, g_stride, int(stride), o, final_state
+
+
+def gdn_linear_workspace_bytes(shape: gdn_shape, ragged: bool) -> int:
+    """Bytes gdn_linear_prefill needs for this shape (0: none)."""
+    n = load_library().gdn_linear_workspace_bytes(ctypes.byref(shape), int(bool(ragged)))
+    if n == ctypes.c_size_t(-1).value:
+        _check(GDN_ERR_INVALID_ARG)
+    return int(n)
+
+
+def gdn_linear_prefill(q, k, v, g, *, scale=None, initial_state=None, initial_state_batch_stride=None,
+                       cu_seqlens=None, o=None, final_state=None, output_final_state=True, workspace=None):
+    """Linear attention with a decay for each head over whole sequences:
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t, g <= 0.
+
+    Dense q/k [B,T,Hq,dk], v [B,T,Hv,dv]; ragged: the same without B (or B=1)
+    plus cu_seqlens int32 [N+1].  g fp32: log decays [..., Hv] per token, or [Hv]
+    the same at every token.  Returns (o, final_state or None)."""
+    lib = load_library()
+    sh, _, g_stride, stride, o, final_state = _linear_common(
+        q, k, v, g, scale, initial_state, initial_state_batch_stride, cu_seqlens, o, final_state, output_final_state)
+    dev = q.device
+    stream = _on_gpu(dev)
+    ref = ctypes.byref(sh)
+    if workspace is None:
+        need = lib.gdn_linear_workspace_bytes(ref, cu_seqlens is not None)
+        if 0 < need < 1 << 62:   # an invalid shape is named by the call itself
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.gdn_linear_prefill(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
+                                _addr(initial_state), stride, _addr(cu_seqlens), o.data_ptr(), _addr(final_state),
+                                _addr(workspace), nbytes, stream)
+    if st:
+        _check(st)
+    return o, final_state
+
+
+def gdn_linear_step(q, k, v, g, *, scale=None, initial_state=None, initial_state_batch_stride=None, cu_seqlens=None,
+                    o=None, final_state=None, output_final_state=True, state_update_capacity=0, capture_count=None,
+                    state_update=None):
+    """gdn_linear_prefill's recurrence token by token (for a few tokens a row),
+    with g of any sign and optional capture of (decay, key, value) records that
+    gdn_replay_state_updates applies.  Returns (o, final_state or None,
+    state_update or None)."""
+    lib = load_library()
+    sh, _, g_stride, stride, o, final_state = _linear_common(
+        q, k, v, g, scale, initial_state, initial_state_batch_stride, cu_seqlens, o, final_state, output_final_state)
+    dev = q.device
+    cap = int(state_update_capacity)
+    if cap > 0:
+        if capture_count is None:
+            raise ValueError("capture_count is required when state_update_capacity > 0")
+        R = sh.Hv + sh.Hq * sh.dk + sh.Hv * sh.dv
+        if state_update is None:
+            state_update = torch.empty((sh.B, cap, R), dtype=torch.float32, device=dev)
+        _need(state_update, "state_update", torch.float32, dev)
+        _need(capture_count, "capture_count", torch.int32, dev)
+        _expect(capture_count, "capture_count", sh.B, at_least=True)
+        _expect(state_update, "state_update", sh.B * cap * R, at_least=True)
+    stream = _on_gpu(dev)
+    st = lib.gdn_linear_step(ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
+                             _addr(initial_state), stride, _addr(cu_seqlens), o.data_ptr(), _addr(final_state), cap,
+                             _addr(capture_count), _addr(state_update), stream)
+    if st:
+        _check(st)
+    return o, final_state, state_update
+
+
+def _rows3(t, name, B, n, V, dtype, dev):
+    """Elements between the rows of a [B, n, V] tensor whose rows are evenly spaced."""
+    if tuple(t.shape) != (B, n, V):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, n, V)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.numel() == 0:
+        return V
+    s0, s1, s2 = t.stride()
+    if V > 1 and s2 != 1:
+        raise ValueError(f"{name} must be contiguous along the vocabulary")
+    row = s1 if n > 1 else (s0 if B > 1 else V)
+    if row < V or (B > 1 and s0 != n * row):
+        raise ValueError(f"{name} must have evenly spaced rows, got strides {t.stride()}")
+    return row
+
+
+def gdn_verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, *, draft_count=None, tokens=None,
+                      emit_count=None, workspace=None):
+    """Verify drafted tokens against the target's probabilities.
+
+    target_probs [B, K+1, V], draft_probs [B, K, V] of the same dtype (None:
+    deterministic drafts), draft_tokens int32 [B, K], uniforms fp32 [B, K+1] in
+    [0, 1), draft_count int32 [B] (None: K each; negative: idle row).  Rows of
+    the probabilities may be padded (evenly spaced).  Returns (tokens int32
+    [B, K+1] = accepted drafts, one drawn token, then -1; emit_count int32 [B])."""
+    lib = load_library()
+    if target_probs.dim() != 3 or draft_tokens.dim() != 2:
+        raise ValueError("target_probs must be [B, K+1, V] and draft_tokens [B, K]")
+    dev, dtype = target_probs.device, target_probs.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    B, K = draft_tokens.shape
+    V = target_probs.shape[2]
+    ps = _rows3(target_probs, "target_probs", B, K + 1, V, dtype, dev)
+    qs = V if draft_probs is None else _rows3(draft_probs, "draft_probs", B, K, V, dtype, dev)
+    _need(draft_tokens, "draft_tokens", torch.int32, dev)
+    _need(uniforms, "uniforms", torch.float32, dev)
+    _expect(uniforms, "uniforms", B * (K + 1))
+    if draft_count is not None:
+        _need(draft_count, "draft_count", torch.int32, dev)
+        _expect(draft_count, "draft_count", B)
+    if tokens is None:
+        tokens = torch.empty((B, K + 1), dtype=torch.int32, device=dev)
+    else:
+        _need(tokens, "tokens", torch.int32, dev)
+        _expect(tokens, "tokens", B * (K + 1))
+    if emit_count is None:
+        emit_count = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _need(emit_count, "emit_count", torch.int32, dev)
+        _expect(emit_count, "emit_count", B)
+    sh = gdn_verify_shape(B, K, V, _DTYPES[dtype], ps, qs)
+    stream = _on_gpu(dev)
+    ref = ctypes.byref(sh)
+    if workspace is None:
+        need = lib.gdn_verify_workspace_bytes(ref)
+        if 0 < need < 1 << 62:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.gdn_verify_drafts(ref, target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(),
+                               uniforms.data_ptr(), _addr(draft_count), tokens.data_ptr(), emit_count.data_ptr(),
+                               _addr(workspace), nbytes, stream)
+    if st:
+        _check(st)
+    return tokens, emit_count
+
+
+_ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def gdn_block_norm(y, *, gate=None, gate_act="silu", residual=None, residual_scale=1.0, post_weight=None,
+                   next_weight=None, eps=1e-6, out=None, normed=None):
+    """h = residual + residual_scale * act(gate) * RMSNorm_group(y) * post_weight and,
+    with next_weight, normed = RMSNorm(h) * next_weight; every part but y is
+    optional.  y, gate, residual [..., D] of one dtype; the group of the first
+    norm is post_weight's length (D, or one of 16, 32, 64, 128 dividing D);
+    next_weight [D].  ``out`` (h) may be y or residual.  Returns (h, normed or
+    None)."""
+    lib = load_library()
+    dev, dtype = y.device, y.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if gate_act not in _ACTS:
+        raise ValueError(f"gate_act {gate_act!r} is not one of {sorted(_ACTS)}")
+    if y.dim() < 1 or y.shape[-1] < 1:
+        raise ValueError(f"y must be [..., D], got shape {tuple(y.shape)}")
+    if gate is not None and gate_act == "none":
+        raise ValueError("gate is given with gate_act 'none'")
+    _need(y, "y")
+    shape, D = y.shape, y.shape[-1]
+    for t, n in ((gate, "gate"), (residual, "residual"), (out, "out"), (normed, "normed")):
+        if t is not None:
+            _need(t, n, dtype, dev)
+            if t.shape != shape:
+                raise ValueError(f"{n} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    group = D
+    if post_weight is not None:
+        _need(post_weight, "post_weight", dtype, dev)
+        group = post_weight.numel()
+        if group < 1 or D % group != 0:
+            raise ValueError(f"post_weight has {group} elements, expected a divisor of {D}")
+    if next_weight is not None:
+        _need(next_weight, "next_weight", dtype, dev)
+        _expect(next_weight, "next_weight", D)
+        if normed is None:
+            normed = torch.empty_like(y)
+    elif normed is not None:
+        raise ValueError("normed is given without next_weight")
+    if out is None:
+        out = torch.empty_like(y)
+    sh = gdn_norm_shape(y.numel() // D, D, group, _DTYPES[dtype], 0 if gate is None else _ACTS[gate_act],
+                        residual_scale, eps)
+    stream = _on_gpu(dev)
+    st = lib.gdn_block_norm(ctypes.byref(sh), y.data_ptr(), _addr(gate), _addr(residual), _addr(post_weight),
+                            _addr(next_weight), out.data_ptr(), _addr(normed), stream)
+    if st:
+        _check(st)
+    return out, normed
+
+
 def gdn_profile_enable(on: bool = True) -> None:
     """Turn per-kernel HIP-event timing inside the library on or off."""
     _check(load_library().gdn_profile_enable(int(bool(on))))
@@ -469,4 +749,6 @@ __all__ = ["gdn_profile_enable", "gdn_profile_collect", "load_library", "GdnErro
            "gdn_prefill_workspace_bytes", "gdn_prefill_chunked", "gdn_prefill_chunked_states",
            "gdn_prefill_chunked_noalloc", "GDN_NOALLOC_SCRATCH_BYTES",
            "gdn_prefill_chunked_ex", "gdn_recurrent_step_ex", "Prologue", "gdn_prologue",
-           "gdn_recurrent_step", "gdn_replay_state_updates", "gdn_state_snapshot", "EXPORTED", "LIB_PATH"]
+           "gdn_recurrent_step", "gdn_replay_state_updates", "gdn_state_snapshot", "gdn_linear_workspace_bytes",
+           "gdn_linear_prefill", "gdn_linear_step", "gdn_verify_drafts", "gdn_verify_shape", "gdn_block_norm",
+           "gdn_norm_shape", "EXPORTED", "LIB_PATH"]

@@ -17,7 +17,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
-SOURCES = ["gdn_api.cpp", "gdn_profile.cpp", "gdn_recurrent.hip", "gdn_prefill.hip"]
+SOURCES = ["gdn_api.cpp", "gdn_ops_api.cpp", "gdn_profile.cpp", "gdn_recurrent.hip", "gdn_prefill.hip",
+           "gdn_linear_f32.hip", "gdn_linear_f16.hip", "gdn_linear_bf16.hip", "gdn_linear_step.hip",
+           "gdn_verify.hip", "gdn_norm.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 VALU forms are disabled for every HIP translation unit.

@@ -11,11 +11,12 @@
 #include <mutex>
 
 #include "../../include/gdn.h"
+#include "gdn_check.h"
 #include "gdn_internal.h"
 
-namespace {
+namespace gdn {
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 gdn_status fail(gdn_status st, const char* fmt, ...) {
   va_list ap;
@@ -107,6 +108,12 @@ gdn_status check_states(const gdn_shape* sh, const float* s0, int64_t stride, co
   return GDN_OK;
 }
 
+}  // namespace gdn
+
+using namespace gdn;
+
+namespace {
+
 gdn_status check_prologue(const gdn_prologue* pr, gdn::Prologue* out) {
   *out = gdn::Prologue{};
   if (pr == nullptr) return GDN_OK;
@@ -142,7 +149,7 @@ const char* gdn_status_string(gdn_status st) {
   return "unknown gdn_status";
 }
 
-const char* gdn_last_error(void) { return g_last_error; }
+const char* gdn_last_error(void) { return gdn::g_last_error; }
 
 // Workspace: [chunk_offsets: B+1 int32][pad to 16][chunk_info: max_chunks x
 // (first token, length) int32 pairs][pad to 256][per (chunk, value head) blocks].

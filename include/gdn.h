@@ -292,6 +292,149 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
                               int32_t dk, int32_t dv, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head (no delta rule)
+ * ---------------------------------------------------------------------------
+ *
+ *     alpha_t = exp(g_t)
+ *     S_t     = alpha_t S_{t-1} + k_t v_t^T          (S is [dk x dv], fp32)
+ *     o_t     = scale * S_t^T q_t
+ *
+ * with the shapes, layouts, head map, state and cu_seqlens rules of the gated
+ * delta rule above; there is no beta.  `g` holds log decays in fp32:
+ * g_token_stride = Hv for one value per token and value head ([T_total, Hv]),
+ * or 0 for one value per value head ([Hv], the same at every token).
+ *
+ * Precision: o is rounded once to the input dtype; for 16-bit inputs the
+ * products with the state and with the in-chunk scores use those rounded to 16
+ * bits, while the state itself is updated from unrounded terms (fp32).
+ *
+ * Precondition of the prefill: g <= 0 (g = -infinity forgets everything before
+ * the token).  The step takes g of any sign.
+ */
+
+/* Bytes of device workspace gdn_linear_prefill needs for `shape` and the input
+ * form (`ragged` nonzero when cu_seqlens will be passed); 0 is a valid answer
+ * (no workspace needed), (size_t)-1 if the arguments are invalid.  Host only. */
+size_t gdn_linear_workspace_bytes(const gdn_shape* shape, int32_t ragged);
+
+/*
+ * Prefill over whole sequences, in chunks.  initial_state,
+ * initial_state_batch_stride, cu_seqlens, o and final_state as in
+ * gdn_prefill_chunked.  Few, long sequences are split into segments whose
+ * states are computed side by side in `workspace` (16-byte aligned, contents on
+ * entry ignored; may be NULL when gdn_linear_workspace_bytes() is 0).
+ */
+gdn_status gdn_linear_prefill(const gdn_shape* shape, const void* q, const void* k, const void* v,
+                              const float* g, int64_t g_token_stride, const float* initial_state,
+                              int64_t initial_state_batch_stride, const int32_t* cu_seqlens, void* o,
+                              float* final_state, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Token by token over each row, with the arguments of gdn_recurrent_step.
+ * Capture (state_update_capacity > 0): row b writes its first
+ * min(max(capture_count[b], 0), capacity, L_b) records
+ * [alpha (Hv) | k (Hq*dk) | v (Hv*dv)] in fp32 into state_update [B, capacity, R];
+ * other entries are left untouched.  gdn_replay_state_updates applies them
+ * (S = alpha*S + outer(k, v)), bit-identical to this step.
+ */
+gdn_status gdn_linear_step(const gdn_shape* shape, const void* q, const void* k, const void* v,
+                           const float* g, int64_t g_token_stride, const float* initial_state,
+                           int64_t initial_state_batch_stride, const int32_t* cu_seqlens, void* o,
+                           float* final_state, int32_t state_update_capacity, const int32_t* capture_count,
+                           float* state_update, void* stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from
+ * given uniform random numbers (speculative sampling).  For row b with
+ * n_b = min(draft_count[b], K) drafts (K without draft_count; < 0: idle row):
+ *
+ *   draft i = 0, 1, ... is accepted while  u[b,i] * q_i[x_i] < p_i[x_i],
+ *   p_i = target_probs[b,i,:], q_i = draft_probs[b,i,:], x_i = draft_tokens[b,i];
+ *   a = number of accepted drafts (the first refusal ends the row).
+ *   One more token is drawn with weights w over the vocabulary:
+ *     a < n_b:  w = max(p_a - q_a, 0); if all of these are 0, w = p_a
+ *     a == n_b: w = p_a
+ *   as the lowest index v with  sum_{j <= v} w_j > u[b,K] * sum_j w_j
+ *   (the last v with w_v > 0 if rounding leaves none).
+ *
+ * Products, differences and sums are taken in 64 bits, so the result does not
+ * depend on how the sums are split.  draft_probs NULL: the drafts are
+ * deterministic (q_i is 1 at x_i and 0 elsewhere).  A draft token outside
+ * [0, V) is refused, with q_a = 0 everywhere if draft_probs is NULL.  Weights
+ * that are NaN or not positive count as 0; a row whose weights are all 0 draws
+ * the token -1.  An idle row (draft_count[b] < 0) emits nothing: emit_count[b] = 0,
+ * its tokens -1.
+ *
+ *  target_probs  [B, K+1, V] dtype, row r = b*(K+1)+i at target_row_stride * r
+ *  draft_probs   [B, K, V] dtype or NULL, row r = b*K+i at draft_row_stride * r
+ *  draft_tokens  int32 [B, K]      uniforms  fp32 [B, K+1], in [0, 1)
+ *  draft_count   int32 [B] or NULL
+ *  tokens        int32 [B, K+1]: the accepted drafts, the drawn token, then -1
+ *  emit_count    int32 [B]: a + 1, the number of tokens emitted.  Where a row
+ *                is the last emitted token followed by the drafts, this is also
+ *                the number of its tokens whose state updates are to be kept,
+ *                i.e. the replay_count of gdn_replay_state_updates.
+ *  workspace     gdn_verify_workspace_bytes() bytes, 16-byte aligned, contents
+ *                on entry ignored.
+ * K >= 0 (K = 0 is plain sampling), V >= 1; the probabilities need only the
+ * alignment of their type.
+ */
+typedef struct {
+  int32_t B;                 /* rows */
+  int32_t K;                 /* drafted tokens per row (capacity) */
+  int32_t V;                 /* vocabulary */
+  int32_t dtype;             /* gdn_dtype of target_probs and draft_probs */
+  int64_t target_row_stride; /* elements between probability rows, >= V */
+  int64_t draft_row_stride;
+} gdn_verify_shape;
+
+size_t gdn_verify_workspace_bytes(const gdn_verify_shape* shape);   /* (size_t)-1 if invalid */
+
+gdn_status gdn_verify_drafts(const gdn_verify_shape* shape, const void* target_probs, const void* draft_probs,
+                             const int32_t* draft_tokens, const float* uniforms, const int32_t* draft_count,
+                             int32_t* tokens, int32_t* emit_count, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * The norms after and before a block, fused with its gate, residual and scale.
+ * For each token (row of D values made of D/group groups):
+ *
+ *   n = y * (mean_group(y^2) + eps)^(-1/2) * post_weight     (n = y without post_weight)
+ *   m = n * act(gate)                                        (m = n with GDN_ACT_NONE)
+ *   h = residual + residual_scale * m                        (no residual: 0)
+ *   normed = h * (mean_D(h^2) + eps)^(-1/2) * next_weight    (only with next_weight)
+ *
+ * everything in fp32, h and normed rounded once to `dtype` (normed is computed
+ * from the unrounded h).  With group = dv, D = Hv*dv and GDN_ACT_SILU this is the
+ * gated output norm of a GDN layer; with group = D it ends a block and
+ * prepares the next one's input.
+ *
+ *  y, gate, residual, h, normed  [T, D] dtype; gate required unless
+ *      GDN_ACT_NONE; residual, post_weight, next_weight may be NULL; normed is
+ *      required exactly with next_weight.
+ *  post_weight [group] dtype, next_weight [D] dtype.
+ *  h may be residual itself or y itself (in place); no other overlap.
+ * group is D, or one of 16, 32, 64, 128 dividing D; D <= 16384.  Rows need only
+ * the alignment of their type.
+ */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_act;
+
+typedef struct {
+  int64_t T;            /* tokens */
+  int32_t D;            /* width */
+  int32_t group;        /* group width of the norm after the block */
+  int32_t dtype;        /* gdn_dtype */
+  int32_t gate_act;     /* gdn_act */
+  float residual_scale;
+  float eps;            /* finite, >= 0 */
+} gdn_norm_shape;
+
+gdn_status gdn_block_norm(const gdn_norm_shape* shape, const void* y, const void* gate, const void* residual,
+                          const void* post_weight, const void* next_weight, void* h, void* normed,
+                          void* stream);
+
+/*
  * Measurement support (not part of the method).  gdn_profile_enable(1) makes
  * every entry point bracket each kernel it launches with a pair of hipEvents
  * recorded on the launch stream; gdn_profile_collect() waits for all pending
