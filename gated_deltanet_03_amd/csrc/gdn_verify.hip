@@ -61,36 +61,48 @@ struct Weights {
     qr = refused && p.q ? static_cast<const T*>(p.q) + ((size_t)b * p.K + a) * (size_t)p.q_stride : nullptr;
     drop = refused && !p.q ? p.x[(size_t)b * p.K + a] : -1;
   }
-  __device__ __forceinline__ void load(int base, int V, double* w) const {
+  struct Raw {
+    Vec16<T> p[VPT / Vec16<T>::N], q[VPT / Vec16<T>::N];
+  };
+  // Entries base .. base+VPT-1, all inside the row.
+  __device__ __forceinline__ void fetch(int base, Raw& r) const {
     constexpr int N = Vec16<T>::N;
 #pragma unroll
-    for (int j = 0; j < VPT; j += N) {
-      const Vec16<T> pv = load_vec(pr, base + j, V);
-      Vec16<T> qv{};
-      if (qr) qv = load_vec(qr, base + j, V);
+    for (int j = 0; j < VPT / N; ++j) __builtin_memcpy(r.p[j].e, pr + base + j * N, 16);
+    if (qr)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const double d = qr ? (double)pv.f(i) - (double)qv.f(i) : (double)pv.f(i);
-        w[j + i] = d > 0.0 && d < __builtin_inf() && base + j + i != drop ? d : 0.0;
-      }
+      for (int j = 0; j < VPT / N; ++j) __builtin_memcpy(r.q[j].e, qr + base + j * N, 16);
+  }
+  __device__ __forceinline__ void weigh(int base, const Raw& r, double* w) const {
+    constexpr int N = Vec16<T>::N;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const double x = (double)r.p[j / N].f(j % N);
+      const double d = qr ? x - (double)r.q[j / N].f(j % N) : x;
+      w[j] = d > 0.0 && d < __builtin_inf() && base + j != drop ? d : 0.0;
     }
   }
-};
-
-__device__ __forceinline__ double wave_scan(double x) {   // inclusive, over the wave's lanes
-  const int lane = threadIdx.x & 63;
+  // Weights base .. base+VPT-1 of a row that ends at `end`.
+  __device__ __forceinline__ void load(int base, int end, double* w) const {
+    constexpr int N = Vec16<T>::N;
+    Raw r;
+    if (base + VPT <= end) {
+      fetch(base, r);
+    } else {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double y = __shfl_up(x, d);
-    if (lane >= d) x += y;
+      for (int j = 0; j < VPT / N; ++j) {
+        r.p[j] = load_vec(pr, base + j * N, end);
+        if (qr) r.q[j] = load_vec(qr, base + j * N, end);
+      }
+    }
+    weigh(base, r, w);
   }
-  return x;
-}
+};
 
 // Inclusive scan over the workgroup's threads and the total.
 __device__ __forceinline__ double block_scan(double x, double* lds, double& total) {
   const int wave = threadIdx.x >> 6;
-  x = wave_scan(x);
+  x = wave_scan64(x);
   __syncthreads();
   if ((threadIdx.x & 63) == 63) lds[wave] = x;
   __syncthreads();
@@ -102,6 +114,48 @@ __device__ __forceinline__ double block_scan(double x, double* lds, double& tota
     total += lds[w];
   }
   return before + x;
+}
+
+// One candidate of a thread, in index order over the threads: an index (-1:
+// none) and the sum before it.
+struct Pick {
+  int at = -1;
+  double before = 0.0;
+};
+
+struct PickLds {
+  int hit[VT / 64], last[VT / 64];
+  double hit_before[VT / 64], last_before[VT / 64];
+};
+
+// The first `hit` of the workgroup, else its last `last` (found = false).
+__device__ __forceinline__ Pick block_pick(const Pick& hit, const Pick& last, PickLds& lds, bool& found) {
+  const int wave = threadIdx.x >> 6;
+  const uint64_t h = __ballot(hit.at >= 0), l = __ballot(last.at >= 0);
+  const int hs = h ? (int)__builtin_ctzll(h) : 0, ls = l ? 63 - (int)__builtin_clzll(l) : 0;
+  const int lane = threadIdx.x & 63;
+  __syncthreads();   // the last call's reads are done
+  if (lane == hs) {
+    lds.hit[wave] = hit.at;
+    lds.hit_before[wave] = hit.before;
+  }
+  if (lane == ls) {
+    lds.last[wave] = last.at;
+    lds.last_before[wave] = last.before;
+  }
+  __syncthreads();
+  Pick best;
+#pragma unroll
+  for (int w = 0; w < VT / 64; ++w)
+    if (lds.last[w] >= 0) best = {lds.last[w], lds.last_before[w]};
+  found = false;
+#pragma unroll
+  for (int w = VT / 64 - 1; w >= 0; --w)
+    if (lds.hit[w] >= 0) {
+      best = {lds.hit[w], lds.hit_before[w]};
+      found = true;
+    }
+  return best;
 }
 
 template <typename T>
@@ -117,28 +171,56 @@ __device__ __forceinline__ double tile_sum(const Weights<T>& wt, const VerifyArg
   return s;
 }
 
-template <typename T>
+// S neighbouring tiles per workgroup: 1 where there are few (one row spreads over
+// many workgroups), 4 for a batch, whose loads are then in flight together.
+template <typename T, int S>
 __global__ __launch_bounds__(VT) void verify_sum_kernel(VerifyArgs p) {
-  __shared__ double lds[VT / 64];
-  const int tile = blockIdx.x, b = blockIdx.y;
+  __shared__ double lds[S][VT / 64];
+  const int tile0 = (int)blockIdx.x * S, b = blockIdx.y, tid = threadIdx.x;
   const int n = drafts_of(p, b);
   if (n < 0) {
-    if (tile == 0 && threadIdx.x == 0) p.emit[b] = 0;
+    if (tile0 == 0 && tid == 0) p.emit[b] = 0;
     return;
   }
   const int a = accepted<T>(p, b, n);
-  if (tile == 0 && threadIdx.x == 0) p.emit[b] = a + 1;
+  if (tile0 == 0 && tid == 0) p.emit[b] = a + 1;
   const Weights<T> wt(p, b, a, a < n);
-  double total;
-  block_scan(tile_sum(wt, p, tile), lds, total);
-  if (threadIdx.x == 0) p.part[(size_t)b * p.tiles + tile] = total;
+  double s[S];
+  if (S > 1 && (int64_t)(tile0 + S) * VSUB <= p.V) {   // S > 1: tiles of VSUB entries
+    typename Weights<T>::Raw raw[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) wt.fetch((tile0 + i) * VSUB + tid * VPT, raw[i]);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      double w[VPT];
+      wt.weigh((tile0 + i) * VSUB + tid * VPT, raw[i], w);
+      s[i] = 0.0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) s[i] += w[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S; ++i) s[i] = tile0 + i < p.tiles ? tile_sum(wt, p, tile0 + i) : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    s[i] = wave_scan64(s[i]);
+    if ((tid & 63) == 63) lds[i][tid >> 6] = s[i];
+  }
+  __syncthreads();
+  if (tid < S && tile0 + tid < p.tiles) {
+    double total = 0.0;
+#pragma unroll
+    for (int w = 0; w < VT / 64; ++w) total += lds[tid][w];
+    p.part[(size_t)b * p.tiles + tile0 + tid] = total;
+  }
 }
 
 template <typename T>
 __global__ __launch_bounds__(VT) void verify_draw_kernel(VerifyArgs p) {
   __shared__ double lds[VT / 64];
   __shared__ double part[VMAXT];
-  __shared__ int first, last;
+  __shared__ PickLds picks;
   const int b = blockIdx.x, tid = threadIdx.x;
   const int a = p.emit[b] - 1;
   const size_t tok = (size_t)b * (p.K + 1);
@@ -177,66 +259,53 @@ __global__ __launch_bounds__(VT) void verify_draw_kernel(VerifyArgs p) {
   }
   const double u = (double)p.u[tok + p.K];
   const double r = (u > 0.0 ? u : 0.0) * total;
-  if (tid == 0) {
-    first = p.tiles;
-    last = -1;
-  }
-  __syncthreads();
-  double start = 0.0;
-  {
-    double c = upto;
+  bool found;
+  Pick hit, last;
+  double c = upto;
 #pragma unroll
-    for (int i = 0; i < TPT; ++i) {
-      const int t = tid * TPT + i;
-      if (t < p.tiles && part[t] > 0.0) {
-        if (c + part[t] > r) atomicMin(&first, t);
-        atomicMax(&last, t);
-        c += part[t];
-      }
+  for (int i = 0; i < TPT; ++i) {
+    const int t = tid * TPT + i;
+    if (t < p.tiles && part[t] > 0.0) {
+      last = {t, c};
+      if (hit.at < 0 && c + part[t] > r) hit = last;
+      c += part[t];
     }
   }
-  __syncthreads();
-  const int tile = first < p.tiles ? first : last;
-  __syncthreads();
-  if (tid == 0) {
-    first = p.V;
-    last = -1;
-  }
-  // sum of the tiles before it, in the order of the scan above
-  if (tid == tile / TPT) {
-    double c = upto;
-    for (int t = tid * TPT; t < tile; ++t) c += part[t];
-    lds[0] = c;
-  }
-  __syncthreads();
-  start = lds[0];
-  __syncthreads();
-  const int end = min(p.V, (tile + 1) * p.tile);
-  for (int e0 = tile * p.tile; e0 < end; e0 += VSUB) {
+  const Pick tile = block_pick(hit, last, picks, found);   // total > 0: there is one
+  double start = tile.before;
+  const int end = min(p.V, (tile.at + 1) * p.tile);
+  int token = -1;
+  for (int e0 = tile.at * p.tile; e0 < end; e0 += VSUB) {
     const int e = e0 + tid * VPT;
     double w[VPT], s = 0.0, sub;
     wt.load(e, end, w);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) s += w[i];
-    double c = start + (block_scan(s, lds, sub) - s);
+    c = start + (block_scan(s, lds, sub) - s);
+    hit = last = Pick{};
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (w[i] > 0.0) {
+        last.at = e + i;
         c += w[i];
-        if (c > r) atomicMin(&first, e + i);
-        atomicMax(&last, e + i);
+        if (hit.at < 0 && c > r) hit.at = e + i;
       }
     }
+    const Pick v = block_pick(hit, last, picks, found);
+    if (v.at >= 0) token = v.at;
+    if (found) break;
     start += sub;
   }
-  __syncthreads();
-  if (tid == 0) p.tokens[tok + a] = first < p.V ? first : last;
+  if (tid == 0) p.tokens[tok + a] = token;
 }
 
 template <typename T>
 static hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t s) {
   prof_begin(K_VERIFY_SUM, s);
-  hipLaunchKernelGGL((verify_sum_kernel<T>), dim3(a.tiles, a.B), dim3(VT), 0, s, a);
+  if (a.tile == VSUB && (int64_t)a.tiles * a.B > 2048)   // 8 workgroups for each CU
+    hipLaunchKernelGGL((verify_sum_kernel<T, 4>), dim3((a.tiles + 3) / 4, a.B), dim3(VT), 0, s, a);
+  else
+    hipLaunchKernelGGL((verify_sum_kernel<T, 1>), dim3(a.tiles, a.B), dim3(VT), 0, s, a);
   prof_end(K_VERIFY_SUM, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
