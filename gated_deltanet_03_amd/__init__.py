@@ -488,7 +488,7 @@ def _on_gpu(dev):
     """The library reads device memory only; a host pointer would fault the GPU."""
     if dev.type != "cuda":
         raise ValueError(f"tensors are on {dev}, expected a GPU")
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _linear_common(q, k, v, g, scale, initial_state, stride, cu_seqlens, o, final_state, output_final_state):
@@ -519,7 +519,7 @@ def _linear_common(q, k, v, g, scale, initial_state, stride, cu_seqlens, o, fina
     if cu_seqlens is not None and cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens must be 1-D [N+1]")
     if o is None:
-        o = torch.empty(v.shape, dtype=dtype, device=dev)
+        o = torch.empty_like(v)
     else:
         _need(o, "o", dtype, dev)
         if o.shape != v.shape:
