@@ -42,6 +42,14 @@ __device__ __forceinline__ void store_vec(T* __restrict__ row, int base, int len
   }
 }
 
+// 16 bytes inside a row that nothing reads again: not kept in the caches.
+template <typename T>
+__device__ __forceinline__ Vec16<T> load_vec_once(const T* __restrict__ p) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+  const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return __builtin_bit_cast(Vec16<T>, x);
+}
+
 // Sum over aligned groups of `lanes` lanes (a power of two up to 64,
 // wave-uniform), left in every lane of the group.
 __device__ __forceinline__ float group_sum(float x, int lanes) {
