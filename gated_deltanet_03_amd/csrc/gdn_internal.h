@@ -112,7 +112,7 @@ struct LinearArgs {
   // prefill only
   int32_t seg_tokens, max_segs;
   float* seg_state;      // [max_segs, Hv, dk, dv]: a segment's own state, then the state before it
-  double* seg_decay;     // [max_segs, Hv]: its summed log decay
+  float* seg_decay;      // [max_segs, Hv]: its decay
 };
 
 struct VerifyArgs {

@@ -6,27 +6,36 @@
 //   o_i   = scale [ e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j ]
 //   S_out = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
 //
-// A workgroup walks the chunks of one (segment, value head) with the fp32 state
-// in the registers of its waves: each wave owns all dk rows of its own 16*NT
-// columns, so the waves share only the staged q, k, v tiles.  Everything is
-// 16x16 MFMA tiles:
-//   * S is carried in accumulators; two of its tiles are directly the B operand
-//     of Q*S (their dk rows permuted inside each 32-row block so that Q's and
-//     K's operands are contiguous 16-byte reads);
-//   * P^T = K Q^T comes out as the A operand of P*V without a shuffle, at the
-//     price that each wave computes the (lower) scores itself;
+// A workgroup walks the chunks of one (segment, value head) with the fp32 state in
+// the registers of its waves: each wave owns all dk rows of its own 16*NT columns.  Everything is 16x16 MFMA tiles:
+//   * S is carried in accumulators; two of its tiles are directly an operand of
+//     S^T Q (their dk rows permuted inside each 32-row block so that Q's and K's
+//     operands are contiguous 16-byte reads);
+//   * the scores come out as P^T = K Q^T, in the form of an operand of V^T P^T;
+//     each wave computes some blocks and hands them to the others
+//     through LDS in fragment order;
+//   * o^T is accumulated, so a lane holds adjacent columns of one token and
+//     writes them with one access;
 //   * K^T and V operands (contraction over tokens) come from transpose reads of
 //     the row-major tiles.
+// Two barriers a chunk: before the first, all products that read the tiles
+// (scores, S^T Q, the state's update) while the next chunk's loads are in flight;
+// after it, V^T P^T on registers while the next tiles are stored.
+//
 // The state's update uses e^{G_C - G_j} v_j split into parts of the input type
 // (three for bf16, two scaled ones for fp16), so the carried state keeps fp32
 // accuracy; the state and the scores are rounded to 16 bits where they are
-// operands of o.
+// operands of o.  Where the final state comes from the carry kernel, the bf16
+// outputs' own walk takes two parts (2^-18 of a term, far below the operands'
+// 2^-9).
 //
-// Log decays are summed in 64 bits and kept as a coarse part (a multiple of
-// 1/64, whose differences are exact) and a fine part: in a long chunk of strong
-// decays |G| reaches thousands while neighbouring G_i - G_j are small.  A decay
-// below e^-128 is 0 in fp32, so g is clamped there and -infinity needs no
-// special case.
+// Log decays are summed in 64 bits.  A decay between two tokens of one 16-token
+// tile is the exponential of a difference of coarse parts (multiples of 1/64,
+// exact) and fine parts: in a long chunk of strong decays |G| reaches thousands
+// while neighbouring G_i - G_j are small.  Between tiles it is the product of two
+// factors that are both at most 1, from the tile's start to the query and from
+// the key to the tile's start.  A decay below e^-128 is 0 in fp32, so g is clamped
+// there and -infinity needs no special case.
 #pragma once
 
 #include "gdn_device.h"
@@ -44,12 +53,21 @@ __device__ __forceinline__ s16x4 lds_read_tr(const void* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
-template <typename T> constexpr int kChunk = sizeof(T) == 2 ? 64 : 32;
+__device__ __forceinline__ float max_all(float x) {   // over the wave, x >= 0
+  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0xb1, 0xf, 0xf, false));    // lane ^ 1
+  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x4e, 0xf, 0xf, false));    // lane ^ 2
+  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x141, 0xf, 0xf, false));   // the other four of 8
+  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x140, 0xf, 0xf, false));   // the other eight of 16
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 
-__device__ __forceinline__ float max_all(float x) {   // over the wave
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
+__device__ __forceinline__ double lane64(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // Exponent shift that brings |x| <= m into [2^13, 2^15) (0 for m = 0 or not finite).
@@ -60,8 +78,7 @@ __device__ __forceinline__ int shift_for(float m) {
 }
 
 // Sequence and token range of segment `seg` (false past the last one).
-__device__ __forceinline__ bool segment_range(const LinearArgs& p, int seg, int& s, int& t0, int& t1, bool& last) {
-  last = true;
+__device__ __forceinline__ bool segment_range(const LinearArgs& p, int seg, int& s, int& t0, int& t1) {
   if (p.seg_tokens == 0) {
     s = seg;
     seq_range(p.cu, p.T, p.total, s, t0, t1);
@@ -111,19 +128,67 @@ __device__ __forceinline__ int state_row(int t, int m) {
   else return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3);
 }
 
-template <typename T, int DK, int NT, int NW>
+// Column of row m of column tile n (counted over all of dv): with at least two
+// tiles, a lane's rows 4g..4g+3 of tiles 2b and 2b+1 are 8 adjacent columns.
+// The same map as the rows', so that it does not depend on how tiles are dealt
+// to waves: the passes may deal them differently.
+__device__ __forceinline__ int state_col(int dv, int n, int m) { return dv < 32 ? m : state_row<32>(n, m); }
+
+// A chunk's decays; the state pass keeps only the first.
+template <int C, bool STATE>
+struct Decays {
+  static constexpr int O = STATE ? 4 : C, RT = C / 16;
+  __align__(16) float w[C];              // e^{G_last - G_i}, times what follows in the state pass
+  __align__(16) float gamma[4];          // e^{G_last}
+  __align__(16) float hi[O];             // coarse and fine part of G_i
+  __align__(16) float lo[O];
+  __align__(16) float eg[O];             // e^{G_i}
+  __align__(16) float row[O];            // e^{G_i - G_s}, s the last token before i's tile
+  __align__(16) float col[STATE ? 1 : RT - 1][O];   // [t - 1][j] = e^{G_{16t-1} - G_j}, j < 16t
+};
+
+// One wave: the decays of a chunk from lane i's log decay (0 past the end);
+// returns their sum.  `rest`: log decay of what follows the chunk (state pass).
+template <int C, bool STATE>
+__device__ __forceinline__ double fill_decays(float g, double rest, Decays<C, STATE>& d) {
+  const int lane = threadIdx.x & 63;
+  const double x = wave_scan64(lane < C ? (double)(g < -128.f ? -128.f : g) : 0.0);
+  const double end = lane64(x, C - 1);
+  if (lane < C) d.w[lane] = expf((float)(rest + (end - x)));
+  if constexpr (!STATE) {
+    constexpr int RT = C / 16;
+    if (lane == 0) d.gamma[0] = expf((float)end);
+    double start = 0.0;
+#pragma unroll
+    for (int t = 1; t < RT; ++t) {
+      const double at = lane64(x, 16 * t - 1);
+      if (lane >= 16 * t) start = at;
+      if (lane < 16 * t) d.col[t - 1][lane] = __expf((float)(at - x));
+    }
+    if (lane < C) {
+      const float hi = rintf((float)x * 64.f) * 0.015625f;
+      d.hi[lane] = hi;
+      d.lo[lane] = (float)(x - (double)hi);
+      d.eg[lane] = expf((float)x);
+      d.row[lane] = __expf((float)(x - start));
+    }
+  }
+  return end;
+}
+
+// Fragments of P: row tile i holds i / 2 + 1 blocks of 32 keys.
+__device__ __forceinline__ constexpr int p_frag(int i, int b) { return (i + 1) * (i + 1) / 4 + b; }
+
+template <typename T, int C, int DK, int NT, int NW, bool STATE>
 struct Smem {
-  static constexpr int C = kChunk<T>, DV = 16 * NT * NW;
+  static constexpr int CW = 16 * NT * NW;
   static constexpr int PAD = 16 / (int)sizeof(T);
-  static constexpr int KS = DK + PAD, VS = DV + PAD;   // row strides
-  __align__(16) T q[C * KS];
+  static constexpr int KS = DK + PAD, VS = CW + PAD;   // row strides
   __align__(16) T k[C * KS];
   __align__(16) T v[C * VS];
-  __align__(16) float hi[C];     // coarse and fine part of G_i
-  __align__(16) float lo[C];
-  __align__(16) float w[C];      // e^{G_last - G_i}
-  __align__(16) float eg[C];     // e^{G_i}
-  float gamma;                   // e^{G_last}
+  __align__(16) T q[STATE ? PAD : C * KS];
+  __align__(16) T p[STATE ? PAD : p_frag(C / 16, 0) * 512];
+  Decays<C, STATE> d[2];
 };
 
 // A (or, transposed, B) operand of rows 16*tile.. over dk block kb.
@@ -177,10 +242,12 @@ __device__ __forceinline__ float frag_get(const Frag<T>& f, int i) {
   else return Elem<T>::to_f(f.v[i]);
 }
 
-// Parts of the decayed v of a fragment: one fp32, three bf16, two fp16.
-template <typename T> constexpr int kParts = sizeof(T) == 4 ? 1 : (__is_same(T, __bf16) ? 3 : 2);
+// Parts of the decayed v of a fragment: one fp32; bf16 three, or two where only
+// outputs follow; fp16 two.
+enum class Pass { kState, kOut, kWhole };   // segment states; outputs from given states; both (no segments)
+template <typename T, Pass P> constexpr int kParts = sizeof(T) == 4 ? 1 : (__is_same(T, __bf16) && P != Pass::kOut ? 3 : 2);
 
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
   if constexpr (sizeof(T) == 4) {
     part[0].lo = f32x4{x[0], x[1], x[2], x[3]};
@@ -190,7 +257,7 @@ __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
     for (int j = 0; j < 8; ++j) {
       float r = x[j];
 #pragma unroll
-      for (int n = 0; n < kParts<T>; ++n) {
+      for (int n = 0; n < N; ++n) {
         part[n].v[j] = Elem<T>::from_f(r);
         r -= Elem<T>::to_f(part[n].v[j]);
       }
@@ -198,19 +265,21 @@ __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
   }
 }
 
-// Walks the chunks of one (segment, head).  STATE: only the segment's own state
-// and decay (for the split); else the outputs, from the state before it.
-template <typename T, int DK, int NT, int NW, bool STATE>
-__global__ __launch_bounds__(64 * NW) void linear_chunk_kernel(LinearArgs p) {
-  using SM = Smem<T, DK, NT, NW>;
-  constexpr int C = SM::C, DV = SM::DV, KS = SM::KS, VS = SM::VS, THREADS = 64 * NW;
+template <typename T, int C, int DK, int NT, int NW, Pass PASS>
+__global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) {
+  constexpr bool STATE = PASS == Pass::kState;
+  using SM = Smem<T, C, DK, NT, NW, STATE>;
+  constexpr int CW = SM::CW, KS = SM::KS, VS = SM::VS, THREADS = 64 * NW;
   constexpr int RT = C / 16, NTB = C / 32;                    // token tiles and 32-token blocks
   constexpr int NST = DK / 16, NKB = DK >= 32 ? DK / 32 : 1;  // state row tiles, dk blocks
-  constexpr int PER = 16 / (int)sizeof(T), KP = DK / PER, VP = DV / PER;   // 16-byte pieces a row
+  constexpr int PER = 16 / (int)sizeof(T), KP = DK / PER, VP = CW / PER;   // 16-byte pieces a row
   constexpr int NKL = (C * KP + THREADS - 1) / THREADS, NVL = (C * VP + THREADS - 1) / THREADS;
+  constexpr int KR = THREADS / KP, VR = THREADS / VP;         // rows between a thread's pieces
+  static_assert(THREADS % KP == 0 && THREADS % VP == 0, "");
+  constexpr int NP = kParts<T, PASS>;
   __shared__ SM sm;
 
-  // XCD-aware order: the value heads that share one segment's keys get ids equal mod 8
+  // XCD-aware order: the workgroups that share one segment's keys get ids equal mod 8
   const int G = p.Hv / p.Hq;
   const int unit = (int)(blockIdx.x >> 3) / G * 8 + (int)(blockIdx.x & 7);
   if (unit >= p.max_segs * p.Hq) return;
@@ -218,92 +287,121 @@ __global__ __launch_bounds__(64 * NW) void linear_chunk_kernel(LinearArgs p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g4 = lane >> 4;
   int s, t0, t1;
-  bool last;
-  if (!segment_range(p, seg, s, t0, t1, last)) return;
+  if (!segment_range(p, seg, s, t0, t1)) return;
   s = __builtin_amdgcn_readfirstlane(s);
   t0 = __builtin_amdgcn_readfirstlane(t0);
   t1 = __builtin_amdgcn_readfirstlane(t1);
-  const size_t per = (size_t)DK * DV;
+  const size_t per = (size_t)DK * CW, krow = (size_t)p.Hq * DK, vrow = (size_t)p.Hv * CW;
   const T* qp = static_cast<const T*>(p.q) + (size_t)hk * DK;
   const T* kp = static_cast<const T*>(p.k) + (size_t)hk * DK;
-  const T* vp = static_cast<const T*>(p.v) + (size_t)h * DV;
-  T* op = static_cast<T*>(p.o) + (size_t)h * DV;
-  const int col0 = wave * 16 * NT;
+  const T* vp = static_cast<const T*>(p.v) + (size_t)h * CW;
+  const int tile0 = wave * NT;   // this wave's first column tile
 
   // state tile (t, n): lane holds rows 4g..4g+3 of the tile, column i16
   f32x4 S[NST][NT];
-  const float* sin = nullptr;
-  if constexpr (!STATE)
-    sin = p.seg_tokens != 0 ? p.seg_state + ((size_t)seg * p.Hv + h) * per
-          : p.s0 != nullptr ? p.s0 + (int64_t)s * p.s0_stride + (size_t)h * per : nullptr;
+  auto seg_at = [&](int t, int n) {   // segment states are kept in this order
+    return reinterpret_cast<f32x4*>(p.seg_state + ((size_t)seg * p.Hv + h) * per) +
+           (t * (NT * NW) + tile0 + n) * 64 + lane;
+  };
+  auto state_at = [&](int t, int n, int e) {
+    return (size_t)h * per + (size_t)state_row<DK>(t, 4 * g4 + e) * CW + state_col(CW, tile0 + n, i16);
+  };
 #pragma unroll
   for (int t = 0; t < NST; ++t)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) S[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (PASS == Pass::kOut) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        S[t][n][e] = sin != nullptr ? sin[(size_t)state_row<DK>(t, 4 * g4 + e) * DV + col0 + 16 * n + i16] : 0.f;
-  double gsum = 0.0;
+    for (int t = 0; t < NST; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) S[t][n] = *seg_at(t, n);
+  } else if constexpr (PASS == Pass::kWhole) {
+    if (p.s0 != nullptr) {
+      const float* s0 = p.s0 + (int64_t)s * p.s0_stride;
+#pragma unroll
+      for (int t = 0; t < NST; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[t][n][e] = s0[state_at(t, n, e)];
+    }
+  }
 
-  uint4 kreg[NKL], qreg[NKL], vreg[NVL];
-  float greg = 0.f;
-  auto fetch = [&](int c0) {
-    const int len = min(C, t1 - c0);
-#pragma unroll
-    for (int i = 0; i < NKL; ++i) {
-      const int x = tid + i * THREADS, r = x / KP, pc = x % KP;
-      const bool in = r < len;
-      const size_t off = (size_t)(c0 + (in ? r : 0)) * p.Hq * DK + pc * PER;
-      kreg[i] = in ? *reinterpret_cast<const uint4*>(kp + off) : uint4{0, 0, 0, 0};
-      if constexpr (!STATE) qreg[i] = in ? *reinterpret_cast<const uint4*>(qp + off) : uint4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int i = 0; i < NVL; ++i) {
-      const int x = tid + i * THREADS, r = x / VP, pc = x % VP;
-      const bool in = r < len;
-      const size_t off = (size_t)(c0 + (in ? r : 0)) * p.Hv * DV + pc * PER;
-      vreg[i] = in ? *reinterpret_cast<const uint4*>(vp + off) : uint4{0, 0, 0, 0};
-    }
-    if (tid < C) greg = tid < len ? p.g[(size_t)(c0 + tid) * (size_t)p.g_stride + h] : 0.f;
+  uint4 kreg[NKL], qreg[STATE ? 1 : NKL], vreg[NVL];
+  const uint32_t koff = (uint32_t)((tid / KP) * krow * sizeof(T)) + (tid % KP) * 16;
+  const uint32_t voff = (uint32_t)((tid / VP) * vrow * sizeof(T)) + (tid % VP) * 16;
+  auto piece = [](const T* base, uint32_t off) {
+    return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + off);
   };
-
-  if (t0 < t1) fetch(t0);
-  for (int c0 = t0; c0 < t1; c0 += C) {
-    const int len = min(C, t1 - c0);
-    lds_barrier();   // the last chunk's reads of the tiles are done
+  auto fetch = [&](int c0) {
+    const T *kc = kp + (size_t)c0 * krow, *qc = qp + (size_t)c0 * krow, *vc = vp + (size_t)c0 * vrow;
+    if (t1 - c0 >= C && C * KP % THREADS == 0 && C * VP % THREADS == 0) {
+#pragma unroll
+      for (int i = 0; i < NKL; ++i) kreg[i] = piece(kc + (size_t)i * KR * krow, koff);
+      if constexpr (!STATE)
+#pragma unroll
+        for (int i = 0; i < NKL; ++i) qreg[i] = piece(qc + (size_t)i * KR * krow, koff);
+#pragma unroll
+      for (int i = 0; i < NVL; ++i) vreg[i] = piece(vc + (size_t)i * VR * vrow, voff);
+    } else {   // rows past the end are 0
+      const int len = min(C, t1 - c0);
+#pragma unroll
+      for (int i = 0; i < NKL; ++i) {
+        const bool in = tid / KP + i * KR < len;
+        kreg[i] = in ? piece(kc + (size_t)i * KR * krow, koff) : uint4{0, 0, 0, 0};
+        if constexpr (!STATE) qreg[i] = in ? piece(qc + (size_t)i * KR * krow, koff) : uint4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < NVL; ++i)
+        vreg[i] = tid / VP + i * VR < len ? piece(vc + (size_t)i * VR * vrow, voff) : uint4{0, 0, 0, 0};
+    }
+  };
+  auto stage = [&] {
 #pragma unroll
     for (int i = 0; i < NKL; ++i) {
-      const int x = tid + i * THREADS, r = x / KP, pc = x % KP;
+      const int r = tid / KP + i * KR;
       if (C * KP % THREADS == 0 || r < C) {
-        *reinterpret_cast<uint4*>(&sm.k[r * KS + pc * PER]) = kreg[i];
-        if constexpr (!STATE) *reinterpret_cast<uint4*>(&sm.q[r * KS + pc * PER]) = qreg[i];
+        *reinterpret_cast<uint4*>(&sm.k[r * KS + tid % KP * PER]) = kreg[i];
+        if constexpr (!STATE) *reinterpret_cast<uint4*>(&sm.q[r * KS + tid % KP * PER]) = qreg[i];
       }
     }
 #pragma unroll
     for (int i = 0; i < NVL; ++i) {
-      const int x = tid + i * THREADS, r = x / VP, pc = x % VP;
-      if (C * VP % THREADS == 0 || r < C) *reinterpret_cast<uint4*>(&sm.v[r * VS + pc * PER]) = vreg[i];
+      const int r = tid / VP + i * VR;
+      if (C * VP % THREADS == 0 || r < C) *reinterpret_cast<uint4*>(&sm.v[r * VS + tid % VP * PER]) = vreg[i];
     }
-    if (wave == 0) {   // cumulative log decays
-      double x = lane < C ? (double)(greg < -128.f ? -128.f : greg) : 0.0;
-#pragma unroll
-      for (int d = 1; d < C; d *= 2) {
-        const double y = __shfl_up(x, d);
-        if (lane >= d) x += y;
-      }
-      const double end = __shfl(x, C - 1);
-      gsum += end;
-      if (lane < C) {
-        const float hi = rintf((float)x * 64.f) * 0.015625f;
-        sm.hi[lane] = hi;
-        sm.lo[lane] = (float)(x - (double)hi);
-        sm.w[lane] = expf((float)(end - x));
-        sm.eg[lane] = expf((float)x);
-      }
-      if (lane == 0) sm.gamma = expf((float)end);
+  };
+  // Wave 0 turns log decays into decays one chunk ahead.  The state pass goes from
+  // the last chunk to the first, so that its state takes no factor on the way
+  // and ends where the next pass begins to read.
+  double gsum = 0.0;
+  auto load_g = [&](int c0) {
+    return lane < C && c0 >= t0 && c0 + lane < t1 ? p.g[(size_t)(c0 + lane) * (size_t)p.g_stride + h] : 0.f;
+  };
+  const int nch = (t1 - t0 + C - 1) / C, step = STATE ? -C : C, begin = STATE ? t0 + (nch - 1) * C : t0;
+  float gnext = 0.f;
+  if (nch > 0) {
+    fetch(begin);
+    if (wave == 0) {
+      const float g0 = load_g(begin);
+      gnext = load_g(begin + step);
+      gsum += fill_decays<C, STATE>(g0, 0.0, sm.d[0]);
     }
-    lds_barrier();
-    if (c0 + C < t1) fetch(c0 + C);
+    stage();
+  }
+  lds_barrier();
+  for (int ch = 0, c0 = begin; ch < nch; ++ch, c0 += step) {
+    const int len = min(C, t1 - c0);
+    const bool more = ch + 1 < nch;
+    const auto& D = sm.d[ch & 1];
+    if (more) {
+      fetch(c0 + step);
+      if (wave == 0) {
+        const float g1 = gnext;
+        gnext = load_g(c0 + 2 * step);
+        gsum += fill_decays<C, STATE>(g1, STATE ? gsum : 0.0, sm.d[(ch + 1) & 1]);
+      }
+    }
 
     // V operands of this wave's columns
     Frag<T> vf[NTB][NT];
@@ -311,10 +409,48 @@ __global__ __launch_bounds__(64 * NW) void linear_chunk_kernel(LinearArgs p) {
     for (int b = 0; b < NTB; ++b)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        vf[b][n] = token_frag<T>(sm.v, VS, b, [&](int m) { return col0 + 16 * n + m; });
+        vf[b][n] = token_frag<T>(sm.v, VS, b, [&](int m) { return state_col(CW, tile0 + n, m); });
 
+    f32x4 acc[STATE ? 1 : RT][NT];
     if constexpr (!STATE) {
-      // state operands; fp16 ones scaled by a power of two into its range
+      // this wave's fragments of the decayed scores (wave 0 has the decays to do)
+      for (int it = NW - 1 - wave; it < p_frag(RT, 0); it += NW) {
+        const int i = it > 0 ? 1 + it / 2 : 0, b = it > 1 ? it & 1 : 0;   // it = p_frag(i, b)
+        Frag<T> qf[NKB];
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) qf[kb] = row_frag<T, DK>(sm.q, KS, i, kb);
+        const float row = D.row[16 * i + i16];
+        f32x4 pt[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = 2 * b + u;
+          pt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (j > i) continue;
+#pragma unroll
+          for (int kb = 0; kb < NKB; ++kb) {
+            const Frag<T> kf = row_frag<T, DK>(sm.k, KS, j, kb);
+            if constexpr (DK >= 32) mma<T>(pt[u], kf, qf[kb]);
+            else mma_lo<T>(pt[u], kf, qf[kb]);
+          }
+          // lane holds (key 16j + 4g + e, query 16i + i16)
+          if (j < i) {
+            const f32x4 col = *reinterpret_cast<const f32x4*>(&D.col[i - 1][16 * j + 4 * g4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pt[u][e] *= row * col[e];
+          } else {
+            const float ih = D.hi[16 * i + i16], il = D.lo[16 * i + i16];
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(&D.hi[16 * j + 4 * g4]);
+            const f32x4 jl = *reinterpret_cast<const f32x4*>(&D.lo[16 * j + 4 * g4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float d = (ih - jh[e]) + (il - jl[e]);
+              pt[u][e] = 4 * g4 + e <= i16 ? pt[u][e] * __expf(d) : 0.f;
+            }
+          }
+        }
+        store_frag_native<T>(&sm.p[it * 512 + lane * 8], make_frag<T>(pt[0], pt[1]));
+      }
+      // the state's part of o; fp16 operands scaled by a power of two into its range
       int sh = 0;
       if constexpr (__is_same(T, _Float16)) {
         float m = 0.f;
@@ -327,9 +463,13 @@ __global__ __launch_bounds__(64 * NW) void linear_chunk_kernel(LinearArgs p) {
         sh = shift_for(max_all(m));
       }
       const float up = ldexpf(1.f, sh), down = ldexpf(1.f, -sh);
-      Frag<T> sf[NKB][NT];
 #pragma unroll
-      for (int b = 0; b < NKB; ++b)
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NKB; ++b) {
+        Frag<T> sf[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           f32x4 lo = S[DK >= 32 ? 2 * b : 0][n], hi = DK >= 32 ? S[DK >= 32 ? 2 * b + 1 : 0][n] : f32x4{0.f, 0.f, 0.f, 0.f};
@@ -337,150 +477,148 @@ __global__ __launch_bounds__(64 * NW) void linear_chunk_kernel(LinearArgs p) {
             lo *= up;
             hi *= up;
           }
-          sf[b][n] = make_frag<T>(lo, hi);
+          sf[n] = make_frag<T>(lo, hi);
         }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const Frag<T> qf = row_frag<T, DK>(sm.q, KS, i, b);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (DK >= 32) mma<T>(acc[i][n], sf[n], qf);
+            else mma_lo<T>(acc[i][n], sf[n], qf);
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        Frag<T> qf[NKB];
+        const float eg = D.eg[16 * i + i16] * down;
 #pragma unroll
-        for (int b = 0; b < NKB; ++b) qf[b] = row_frag<T, DK>(sm.q, KS, i, b);
-        f32x4 acc[NT];
-        const f32x4 eg = *reinterpret_cast<const f32x4*>(&sm.eg[16 * i + 4 * g4]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int b = 0; b < NKB; ++b) {
-            if constexpr (DK >= 32) mma<T>(acc[n], qf[b], sf[b][n]);
-            else mma_lo<T>(acc[n], qf[b], sf[b][n]);
-          }
-          acc[n] *= eg * down;
-        }
-        const float ih = sm.hi[16 * i + i16], il = sm.lo[16 * i + i16];
-#pragma unroll
-        for (int b = 0; b <= i / 2; ++b) {
-          f32x4 pt[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int j = 2 * b + u;
-            pt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (j > i) continue;
-#pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-              const Frag<T> kf = row_frag<T, DK>(sm.k, KS, j, kb);
-              if constexpr (DK >= 32) mma<T>(pt[u], kf, qf[kb]);
-              else mma_lo<T>(pt[u], kf, qf[kb]);
-            }
-            // lane holds (key 16j + 4g + e, query 16i + i16)
-            const f32x4 jh = *reinterpret_cast<const f32x4*>(&sm.hi[16 * j + 4 * g4]);
-            const f32x4 jl = *reinterpret_cast<const f32x4*>(&sm.lo[16 * j + 4 * g4]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float d = (ih - jh[e]) + (il - jl[e]);
-              pt[u][e] = j < i || 4 * g4 + e <= i16 ? pt[u][e] * __expf(d) : 0.f;
-            }
-          }
-          const Frag<T> pf = make_frag<T>(pt[0], pt[1]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma<T>(acc[n], pf, vf[b][n]);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 16 * i + 4 * g4 + e;
-            if (r < len)
-              op[(size_t)(c0 + r) * p.Hv * DV + col0 + 16 * n + i16] = Elem<T>::from_f(p.scale * acc[n][e]);
-          }
+        for (int n = 0; n < NT; ++n) acc[i][n] *= eg;
       }
     }
 
     // S = gamma S + K^T (w v)
-    float x[NTB][NT][8];
-    float m = 0.f;
+    if (STATE || more || PASS == Pass::kWhole) {
+      float x[NTB][NT][8];
+      float m = 0.f;
 #pragma unroll
-    for (int b = 0; b < NTB; ++b) {
-      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&sm.w[32 * b + 4 * g4]);
-      const f32x4 w1 = *reinterpret_cast<const f32x4*>(&sm.w[32 * b + 16 + 4 * g4]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[b][n][j] = (j < 4 ? w0[j & 3] : w1[j & 3]) * frag_get<T>(vf[b][n], j);
-          m = fmaxf(m, fabsf(x[b][n][j]));
-        }
-    }
-    float up = 1.f, down = 1.f;
-    if constexpr (__is_same(T, _Float16)) {
-      const int sh = shift_for(max_all(m));
-      up = ldexpf(1.f, sh);
-      down = ldexpf(1.f, -sh);
-    }
-    const float gamma = sm.gamma * up;
-#pragma unroll
-    for (int t = 0; t < NST; ++t)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) S[t][n] *= gamma;
-#pragma unroll
-    for (int b = 0; b < NTB; ++b) {
-      Frag<T> part[NT][kParts<T>];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if constexpr (__is_same(T, _Float16)) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[b][n][j] *= up;
-        }
-        split<T>(x[b][n], part[n]);
-      }
-#pragma unroll
-      for (int t = 0; t < NST; ++t) {
-        const Frag<T> kt = token_frag<T>(sm.k, KS, b, [&](int r) { return state_row<DK>(t, r); });
+      for (int b = 0; b < NTB; ++b) {
+        const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[32 * b + 4 * g4]);
+        const f32x4 w1 = *reinterpret_cast<const f32x4*>(&D.w[32 * b + 16 + 4 * g4]);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int q = 0; q < kParts<T>; ++q) mma<T>(S[t][n], kt, part[n][q]);
+          for (int j = 0; j < 8; ++j) {
+            x[b][n][j] = (j < 4 ? w0[j & 3] : w1[j & 3]) * frag_get<T>(vf[b][n], j);
+            m = fmaxf(m, fabsf(x[b][n][j]));
+          }
+      }
+      float up = 1.f, down = 1.f;
+      if constexpr (__is_same(T, _Float16)) {
+        const int sh = shift_for(max_all(m));
+        up = ldexpf(1.f, sh);
+        down = ldexpf(1.f, -sh);
+      }
+      const float gamma = STATE ? up : D.gamma[0] * up;
+      if (!STATE || __is_same(T, _Float16)) {
+#pragma unroll
+        for (int t = 0; t < NST; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) S[t][n] *= gamma;
+      }
+#pragma unroll
+      for (int b = 0; b < NTB; ++b) {
+        Frag<T> part[NT][NP];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[b][n][j] *= up;
+          }
+          split<T, NP>(x[b][n], part[n]);
+        }
+#pragma unroll
+        for (int t = 0; t < NST; ++t) {
+          const Frag<T> kt = token_frag<T>(sm.k, KS, b, [&](int r) { return state_row<DK>(t, r); });
+#pragma unroll
+          for (int q = 0; q < NP; ++q)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma<T>(S[t][n], kt, part[n][q]);
+        }
+      }
+      if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+        for (int t = 0; t < NST; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) S[t][n] *= down;
       }
     }
-    if constexpr (__is_same(T, _Float16)) {
+    lds_barrier();   // the tiles are read, P is written
+
+    if constexpr (!STATE) {
+      T* orow = static_cast<T*>(p.o) + ((size_t)c0 + i16) * vrow + (size_t)h * CW;
 #pragma unroll
-      for (int t = 0; t < NST; ++t)
+      for (int i = 0; i < RT; ++i) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) S[t][n] *= down;
+        for (int b = 0; b <= i / 2; ++b) {
+          const Frag<T> pf = load_frag_native<T>(&sm.p[p_frag(i, b) * 512 + lane * 8]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma<T>(acc[i][n], vf[b][n], pf);
+        }
+        // lane holds token 16i + i16, columns state_col(4g..4g+3) of each tile
+        if (16 * i + i16 < len) {
+          T* at = orow + (size_t)(16 * i) * vrow;
+          if constexpr (NT == 2 && sizeof(T) == 2) {
+            const Frag<T> f = make_frag<T>(p.scale * acc[i][0], p.scale * acc[i][1]);
+            store_frag_native<T>(at + state_col(CW, tile0, 4 * g4), f);
+          } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const f32x4 x = p.scale * acc[i][n];
+              store4<T>(at + state_col(CW, tile0 + n, 4 * g4), x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+      }
     }
+    if (more) stage();
+    lds_barrier();
   }
 
-  float* sout = nullptr;
   if constexpr (STATE) {
-    sout = p.seg_state + ((size_t)seg * p.Hv + h) * per;
-    if (tid == 0) p.seg_decay[(size_t)seg * p.Hv + h] = gsum;
-  } else if (p.seg_tokens == 0 && p.s_out != nullptr) {
-    sout = p.s_out + ((size_t)s * p.Hv + h) * per;
-  }
-  if (sout != nullptr) {
+    if (tid == 0) p.seg_decay[(size_t)seg * p.Hv + h] = expf((float)gsum);
 #pragma unroll
     for (int t = 0; t < NST; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) *seg_at(t, n) = S[t][n];
+  } else if constexpr (PASS == Pass::kWhole) {
+    if (p.s_out != nullptr) {
+      float* so = p.s_out + (size_t)s * p.Hv * per;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sout[(size_t)state_row<DK>(t, 4 * g4 + e) * DV + col0 + 16 * n + i16] = S[t][n][e];
+      for (int t = 0; t < NST; ++t)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) so[state_at(t, n, e)] = S[t][n][e];
+    }
   }
 }
 
 // Replaces each segment's own state by the state before it, and writes the
-// final states: element-wise recurrences over the segments of a sequence.
-template <typename T>
-__global__ __launch_bounds__(256) void linear_carry_kernel(LinearArgs p) {
-  const size_t per = (size_t)p.dk * p.dv;
-  const int nblk = (int)((per / 4 + 255) / 256);
-  const int blk = (int)(blockIdx.x % nblk), pair = (int)(blockIdx.x / nblk);
+// final states: element-wise recurrences over the segments of a sequence, in the
+// segment states' order (a thread holds four rows of one column).
+template <int DK, int DV>
+__global__ __launch_bounds__(64) void linear_carry_kernel(LinearArgs p) {
+  constexpr int NB = DK * DV / 256, AHEAD = 8;   // tiles a state, segments in flight
+  constexpr size_t per = (size_t)DK * DV;
+  const int tile = (int)(blockIdx.x % NB), pair = (int)(blockIdx.x / NB);
   const int s = pair / p.Hv, h = pair % p.Hv, L = p.seg_tokens;
+  const int lane = threadIdx.x;
   int first = 0, n = 0;
   if (p.cu == nullptr) {
     n = (p.T + L - 1) / L;
     first = s * n;
   } else {
-    const int lane = threadIdx.x & 63;
     for (int i0 = 0; i0 <= s; i0 += 64) {
       int a = 0, b = 0;
       if (i0 + lane <= s) clamp_range(p.cu[i0 + lane], p.cu[i0 + lane + 1], p.total, a, b);
@@ -491,54 +629,73 @@ __global__ __launch_bounds__(256) void linear_carry_kernel(LinearArgs p) {
       first += c;
       n = mine;
     }
-    first -= n;
+    first = __builtin_amdgcn_readfirstlane(first - n);
+    n = __builtin_amdgcn_readfirstlane(n);
   }
   n = min(n, p.max_segs - first);
-  const size_t e = ((size_t)blk * 256 + threadIdx.x) * 4;
-  if (e >= per) return;
+  const int row = state_row<DK>(tile / (DV / 16), 4 * (lane >> 4)), col = state_col(DV, tile % (DV / 16), lane & 15);
+  const size_t at = (size_t)h * per + (size_t)row * DV + col;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (p.s0 != nullptr) S = *reinterpret_cast<const f32x4*>(p.s0 + (int64_t)s * p.s0_stride + (size_t)h * per + e);
-  for (int j = 0; j < n; ++j) {
-    const size_t at = (size_t)(first + j) * p.Hv + h;
-    f32x4* x = reinterpret_cast<f32x4*>(p.seg_state + at * per + e);
-    const f32x4 own = *x;
-    *x = S;
-    const float a = expf((float)p.seg_decay[at]);
+  if (p.s0 != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[i] = fmaf(a, S[i], own[i]);
+    for (int e = 0; e < 4; ++e) S[e] = p.s0[(int64_t)s * p.s0_stride + at + (size_t)e * DV];
   }
-  if (p.s_out != nullptr) *reinterpret_cast<f32x4*>(p.s_out + ((size_t)s * p.Hv + h) * per + e) = S;
+  f32x4* x = reinterpret_cast<f32x4*>(p.seg_state + ((size_t)first * p.Hv + h) * per) + tile * 64 + lane;
+  const float* a = p.seg_decay + (size_t)first * p.Hv + h;
+  const size_t step = (size_t)p.Hv * per / 4;
+  for (int j0 = 0; j0 < n; j0 += AHEAD) {
+    f32x4 own[AHEAD];
+    const int m = min(AHEAD, n - j0);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (j < m) own[j] = x[(size_t)(j0 + j) * step];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (j < m) {
+        x[(size_t)(j0 + j) * step] = S;
+        const float f = a[(size_t)(j0 + j) * p.Hv];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[i] = fmaf(f, S[i], own[j][i]);
+      }
+  }
+  if (p.s_out != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p.s_out[(size_t)s * p.Hv * per + at + (size_t)e * DV] = S[e];
+  }
 }
 
-template <typename T, int DK, int NT, int NW>
-static hipError_t launch_w(const LinearArgs& a, hipStream_t s) {
+template <typename T, int C, int DK, int NT, int NW, Pass P>
+static hipError_t run_pass(KernelId id, const LinearArgs& a, hipStream_t s) {
   const long long units = (long long)a.max_segs * a.Hq;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * (a.Hv / a.Hq))), block(64 * NW);
-  hipError_t e;
-  if (a.seg_tokens != 0) {
-    prof_begin(K_LIN_STATE, s);
-    hipLaunchKernelGGL((linear_chunk_kernel<T, DK, NT, NW, true>), grid, block, 0, s, a);
-    prof_end(K_LIN_STATE, s);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    prof_begin(K_LIN_CARRY, s);
-    const long long nblk = ((long long)a.dk * a.dv / 4 + 255) / 256;
-    hipLaunchKernelGGL((linear_carry_kernel<T>), dim3((unsigned)(nblk * a.B * a.Hv)), dim3(256), 0, s, a);
-    prof_end(K_LIN_CARRY, s);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  prof_begin(K_LIN_OUT, s);
-  hipLaunchKernelGGL((linear_chunk_kernel<T, DK, NT, NW, false>), grid, block, 0, s, a);
-  prof_end(K_LIN_OUT, s);
+  const dim3 grid((unsigned)((units + 7) / 8 * 8 * (a.Hv / a.Hq)));
+  prof_begin(id, s);
+  hipLaunchKernelGGL((linear_chunk_kernel<T, C, DK, NT, NW, P>), grid, dim3(64 * NW), 0, s, a);
+  prof_end(id, s);
   return hipGetLastError();
+}
+
+template <typename T, int DK, int DV>
+static hipError_t launch_d(const LinearArgs& a, hipStream_t s) {
+  // one column tile a wave; the output pass of 16-bit inputs two, in shorter chunks
+  constexpr int TILES = DV / 16, C = sizeof(T) == 2 ? 64 : 32;
+  constexpr int NT = sizeof(T) == 2 && TILES > 1 ? 2 : 1;
+  if (a.seg_tokens == 0) return run_pass<T, C, DK, 1, TILES, Pass::kWhole>(K_LIN_OUT, a, s);
+  hipError_t e = run_pass<T, C, DK, 1, TILES, Pass::kState>(K_LIN_STATE, a, s);
+  if (e != hipSuccess) return e;
+  prof_begin(K_LIN_CARRY, s);
+  hipLaunchKernelGGL((linear_carry_kernel<DK, DV>), dim3((unsigned)(DK * DV / 256 * a.B * a.Hv)), dim3(64), 0, s, a);
+  prof_end(K_LIN_CARRY, s);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return run_pass<T, 32, DK, NT, TILES / NT, Pass::kOut>(K_LIN_OUT, a, s);
 }
 
 template <typename T, int DK>
 static hipError_t launch_dk(const LinearArgs& a, hipStream_t s) {
   switch (a.dv) {
-    case 16: return launch_w<T, DK, 1, 1>(a, s);
-    case 32: return launch_w<T, DK, 1, 2>(a, s);
-    case 64: return launch_w<T, DK, 1, 4>(a, s);
-    case 128: return launch_w<T, DK, 2, 4>(a, s);
+    case 16: return launch_d<T, DK, 16>(a, s);
+    case 32: return launch_d<T, DK, 32>(a, s);
+    case 64: return launch_d<T, DK, 64>(a, s);
+    case 128: return launch_d<T, DK, 128>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -35,10 +35,11 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 //
 // A segment's workgroup walks its chunks one after another, so (sequence, head)
 // pairs alone fill the 256 CUs only from a few hundred on.  Below that the
-// tokens are cut so that about kTargetWg (segment, head) workgroups exist, but
-// not into fewer than kMinSeg tokens: a segment costs four passes over its
-// [dk x dv] fp32 state beside its tokens, and the split two more launches.
-constexpr int64_t kTargetWg = 768, kFullWg = 512, kMinSeg = 128;
+// tokens are cut so that about kTargetWg (segment, head) workgroups exist (two
+// for each CU run together), but not into fewer than kMinSeg tokens: a segment
+// costs four passes over its [dk x dv] fp32 state beside its tokens, and the
+// split two more launches.
+constexpr int64_t kTargetWg = 480, kFullWg = 512, kMinSeg = 128;
 
 int32_t segment_tokens(const gdn_shape* sh, int64_t total, bool ragged) {
   const int64_t pairs = (int64_t)sh->B * sh->Hv;
@@ -56,7 +57,7 @@ int64_t max_segments(const gdn_shape* sh, int64_t total, bool ragged, int32_t se
   return total / seg + sh->B;   // every sequence adds at most one partial segment
 }
 
-size_t decay_bytes(int64_t segs, int32_t Hv) { return align_up((size_t)segs * Hv * sizeof(double), 256); }
+size_t decay_bytes(int64_t segs, int32_t Hv) { return align_up((size_t)segs * Hv * sizeof(float), 256); }
 
 size_t linear_workspace(const gdn_shape* sh, int64_t total, bool ragged) {
   const int32_t seg = segment_tokens(sh, total, ragged);
@@ -144,7 +145,7 @@ gdn_status gdn_linear_prefill(const gdn_shape* sh, const void* q, const void* k,
     all[6] = {o, (size_t)total * sh->Hv * sh->dv * es, "o"};
     all[7] = {s_out, (size_t)sh->B * per, "final_state"};
     if ((st = check_apart({ws, need, "workspace"}, all, 8)) != GDN_OK) return st;
-    a.seg_decay = static_cast<double*>(ws);
+    a.seg_decay = static_cast<float*>(ws);
     a.seg_state = reinterpret_cast<float*>(static_cast<char*>(ws) + decay_bytes(segs, sh->Hv));
   }
   if (sh->B == 0 || (total == 0 && s_out == nullptr)) return GDN_OK;
