@@ -491,49 +491,85 @@ def _on_gpu(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+_kept = {}
+
+
+def _descriptor(cls, key):
+    """The C struct of these values and a reference to it.  A serving loop makes the
+    same few descriptors over and over; they are kept by value."""
+    hit = _kept.get((cls, key))
+    if hit is None:
+        if len(_kept) >= 1024:
+            _kept.clear()
+        sh = cls(*key)
+        hit = _kept[cls, key] = (sh, ctypes.byref(sh))
+    return hit
+
+
+def _scratch(need, dev):
+    return torch.empty(need, dtype=torch.uint8, device=dev) if 0 < need < 1 << 62 else None
+
+
 def _linear_common(q, k, v, g, scale, initial_state, stride, cu_seqlens, o, final_state, output_final_state):
     """Checks shared by gdn_linear_prefill and gdn_linear_step."""
-    dev, dtype = q.device, q.dtype
-    sh = _shape_from(q, k, v, scale, cu_seqlens)
+    dev, dtype, qs, vs = q.device, q.dtype, q.shape, v.shape
+    if cu_seqlens is None:
+        if len(qs) != 4:
+            raise ValueError("dense q must be [B, T, Hq, dk]")
+        B, T, Hq, dk = qs
+    else:
+        if len(qs) == 4 and qs[0] != 1:
+            raise ValueError("ragged q must be [1, T, Hq, dk] or [T, Hq, dk]")
+        T, Hq, dk = qs[-3:]
+        B = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if B < 0:
+            raise ValueError("cu_seqlens must be 1-D [N+1]")
+    Hv, dv = vs[-2:]
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
     _need(q, "q")
     _need(k, "k", dtype, dev)
     _need(v, "v", dtype, dev)
     _need(g, "g", torch.float32, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    _need(initial_state, "initial_state", torch.float32, dev)
-    if sh.Hq <= 0 or sh.Hv % sh.Hq != 0:
-        raise ValueError(f"Hv={sh.Hv} must be a multiple of Hq={sh.Hq}")
-    ntok = sh.T if cu_seqlens is not None else sh.B * sh.T
-    if k.shape != q.shape:
-        raise ValueError(f"k has shape {tuple(k.shape)}, q has {tuple(q.shape)}")
-    if v.dim() != q.dim() or v.shape[:-2] != q.shape[:-2]:
-        raise ValueError(f"v has shape {tuple(v.shape)}; its leading dims must match q's {tuple(q.shape[:-2])}")
-    if g.dim() == 1:
-        g_stride = 0
-        if g.shape[0] != sh.Hv:
-            raise ValueError(f"g has shape {tuple(g.shape)}, expected {(sh.Hv,)} or {tuple(v.shape[:-1])}")
-    else:
-        g_stride = sh.Hv
-        if g.shape != v.shape[:-1]:
-            raise ValueError(f"g has shape {tuple(g.shape)}, expected {(sh.Hv,)} or {tuple(v.shape[:-1])}")
-    if cu_seqlens is not None and cu_seqlens.dim() != 1:
-        raise ValueError("cu_seqlens must be 1-D [N+1]")
+    if Hq <= 0 or Hv % Hq != 0:
+        raise ValueError(f"Hv={Hv} must be a multiple of Hq={Hq}")
+    if k.shape != qs:
+        raise ValueError(f"k has shape {tuple(k.shape)}, q has {tuple(qs)}")
+    if len(vs) != len(qs) or vs[:-2] != qs[:-2]:
+        raise ValueError(f"v has shape {tuple(vs)}; its leading dims must match q's {tuple(qs[:-2])}")
+    g_stride = 0 if g.dim() == 1 else Hv
+    if g.shape != ((Hv,) if g_stride == 0 else vs[:-1]):
+        raise ValueError(f"g has shape {tuple(g.shape)}, expected {(Hv,)} or {tuple(vs[:-1])}")
     if o is None:
         o = torch.empty_like(v)
     else:
         _need(o, "o", dtype, dev)
-        if o.shape != v.shape:
-            raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(v.shape)}")
-    if final_state is None:
-        if output_final_state:
-            final_state = torch.empty((sh.B, sh.Hv, sh.dk, sh.dv), dtype=torch.float32, device=dev)
+        if o.shape != vs:
+            raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(vs)}")
+    per, states = Hv * dk * dv, (B, Hv, dk, dv)
+    same = False
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, dev)
+        same = initial_state.shape == states
+        if stride is None:
+            stride = 0 if B > 1 and initial_state.shape[0] == 1 else per
+        stride = int(stride)
+        if stride < 0:
+            raise ValueError(f"initial_state_batch_stride={stride} < 0")
+        if B > 0 and not (same and stride <= per):
+            _expect(initial_state, "initial_state", (B - 1) * stride + per, at_least=True)
     else:
+        stride = per
+    if final_state is not None:
         _need(final_state, "final_state", torch.float32, dev)
-    per = sh.Hv * sh.dk * sh.dv
-    if stride is None:
-        stride = 0 if (initial_state is not None and initial_state.shape[0] == 1 and sh.B > 1) else per
-    _check_states(sh, initial_state, int(stride), final_state)
-    return sh, ntok, g_stride, int(stride), o, final_state
+        if final_state.shape != states:
+            raise ValueError(f"final_state has shape {tuple(final_state.shape)}, expected {states}")
+    elif output_final_state:
+        final_state = torch.empty_like(initial_state) if same else torch.empty(states, dtype=torch.float32, device=dev)
+    sh, ref = _descriptor(gdn_shape, (B, T, Hq, Hv, dk, dv, dk ** -0.5 if scale is None else float(scale), code))
+    return sh, ref, g_stride, stride, o, final_state
 
 
 def gdn_linear_workspace_bytes(shape: gdn_shape, ragged: bool) -> int:
@@ -553,15 +589,12 @@ def gdn_linear_prefill(q, k, v, g, *, scale=None, initial_state=None, initial_st
     plus cu_seqlens int32 [N+1].  g fp32: log decays [..., Hv] per token, or [Hv]
     the same at every token.  Returns (o, final_state or None)."""
     lib = load_library()
-    sh, _, g_stride, stride, o, final_state = _linear_common(
+    sh, ref, g_stride, stride, o, final_state = _linear_common(
         q, k, v, g, scale, initial_state, initial_state_batch_stride, cu_seqlens, o, final_state, output_final_state)
     dev = q.device
     stream = _on_gpu(dev)
-    ref = ctypes.byref(sh)
-    if workspace is None:
-        need = lib.gdn_linear_workspace_bytes(ref, cu_seqlens is not None)
-        if 0 < need < 1 << 62:   # an invalid shape is named by the call itself
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:   # an invalid shape is named by the call itself
+        workspace = _scratch(lib.gdn_linear_workspace_bytes(ref, cu_seqlens is not None), dev)
     else:
         _need(workspace, "workspace", None, dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -581,7 +614,7 @@ def gdn_linear_step(q, k, v, g, *, scale=None, initial_state=None, initial_state
     gdn_replay_state_updates applies.  Returns (o, final_state or None,
     state_update or None)."""
     lib = load_library()
-    sh, _, g_stride, stride, o, final_state = _linear_common(
+    sh, ref, g_stride, stride, o, final_state = _linear_common(
         q, k, v, g, scale, initial_state, initial_state_batch_stride, cu_seqlens, o, final_state, output_final_state)
     dev = q.device
     cap = int(state_update_capacity)
@@ -596,7 +629,7 @@ def gdn_linear_step(q, k, v, g, *, scale=None, initial_state=None, initial_state
         _expect(capture_count, "capture_count", sh.B, at_least=True)
         _expect(state_update, "state_update", sh.B * cap * R, at_least=True)
     stream = _on_gpu(dev)
-    st = lib.gdn_linear_step(ctypes.byref(sh), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
+    st = lib.gdn_linear_step(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), g_stride,
                              _addr(initial_state), stride, _addr(cu_seqlens), o.data_ptr(), _addr(final_state), cap,
                              _addr(capture_count), _addr(state_update), stream)
     if st:
@@ -606,13 +639,13 @@ def gdn_linear_step(q, k, v, g, *, scale=None, initial_state=None, initial_state
 
 def _rows3(t, name, B, n, V, dtype, dev):
     """Elements between the rows of a [B, n, V] tensor whose rows are evenly spaced."""
-    if tuple(t.shape) != (B, n, V):
+    if t.shape != (B, n, V):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, n, V)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.numel() == 0:
+    if t.is_contiguous():
         return V
     s0, s1, s2 = t.stride()
     if V > 1 and s2 != 1:
@@ -658,13 +691,10 @@ def gdn_verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, *, draf
     else:
         _need(emit_count, "emit_count", torch.int32, dev)
         _expect(emit_count, "emit_count", B)
-    sh = gdn_verify_shape(B, K, V, _DTYPES[dtype], ps, qs)
+    _, ref = _descriptor(gdn_verify_shape, (B, K, V, _DTYPES[dtype], ps, qs))
     stream = _on_gpu(dev)
-    ref = ctypes.byref(sh)
     if workspace is None:
-        need = lib.gdn_verify_workspace_bytes(ref)
-        if 0 < need < 1 << 62:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _scratch(lib.gdn_verify_workspace_bytes(ref), dev)
     else:
         _need(workspace, "workspace", None, dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -719,10 +749,10 @@ def gdn_block_norm(y, *, gate=None, gate_act="silu", residual=None, residual_sca
         raise ValueError("normed is given without next_weight")
     if out is None:
         out = torch.empty_like(y)
-    sh = gdn_norm_shape(y.numel() // D, D, group, _DTYPES[dtype], 0 if gate is None else _ACTS[gate_act],
-                        residual_scale, eps)
+    _, ref = _descriptor(gdn_norm_shape, (y.numel() // D, D, group, _DTYPES[dtype],
+                                          0 if gate is None else _ACTS[gate_act], residual_scale, eps))
     stream = _on_gpu(dev)
-    st = lib.gdn_block_norm(ctypes.byref(sh), y.data_ptr(), _addr(gate), _addr(residual), _addr(post_weight),
+    st = lib.gdn_block_norm(ref, y.data_ptr(), _addr(gate), _addr(residual), _addr(post_weight),
                             _addr(next_weight), out.data_ptr(), _addr(normed), stream)
     if st:
         _check(st)
