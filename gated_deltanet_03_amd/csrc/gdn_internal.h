@@ -111,7 +111,7 @@ struct LinearArgs {
   float* su;             // [B, cap, R]
   // prefill only
   int32_t seg_tokens, max_segs;
-  float* seg_state;      // [max_segs, Hv, dk, dv]: a segment's own state, then the state before it
+  float* seg_state;      // [max_segs, Hv, dk, dv]: a segment's own state (the first's with the initial one)
   float* seg_decay;      // [max_segs, Hv]: its decay
 };
 
@@ -145,7 +145,7 @@ struct NormArgs {
 // Opt-in per-kernel event timing (gdn_profile_enable / gdn_profile_collect).
 enum KernelId : int {
   K_PLAN = 0, K_PREP, K_STATE, K_RECURRENT, K_REPLAY, K_COPY,
-  K_LIN_STATE, K_LIN_CARRY, K_LIN_OUT, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_NORM, kNumKernels
+  K_LIN_STATE, K_LIN_OUT, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_NORM, kNumKernels
 };
 void prof_begin(KernelId id, hipStream_t s);
 void prof_end(KernelId id, hipStream_t s);

@@ -6,28 +6,34 @@
 //   o_i   = scale [ e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j ]
 //   S_out = e^{G_C} S + sum_j e^{G_C - G_j} k_j v_j^T
 //
-// A workgroup walks the chunks of one (segment, value head) with the fp32 state in
-// the registers of its waves: each wave owns all dk rows of its own 16*NT columns.  Everything is 16x16 MFMA tiles:
+// Long sequences are cut into segments (few sequences and heads would leave most
+// CUs idle).  Pass kState gives each segment's own state, the first's with the
+// initial one; pass kOut sums those before its segment, walks it for the outputs,
+// and writes the final state after the last.  Without segments one pass, kWhole,
+// does both.
+//
+// A workgroup walks the chunks of one (segment, value head, column slice) with
+// the fp32 state in the registers of its waves: each wave owns all dk rows of its
+// own 16*NT columns.  Everything is 16x16 MFMA tiles:
 //   * S is carried in accumulators; two of its tiles are directly an operand of
 //     S^T Q (their dk rows permuted inside each 32-row block so that Q's and K's
 //     operands are contiguous 16-byte reads);
 //   * the scores come out as P^T = K Q^T, in the form of an operand of V^T P^T;
-//     each wave computes some blocks and hands them to the others
-//     through LDS in fragment order;
+//     each wave computes some tiles and hands them to the others through LDS in
+//     fragment order;
 //   * o^T is accumulated, so a lane holds adjacent columns of one token and
 //     writes them with one access;
 //   * K^T and V operands (contraction over tokens) come from transpose reads of
 //     the row-major tiles.
 // Two barriers a chunk: before the first, all products that read the tiles
-// (scores, S^T Q, the state's update) while the next chunk's loads are in flight;
-// after it, V^T P^T on registers while the next tiles are stored.
+// (scores, S^T Q, the state's update) while later chunks' loads are in flight;
+// after it, V^T P^T on registers once the next tiles are stored.
 //
 // The state's update uses e^{G_C - G_j} v_j split into parts of the input type
 // (three for bf16, two scaled ones for fp16), so the carried state keeps fp32
 // accuracy; the state and the scores are rounded to 16 bits where they are
-// operands of o.  Where the final state comes from the carry kernel, the bf16
-// outputs' own walk takes two parts (2^-18 of a term, far below the operands'
-// 2^-9).
+// operands of o.  kOut's own walk, which ends in no final state, takes two bf16
+// parts (2^-17 of a term, far below the operands' 2^-8).
 //
 // Log decays are summed in 64 bits.  A decay between two tokens of one 16-token
 // tile is the exponential of a difference of coarse parts (multiples of 1/64,
@@ -36,6 +42,15 @@
 // factors that are both at most 1, from the tile's start to the query and from
 // the key to the tile's start.  A decay below e^-128 is 0 in fp32, so g is clamped
 // there and -infinity needs no special case.
+//
+// What bounds it: 14286 ragged tokens x 32 heads, d = 128, bf16 take 62 us (state)
+// and 96 us (outputs), where a copy of the same bytes would take 35 and 75.  In
+// the output pass a 32-token chunk of a workgroup takes 5.6 k cycles, two
+// workgroups a CU: 0.6 k to issue the loads, 0.9 k scores, 0.6 k S^T Q, 1.3 k
+// update, 0.7 k V^T P^T and stores, 0.5 k staging, 0.8 k barriers.  VALU, MFMA and
+// LDS are busy 28, 20 and 33 % of the time: latencies inside a wave, with two
+// waves a SIMD (232 VGPRs) to hide them.  Chunks re-read from the cache are no
+// faster, bank-conflict-free tiles gained 1 %, a third wave a SIMD spills.
 #pragma once
 
 #include "gdn_device.h"
@@ -77,20 +92,29 @@ __device__ __forceinline__ int shift_for(float m) {
   return e < -100 ? -100 : (e > 100 ? 100 : e);
 }
 
-// Sequence and token range of segment `seg` (false past the last one).
-__device__ __forceinline__ bool segment_range(const LinearArgs& p, int seg, int& s, int& t0, int& t1) {
+// Segment `seg`: its sequence and tokens, its number in the sequence and whether
+// it is the last.  An empty sequence has one empty segment.  False past the end.
+struct Segment {
+  int s, t0, t1, j;
+  bool last;
+};
+
+__device__ __forceinline__ bool find_segment(const LinearArgs& p, int seg, Segment& x) {
   if (p.seg_tokens == 0) {
-    s = seg;
-    seq_range(p.cu, p.T, p.total, s, t0, t1);
+    x.s = seg;
+    x.j = 0;
+    x.last = true;
+    seq_range(p.cu, p.T, p.total, seg, x.t0, x.t1);
     return true;
   }
   const int L = p.seg_tokens;
   if (p.cu == nullptr) {
     const int per = (p.T + L - 1) / L;
-    s = seg / per;
-    const int first = s * p.T + (seg % per) * L;
-    t0 = first;
-    t1 = min(first + L, (s + 1) * p.T);
+    x.s = seg / per;
+    x.j = seg % per;
+    x.last = x.j == per - 1;
+    x.t0 = x.s * p.T + x.j * L;
+    x.t1 = min(x.t0 + L, (x.s + 1) * p.T);
     return true;
   }
   const int lane = threadIdx.x & 63;
@@ -98,7 +122,7 @@ __device__ __forceinline__ bool segment_range(const LinearArgs& p, int seg, int&
   for (int s0 = 0; s0 < p.B; s0 += 64) {
     int a = 0, b = 0;
     if (s0 + lane < p.B) clamp_range(p.cu[s0 + lane], p.cu[s0 + lane + 1], p.total, a, b);
-    const int n = (b - a + L - 1) / L;
+    const int n = s0 + lane < p.B ? max(1, (b - a + L - 1) / L) : 0;
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -108,14 +132,15 @@ __device__ __forceinline__ bool segment_range(const LinearArgs& p, int seg, int&
     const uint64_t hit = __ballot(base + incl > seg);
     if (hit) {
       const int f = (int)__builtin_ctzll(hit);
-      const int j = seg - (base + __shfl(incl, f) - __shfl(n, f));
-      const int begin = __shfl(a, f), end = __shfl(b, f);
-      s = s0 + f;
-      t0 = begin + j * L;
-      t1 = min(t0 + L, end);
+      const int count = __builtin_amdgcn_readlane(n, f);
+      x.s = s0 + f;
+      x.j = seg - (base + __builtin_amdgcn_readlane(incl, f) - count);
+      x.last = x.j == count - 1;
+      x.t0 = __builtin_amdgcn_readlane(a, f) + x.j * L;
+      x.t1 = min(x.t0 + L, __builtin_amdgcn_readlane(b, f));
       return true;
     }
-    base += __shfl(incl, 63);
+    base += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -134,11 +159,11 @@ __device__ __forceinline__ int state_row(int t, int m) {
 // to waves: the passes may deal them differently.
 __device__ __forceinline__ int state_col(int dv, int n, int m) { return dv < 32 ? m : state_row<32>(n, m); }
 
-// A chunk's decays; the state pass keeps only the first.
+// A chunk's decays; the state pass keeps only the first two.
 template <int C, bool STATE>
 struct Decays {
   static constexpr int O = STATE ? 4 : C, RT = C / 16;
-  __align__(16) float w[C];              // e^{G_last - G_i}, times what follows in the state pass
+  __align__(16) float w[C];              // e^{G_last - G_i}
   __align__(16) float gamma[4];          // e^{G_last}
   __align__(16) float hi[O];             // coarse and fine part of G_i
   __align__(16) float lo[O];
@@ -148,16 +173,16 @@ struct Decays {
 };
 
 // One wave: the decays of a chunk from lane i's log decay (0 past the end);
-// returns their sum.  `rest`: log decay of what follows the chunk (state pass).
+// returns their sum.
 template <int C, bool STATE>
-__device__ __forceinline__ double fill_decays(float g, double rest, Decays<C, STATE>& d) {
+__device__ __forceinline__ double fill_decays(float g, Decays<C, STATE>& d) {
   const int lane = threadIdx.x & 63;
   const double x = wave_scan64(lane < C ? (double)(g < -128.f ? -128.f : g) : 0.0);
   const double end = lane64(x, C - 1);
-  if (lane < C) d.w[lane] = expf((float)(rest + (end - x)));
+  if (lane < C) d.w[lane] = expf((float)(end - x));
+  if (lane == 0) d.gamma[0] = expf((float)end);
   if constexpr (!STATE) {
     constexpr int RT = C / 16;
-    if (lane == 0) d.gamma[0] = expf((float)end);
     double start = 0.0;
 #pragma unroll
     for (int t = 1; t < RT; ++t) {
@@ -179,31 +204,45 @@ __device__ __forceinline__ double fill_decays(float g, double rest, Decays<C, ST
 // Fragments of P: row tile i holds i / 2 + 1 blocks of 32 keys.
 __device__ __forceinline__ constexpr int p_frag(int i, int b) { return (i + 1) * (i + 1) / 4 + b; }
 
+// A row-major tile of W columns in LDS.  16-bit rows are unpadded; the 16-byte
+// pieces of row r are permuted by an exclusive or with a value that makes both
+// the 16 rows of one piece (row_frag) and the 4 rows x 4 pieces of a transpose
+// read (token_frag) fall on different banks.
+template <typename T, int W>
+struct Tile {
+  static constexpr int P = W * (int)sizeof(T) / 16;             // pieces a row
+  static constexpr int STRIDE = sizeof(T) == 2 ? W : W + 4;
+  static __device__ __forceinline__ int at(int r, int c) {
+    if constexpr (sizeof(T) == 4) return r * STRIDE + c;
+    const int q = r >> 2 & 3;
+    const int x = P == 16 ? (r & 3) << 2 | q : P == 8 ? (r & 2) << 1 | q : P == 4 ? q : r >> 3 & 1;
+    return r * STRIDE + ((c >> 3 ^ x) << 3) + (c & 7);
+  }
+};
+
 template <typename T, int C, int DK, int NT, int NW, bool STATE>
 struct Smem {
   static constexpr int CW = 16 * NT * NW;
-  static constexpr int PAD = 16 / (int)sizeof(T);
-  static constexpr int KS = DK + PAD, VS = CW + PAD;   // row strides
-  __align__(16) T k[C * KS];
-  __align__(16) T v[C * VS];
-  __align__(16) T q[STATE ? PAD : C * KS];
-  __align__(16) T p[STATE ? PAD : p_frag(C / 16, 0) * 512];
+  __align__(16) T k[C * Tile<T, DK>::STRIDE];
+  __align__(16) T v[C * Tile<T, CW>::STRIDE];
+  __align__(16) T q[STATE ? 8 : C * Tile<T, DK>::STRIDE];
+  __align__(16) T p[STATE ? 8 : p_frag(C / 16, 0) * 512];
   Decays<C, STATE> d[2];
 };
 
 // A (or, transposed, B) operand of rows 16*tile.. over dk block kb.
 template <typename T, int DK>
-__device__ __forceinline__ Frag<T> row_frag(const T* base, int stride, int tile, int kb) {
+__device__ __forceinline__ Frag<T> row_frag(const T* base, int tile, int kb) {
   const int lane = threadIdx.x & 63, i16 = lane & 15, g4 = lane >> 4;
-  const T* r = base + (16 * tile + i16) * stride;
+  const T* r = base + 16 * tile * Tile<T, DK>::STRIDE + Tile<T, DK>::at(i16, DK >= 32 ? 32 * kb + 8 * g4 : 4 * g4);
   if constexpr (DK >= 32) {
-    return load_frag_8<T>(r + 32 * kb + 8 * g4);
+    return load_frag_8<T>(r);
   } else {
     Frag<T> f = zero_frag<T>();
     if constexpr (sizeof(T) == 4) {
-      f.lo = *reinterpret_cast<const f32x4*>(r + 4 * g4);
+      f.lo = *reinterpret_cast<const f32x4*>(r);
     } else {
-      const auto a = *reinterpret_cast<const typename Half4<T>::type*>(r + 4 * g4);
+      const auto a = *reinterpret_cast<const typename Half4<T>::type*>(r);
       f.v[0] = a[0]; f.v[1] = a[1]; f.v[2] = a[2]; f.v[3] = a[3];
     }
     return f;
@@ -212,22 +251,22 @@ __device__ __forceinline__ Frag<T> row_frag(const T* base, int stride, int tile,
 
 // Operand over the 32 tokens of block tb for column tile `c0..`: slot 8g + j is
 // token 32tb + 4g + j (j < 4) or 32tb + 16 + 4g + j - 4.  `cols(m)`: column of row m.
-template <typename T, typename F>
-__device__ __forceinline__ Frag<T> token_frag(const T* base, int stride, int tb, F cols) {
+template <typename T, int W, typename F>
+__device__ __forceinline__ Frag<T> token_frag(const T* base, int tb, F cols) {
+  using M = Tile<T, W>;
   const int lane = threadIdx.x & 63, i16 = lane & 15, g4 = lane >> 4;
   Frag<T> f;
   if constexpr (sizeof(T) == 4) {
     const int c = cols(i16);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      f.lo[q] = base[(32 * tb + 4 * g4 + q) * stride + c];
-      f.hi[q] = base[(32 * tb + 16 + 4 * g4 + q) * stride + c];
+      f.lo[q] = base[M::at(32 * tb + 4 * g4 + q, c)];
+      f.hi[q] = base[M::at(32 * tb + 16 + 4 * g4 + q, c)];
     }
   } else {
     // lane i addresses token i / 4 and the four columns of rows 4 (i % 4) ..
-    const int c = cols(4 * (i16 & 3));
-    const T* a = base + (32 * tb + 4 * g4 + (i16 >> 2)) * stride + c;
-    const s16x4 x = lds_read_tr(a), y = lds_read_tr(a + 16 * stride);
+    const T* a = base + 32 * tb * M::STRIDE + M::at(4 * g4 + (i16 >> 2), cols(4 * (i16 & 3)));
+    const s16x4 x = lds_read_tr(a), y = lds_read_tr(a + 16 * M::STRIDE);
     union { s16x4 s[2]; decltype(f.v) v; } u;
     u.s[0] = x;
     u.s[1] = y;
@@ -269,7 +308,9 @@ template <typename T, int C, int DK, int NT, int NW, Pass PASS>
 __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) {
   constexpr bool STATE = PASS == Pass::kState;
   using SM = Smem<T, C, DK, NT, NW, STATE>;
-  constexpr int CW = SM::CW, KS = SM::KS, VS = SM::VS, THREADS = 64 * NW;
+  constexpr int CW = SM::CW, THREADS = 64 * NW;
+  using KT = Tile<T, DK>;
+  using VT = Tile<T, CW>;
   constexpr int RT = C / 16, NTB = C / 32;                    // token tiles and 32-token blocks
   constexpr int NST = DK / 16, NKB = DK >= 32 ? DK / 32 : 1;  // state row tiles, dk blocks
   constexpr int PER = 16 / (int)sizeof(T), KP = DK / PER, VP = CW / PER;   // 16-byte pieces a row
@@ -280,128 +321,169 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
   __shared__ SM sm;
 
   // XCD-aware order: the workgroups that share one segment's keys get ids equal mod 8
-  const int G = p.Hv / p.Hq;
-  const int unit = (int)(blockIdx.x >> 3) / G * 8 + (int)(blockIdx.x & 7);
+  const int G = p.Hv / p.Hq, nsl = p.dv / CW, share = G * nsl;
+  const int unit = (int)(blockIdx.x >> 3) / share * 8 + (int)(blockIdx.x & 7);
   if (unit >= p.max_segs * p.Hq) return;
-  const int seg = unit / p.Hq, hk = unit % p.Hq, h = hk * G + (int)(blockIdx.x >> 3) % G;
+  const int seg = unit / p.Hq, hk = unit % p.Hq, sub = (int)(blockIdx.x >> 3) % share;
+  const int h = hk * G + sub / nsl, slice = sub % nsl;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, g4 = lane >> 4;
-  int s, t0, t1;
-  if (!segment_range(p, seg, s, t0, t1)) return;
-  s = __builtin_amdgcn_readfirstlane(s);
-  t0 = __builtin_amdgcn_readfirstlane(t0);
-  t1 = __builtin_amdgcn_readfirstlane(t1);
-  const size_t per = (size_t)DK * CW, krow = (size_t)p.Hq * DK, vrow = (size_t)p.Hv * CW;
+  Segment sg;
+  if (!find_segment(p, seg, sg)) return;
+  const int s = __builtin_amdgcn_readfirstlane(sg.s), t0 = __builtin_amdgcn_readfirstlane(sg.t0),
+            t1 = __builtin_amdgcn_readfirstlane(sg.t1), sj = __builtin_amdgcn_readfirstlane(sg.j);
+  const size_t per = (size_t)DK * p.dv, krow = (size_t)p.Hq * DK, vrow = (size_t)p.Hv * p.dv;
   const T* qp = static_cast<const T*>(p.q) + (size_t)hk * DK;
   const T* kp = static_cast<const T*>(p.k) + (size_t)hk * DK;
-  const T* vp = static_cast<const T*>(p.v) + (size_t)h * CW;
-  const int tile0 = wave * NT;   // this wave's first column tile
+  const T* vp = static_cast<const T*>(p.v) + (size_t)h * p.dv + slice * CW;
+  const int tile0 = wave * NT;   // this wave's first column tile in the slice
 
   // state tile (t, n): lane holds rows 4g..4g+3 of the tile, column i16
   f32x4 S[NST][NT];
-  auto seg_at = [&](int t, int n) {   // segment states are kept in this order
-    return reinterpret_cast<f32x4*>(p.seg_state + ((size_t)seg * p.Hv + h) * per) +
-           (t * (NT * NW) + tile0 + n) * 64 + lane;
+  auto seg_at = [&](int j, int t, int n) {   // segment states are kept in this order
+    return reinterpret_cast<f32x4*>(p.seg_state + ((size_t)(seg - sj + j) * p.Hv + h) * per) +
+           (t * (p.dv / 16) + slice * (CW / 16) + tile0 + n) * 64 + lane;
   };
   auto state_at = [&](int t, int n, int e) {
-    return (size_t)h * per + (size_t)state_row<DK>(t, 4 * g4 + e) * CW + state_col(CW, tile0 + n, i16);
+    return (size_t)h * per + (size_t)state_row<DK>(t, 4 * g4 + e) * p.dv + slice * CW + state_col(CW, tile0 + n, i16);
   };
+  const float* s0 = p.s0 != nullptr ? p.s0 + (int64_t)s * p.s0_stride : nullptr;
+  float* so = p.s_out != nullptr ? p.s_out + (size_t)s * p.Hv * per : nullptr;
+  const float* decay = p.seg_decay + (size_t)(seg - sj) * p.Hv + h;   // of this sequence's segments
 #pragma unroll
   for (int t = 0; t < NST; ++t)
 #pragma unroll
     for (int n = 0; n < NT; ++n) S[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if constexpr (PASS == Pass::kOut) {
+  if (sj == 0 && s0 != nullptr) {
 #pragma unroll
     for (int t = 0; t < NST; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) S[t][n] = *seg_at(t, n);
-  } else if constexpr (PASS == Pass::kWhole) {
-    if (p.s0 != nullptr) {
-      const float* s0 = p.s0 + (int64_t)s * p.s0_stride;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][n][e] = s0[state_at(t, n, e)];
+  }
+  if constexpr (PASS == Pass::kOut) {
+    // the state before this segment, from those of the segments before it (the
+    // first of which includes the initial state), and after the last the final one
+    constexpr int AHEAD = 4, TG = NST * NT > 8 ? 8 / NT : NST;   // 8 tiles of 4 segments in flight
+#pragma unroll
+    for (int tg = 0; tg < NST; tg += TG) {
+      for (int j0 = 0; j0 < sj; j0 += AHEAD) {
+        f32x4 own[AHEAD][TG][NT];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+          if (j0 + j < sj)
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) own[j][t][n] = *seg_at(j0 + j, tg + t, n);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+          if (j0 + j < sj) {
+            const float f = decay[(size_t)(j0 + j) * p.Hv];
+#pragma unroll
+            for (int t = 0; t < TG; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  S[tg + t][n][e] = j0 + j > 0 ? fmaf(f, S[tg + t][n][e], own[j][t][n][e]) : own[j][t][n][e];
+          }
+      }
+    }
+    if (sg.last && so != nullptr) {
+      const float f = decay[(size_t)sj * p.Hv];
 #pragma unroll
       for (int t = 0; t < NST; ++t)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          const f32x4 own = *seg_at(sj, t, n);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) S[t][n][e] = s0[state_at(t, n, e)];
+          for (int e = 0; e < 4; ++e) so[state_at(t, n, e)] = sj > 0 ? fmaf(f, S[t][n][e], own[e]) : own[e];
+        }
     }
   }
 
-  uint4 kreg[NKL], qreg[STATE ? 1 : NKL], vreg[NVL];
-  const uint32_t koff = (uint32_t)((tid / KP) * krow * sizeof(T)) + (tid % KP) * 16;
-  const uint32_t voff = (uint32_t)((tid / VP) * vrow * sizeof(T)) + (tid % VP) * 16;
+  // A chunk's tiles on their way through registers, two chunks ahead where two
+  // sets fit.  Every fetch issues the same loads (past the end those of the last
+  // row), so that waiting for one set does not wait for the next.
+  struct Set {
+    uint4 k[NKL], q[STATE ? 1 : NKL], v[NVL];
+  };
+    constexpr bool DEEP = !STATE && 2 * NKL + NVL <= 8;   // the state pass: slower with it (74 us against 62)
+  const uint32_t krow_b = (uint32_t)(krow * sizeof(T)), vrow_b = (uint32_t)(vrow * sizeof(T));
+  const uint32_t koff = (uint32_t)(tid / KP) * krow_b, voff = (uint32_t)(tid / VP) * vrow_b;
   auto piece = [](const T* base, uint32_t off) {
     return *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(base) + off);
   };
-  auto fetch = [&](int c0) {
+  auto fetch = [&](int c0, Set& x) {
+    c0 = min(c0, t1 - 1);
+    const uint32_t last = (uint32_t)(min(C, t1 - c0) - 1);
     const T *kc = kp + (size_t)c0 * krow, *qc = qp + (size_t)c0 * krow, *vc = vp + (size_t)c0 * vrow;
-    if (t1 - c0 >= C && C * KP % THREADS == 0 && C * VP % THREADS == 0) {
 #pragma unroll
-      for (int i = 0; i < NKL; ++i) kreg[i] = piece(kc + (size_t)i * KR * krow, koff);
-      if constexpr (!STATE)
+    for (int i = 0; i < NKL; ++i) {
+      const uint32_t off = min(koff + (uint32_t)(i * KR) * krow_b, last * krow_b) + tid % KP * 16;
+      x.k[i] = piece(kc, off);
+      if constexpr (!STATE) x.q[i] = piece(qc, off);
+    }
 #pragma unroll
-        for (int i = 0; i < NKL; ++i) qreg[i] = piece(qc + (size_t)i * KR * krow, koff);
-#pragma unroll
-      for (int i = 0; i < NVL; ++i) vreg[i] = piece(vc + (size_t)i * VR * vrow, voff);
-    } else {   // rows past the end are 0
-      const int len = min(C, t1 - c0);
+    for (int i = 0; i < NVL; ++i)
+      x.v[i] = piece(vc, min(voff + (uint32_t)(i * VR) * vrow_b, last * vrow_b) + tid % VP * 16);
+  };
+  auto stage = [&](int c0, Set& x) {
+    if (t1 - c0 < C) {   // rows past the end are 0
 #pragma unroll
       for (int i = 0; i < NKL; ++i) {
-        const bool in = tid / KP + i * KR < len;
-        kreg[i] = in ? piece(kc + (size_t)i * KR * krow, koff) : uint4{0, 0, 0, 0};
-        if constexpr (!STATE) qreg[i] = in ? piece(qc + (size_t)i * KR * krow, koff) : uint4{0, 0, 0, 0};
+        const bool in = tid / KP + i * KR < t1 - c0;
+        x.k[i] = in ? x.k[i] : uint4{0, 0, 0, 0};
+        if constexpr (!STATE) x.q[i] = in ? x.q[i] : uint4{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int i = 0; i < NVL; ++i)
-        vreg[i] = tid / VP + i * VR < len ? piece(vc + (size_t)i * VR * vrow, voff) : uint4{0, 0, 0, 0};
+      for (int i = 0; i < NVL; ++i) x.v[i] = tid / VP + i * VR < t1 - c0 ? x.v[i] : uint4{0, 0, 0, 0};
     }
-  };
-  auto stage = [&] {
 #pragma unroll
     for (int i = 0; i < NKL; ++i) {
       const int r = tid / KP + i * KR;
       if (C * KP % THREADS == 0 || r < C) {
-        *reinterpret_cast<uint4*>(&sm.k[r * KS + tid % KP * PER]) = kreg[i];
-        if constexpr (!STATE) *reinterpret_cast<uint4*>(&sm.q[r * KS + tid % KP * PER]) = qreg[i];
+        *reinterpret_cast<uint4*>(&sm.k[KT::at(r, tid % KP * PER)]) = x.k[i];
+        if constexpr (!STATE) *reinterpret_cast<uint4*>(&sm.q[KT::at(r, tid % KP * PER)]) = x.q[i];
       }
     }
 #pragma unroll
     for (int i = 0; i < NVL; ++i) {
       const int r = tid / VP + i * VR;
-      if (C * VP % THREADS == 0 || r < C) *reinterpret_cast<uint4*>(&sm.v[r * VS + tid % VP * PER]) = vreg[i];
+      if (C * VP % THREADS == 0 || r < C) *reinterpret_cast<uint4*>(&sm.v[VT::at(r, tid % VP * PER)]) = x.v[i];
     }
   };
-  // Wave 0 turns log decays into decays one chunk ahead.  The state pass goes from
-  // the last chunk to the first, so that its state takes no factor on the way
-  // and ends where the next pass begins to read.
+  // wave 0 turns log decays into decays one chunk ahead
   double gsum = 0.0;
   auto load_g = [&](int c0) {
-    return lane < C && c0 >= t0 && c0 + lane < t1 ? p.g[(size_t)(c0 + lane) * (size_t)p.g_stride + h] : 0.f;
+    return lane < C && c0 + lane < t1 ? p.g[(size_t)(c0 + lane) * (size_t)p.g_stride + h] : 0.f;
   };
-  const int nch = (t1 - t0 + C - 1) / C, step = STATE ? -C : C, begin = STATE ? t0 + (nch - 1) * C : t0;
   float gnext = 0.f;
-  if (nch > 0) {
-    fetch(begin);
+  Set xa, xb;
+  if (t0 < t1) {
+    float g0 = 0.f;
     if (wave == 0) {
-      const float g0 = load_g(begin);
-      gnext = load_g(begin + step);
-      gsum += fill_decays<C, STATE>(g0, 0.0, sm.d[0]);
+      g0 = load_g(t0);
+      gnext = load_g(t0 + C);
     }
-    stage();
+    fetch(t0, xa);
+    if constexpr (DEEP) fetch(t0 + C, xb);
+    if (wave == 0) gsum += fill_decays<C, STATE>(g0, sm.d[0]);
+    stage(t0, xa);
   }
   lds_barrier();
-  for (int ch = 0, c0 = begin; ch < nch; ++ch, c0 += step) {
+  // one chunk, `next` holding the one after it and `free` taking the one fetched
+  auto chunk = [&](int c0, int par, Set& next, Set& free) __attribute__((always_inline)) {
     const int len = min(C, t1 - c0);
-    const bool more = ch + 1 < nch;
-    const auto& D = sm.d[ch & 1];
-    if (more) {
-      fetch(c0 + step);
-      if (wave == 0) {
-        const float g1 = gnext;
-        gnext = load_g(c0 + 2 * step);
-        gsum += fill_decays<C, STATE>(g1, STATE ? gsum : 0.0, sm.d[(ch + 1) & 1]);
-      }
-    }
+    const bool more = c0 + C < t1;
+    const auto& D = sm.d[par];
+    // the log decays first: once the tiles are staged they have arrived too
+    const float g1 = gnext;
+    if (wave == 0) gnext = load_g(c0 + 2 * C);
+    fetch(c0 + (DEEP ? 2 * C : C), free);
+    if (wave == 0 && more) gsum += fill_decays<C, STATE>(g1, sm.d[par ^ 1]);
 
     // V operands of this wave's columns
     Frag<T> vf[NTB][NT];
@@ -409,46 +491,40 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
     for (int b = 0; b < NTB; ++b)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        vf[b][n] = token_frag<T>(sm.v, VS, b, [&](int m) { return state_col(CW, tile0 + n, m); });
+        vf[b][n] = token_frag<T, CW>(sm.v, b, [&](int m) { return state_col(CW, tile0 + n, m); });
 
     f32x4 acc[STATE ? 1 : RT][NT];
     if constexpr (!STATE) {
-      // this wave's fragments of the decayed scores (wave 0 has the decays to do)
-      for (int it = NW - 1 - wave; it < p_frag(RT, 0); it += NW) {
-        const int i = it > 0 ? 1 + it / 2 : 0, b = it > 1 ? it & 1 : 0;   // it = p_frag(i, b)
-        Frag<T> qf[NKB];
+      // this wave's tiles of the decayed scores (wave 0 has the decays to do)
+      for (int it = NW - 1 - wave; it < RT * (RT + 1) / 2; it += NW) {
+        const int i = it < 1 ? 0 : it < 3 ? 1 : it < 6 ? 2 : 3, j = it - i * (i + 1) / 2;   // j <= i
+        f32x4 pt = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) qf[kb] = row_frag<T, DK>(sm.q, KS, i, kb);
-        const float row = D.row[16 * i + i16];
-        f32x4 pt[2];
+        for (int kb = 0; kb < NKB; ++kb) {
+          const Frag<T> qf = row_frag<T, DK>(sm.q, i, kb), kf = row_frag<T, DK>(sm.k, j, kb);
+          if constexpr (DK >= 32) mma<T>(pt, kf, qf);
+          else mma_lo<T>(pt, kf, qf);
+        }
+        // lane holds (key 16j + 4g + e, query 16i + i16)
+        if (j < i) {
+          const float row = D.row[16 * i + i16];
+          const f32x4 col = *reinterpret_cast<const f32x4*>(&D.col[i - 1][16 * j + 4 * g4]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = 2 * b + u;
-          pt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (j > i) continue;
+          for (int e = 0; e < 4; ++e) pt[e] *= row * col[e];
+        } else {
+          const float ih = D.hi[16 * i + i16], il = D.lo[16 * i + i16];
+          const f32x4 jh = *reinterpret_cast<const f32x4*>(&D.hi[16 * j + 4 * g4]);
+          const f32x4 jl = *reinterpret_cast<const f32x4*>(&D.lo[16 * j + 4 * g4]);
 #pragma unroll
-          for (int kb = 0; kb < NKB; ++kb) {
-            const Frag<T> kf = row_frag<T, DK>(sm.k, KS, j, kb);
-            if constexpr (DK >= 32) mma<T>(pt[u], kf, qf[kb]);
-            else mma_lo<T>(pt[u], kf, qf[kb]);
-          }
-          // lane holds (key 16j + 4g + e, query 16i + i16)
-          if (j < i) {
-            const f32x4 col = *reinterpret_cast<const f32x4*>(&D.col[i - 1][16 * j + 4 * g4]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pt[u][e] *= row * col[e];
-          } else {
-            const float ih = D.hi[16 * i + i16], il = D.lo[16 * i + i16];
-            const f32x4 jh = *reinterpret_cast<const f32x4*>(&D.hi[16 * j + 4 * g4]);
-            const f32x4 jl = *reinterpret_cast<const f32x4*>(&D.lo[16 * j + 4 * g4]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float d = (ih - jh[e]) + (il - jl[e]);
-              pt[u][e] = 4 * g4 + e <= i16 ? pt[u][e] * __expf(d) : 0.f;
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float d = (ih - jh[e]) + (il - jl[e]);
+            pt[e] = 4 * g4 + e <= i16 ? pt[e] * __expf(d) : 0.f;
           }
         }
-        store_frag_native<T>(&sm.p[it * 512 + lane * 8], make_frag<T>(pt[0], pt[1]));
+        // half a fragment; the last row tile's other half is 0
+        T* half = &sm.p[p_frag(i, j >> 1) * 512 + lane * 8 + 4 * (j & 1)];
+        store4<T>(half, pt[0], pt[1], pt[2], pt[3]);
+        if (j == i && (j & 1) == 0) store4<T>(half + 4, 0.f, 0.f, 0.f, 0.f);
       }
       // the state's part of o; fp16 operands scaled by a power of two into its range
       int sh = 0;
@@ -481,7 +557,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          const Frag<T> qf = row_frag<T, DK>(sm.q, KS, i, b);
+          const Frag<T> qf = row_frag<T, DK>(sm.q, i, b);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if constexpr (DK >= 32) mma<T>(acc[i][n], sf[n], qf);
@@ -519,13 +595,11 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         up = ldexpf(1.f, sh);
         down = ldexpf(1.f, -sh);
       }
-      const float gamma = STATE ? up : D.gamma[0] * up;
-      if (!STATE || __is_same(T, _Float16)) {
+      const float gamma = D.gamma[0] * up;
 #pragma unroll
-        for (int t = 0; t < NST; ++t)
+      for (int t = 0; t < NST; ++t)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) S[t][n] *= gamma;
-      }
+        for (int n = 0; n < NT; ++n) S[t][n] *= gamma;
 #pragma unroll
       for (int b = 0; b < NTB; ++b) {
         Frag<T> part[NT][NP];
@@ -539,7 +613,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         }
 #pragma unroll
         for (int t = 0; t < NST; ++t) {
-          const Frag<T> kt = token_frag<T>(sm.k, KS, b, [&](int r) { return state_row<DK>(t, r); });
+          const Frag<T> kt = token_frag<T, DK>(sm.k, b, [&](int r) { return state_row<DK>(t, r); });
 #pragma unroll
           for (int q = 0; q < NP; ++q)
 #pragma unroll
@@ -554,9 +628,10 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
       }
     }
     lds_barrier();   // the tiles are read, P is written
+    if (more) stage(c0 + C, next);
 
     if constexpr (!STATE) {
-      T* orow = static_cast<T*>(p.o) + ((size_t)c0 + i16) * vrow + (size_t)h * CW;
+      T* orow = static_cast<T*>(p.o) + ((size_t)c0 + i16) * vrow + (size_t)h * p.dv + slice * CW;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
 #pragma unroll
@@ -581,19 +656,25 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         }
       }
     }
-    if (more) stage();
     lds_barrier();
+  };
+  if constexpr (DEEP) {
+    for (int c0 = t0; c0 < t1; c0 += 2 * C) {
+      chunk(c0, 0, xb, xa);
+      if (c0 + C < t1) chunk(c0 + C, 1, xa, xb);
+    }
+  } else {
+    for (int c0 = t0, par = 0; c0 < t1; c0 += C, par ^= 1) chunk(c0, par, xa, xa);
   }
 
   if constexpr (STATE) {
-    if (tid == 0) p.seg_decay[(size_t)seg * p.Hv + h] = expf((float)gsum);
+    if (tid == 0 && slice == 0) p.seg_decay[(size_t)seg * p.Hv + h] = expf((float)gsum);
 #pragma unroll
     for (int t = 0; t < NST; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) *seg_at(t, n) = S[t][n];
+      for (int n = 0; n < NT; ++n) *seg_at(sj, t, n) = S[t][n];
   } else if constexpr (PASS == Pass::kWhole) {
-    if (p.s_out != nullptr) {
-      float* so = p.s_out + (size_t)s * p.Hv * per;
+    if (so != nullptr) {
 #pragma unroll
       for (int t = 0; t < NST; ++t)
 #pragma unroll
@@ -604,89 +685,35 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
   }
 }
 
-// Replaces each segment's own state by the state before it, and writes the
-// final states: element-wise recurrences over the segments of a sequence, in the
-// segment states' order (a thread holds four rows of one column).
-template <int DK, int DV>
-__global__ __launch_bounds__(64) void linear_carry_kernel(LinearArgs p) {
-  constexpr int NB = DK * DV / 256, AHEAD = 8;   // tiles a state, segments in flight
-  constexpr size_t per = (size_t)DK * DV;
-  const int tile = (int)(blockIdx.x % NB), pair = (int)(blockIdx.x / NB);
-  const int s = pair / p.Hv, h = pair % p.Hv, L = p.seg_tokens;
-  const int lane = threadIdx.x;
-  int first = 0, n = 0;
-  if (p.cu == nullptr) {
-    n = (p.T + L - 1) / L;
-    first = s * n;
-  } else {
-    for (int i0 = 0; i0 <= s; i0 += 64) {
-      int a = 0, b = 0;
-      if (i0 + lane <= s) clamp_range(p.cu[i0 + lane], p.cu[i0 + lane + 1], p.total, a, b);
-      int c = (b - a + L - 1) / L;
-      const int mine = __shfl(c, s - i0 < 64 ? s - i0 : 63);
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) c += __shfl_xor(c, d);
-      first += c;
-      n = mine;
-    }
-    first = __builtin_amdgcn_readfirstlane(first - n);
-    n = __builtin_amdgcn_readfirstlane(n);
-  }
-  n = min(n, p.max_segs - first);
-  const int row = state_row<DK>(tile / (DV / 16), 4 * (lane >> 4)), col = state_col(DV, tile % (DV / 16), lane & 15);
-  const size_t at = (size_t)h * per + (size_t)row * DV + col;
-  f32x4 S = {0.f, 0.f, 0.f, 0.f};
-  if (p.s0 != nullptr) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[e] = p.s0[(int64_t)s * p.s0_stride + at + (size_t)e * DV];
-  }
-  f32x4* x = reinterpret_cast<f32x4*>(p.seg_state + ((size_t)first * p.Hv + h) * per) + tile * 64 + lane;
-  const float* a = p.seg_decay + (size_t)first * p.Hv + h;
-  const size_t step = (size_t)p.Hv * per / 4;
-  for (int j0 = 0; j0 < n; j0 += AHEAD) {
-    f32x4 own[AHEAD];
-    const int m = min(AHEAD, n - j0);
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (j < m) own[j] = x[(size_t)(j0 + j) * step];
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (j < m) {
-        x[(size_t)(j0 + j) * step] = S;
-        const float f = a[(size_t)(j0 + j) * p.Hv];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[i] = fmaf(f, S[i], own[j][i]);
-      }
-  }
-  if (p.s_out != nullptr) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p.s_out[(size_t)s * p.Hv * per + at + (size_t)e * DV] = S[e];
-  }
-}
-
 template <typename T, int C, int DK, int NT, int NW, Pass P>
 static hipError_t run_pass(KernelId id, const LinearArgs& a, hipStream_t s) {
   const long long units = (long long)a.max_segs * a.Hq;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * (a.Hv / a.Hq)));
+  const dim3 grid((unsigned)((units + 7) / 8 * 8 * (a.Hv / a.Hq) * (a.dv / (16 * NT * NW))));
   prof_begin(id, s);
   hipLaunchKernelGGL((linear_chunk_kernel<T, C, DK, NT, NW, P>), grid, dim3(64 * NW), 0, s, a);
   prof_end(id, s);
   return hipGetLastError();
 }
 
+// TILES column tiles a workgroup, NT a wave in the output pass (whose chunks
+// are COUT tokens), else one.
+template <typename T, int DK, int TILES, int NT, int COUT>
+static hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
+  constexpr int C = sizeof(T) == 2 ? 64 : 32;
+  if (a.seg_tokens == 0) return run_pass<T, C, DK, 1, TILES, Pass::kWhole>(K_LIN_OUT, a, s);
+  const hipError_t e = run_pass<T, C, DK, 1, TILES, Pass::kState>(K_LIN_STATE, a, s);
+  return e == hipSuccess ? run_pass<T, COUT, DK, NT, TILES / NT, Pass::kOut>(K_LIN_OUT, a, s) : e;
+}
+
+// Up to 256 (segment, head) pairs leave CUs idle: half the columns a workgroup,
+// one column tile a wave (2048 tokens x 6 heads fp16: 30 us, 34 us without).
 template <typename T, int DK, int DV>
 static hipError_t launch_d(const LinearArgs& a, hipStream_t s) {
-  // one column tile a wave; the output pass of 16-bit inputs two, in shorter chunks
-  constexpr int TILES = DV / 16, C = sizeof(T) == 2 ? 64 : 32;
-  constexpr int NT = sizeof(T) == 2 && TILES > 1 ? 2 : 1;
-  if (a.seg_tokens == 0) return run_pass<T, C, DK, 1, TILES, Pass::kWhole>(K_LIN_OUT, a, s);
-  hipError_t e = run_pass<T, C, DK, 1, TILES, Pass::kState>(K_LIN_STATE, a, s);
-  if (e != hipSuccess) return e;
-  prof_begin(K_LIN_CARRY, s);
-  hipLaunchKernelGGL((linear_carry_kernel<DK, DV>), dim3((unsigned)(DK * DV / 256 * a.B * a.Hv)), dim3(64), 0, s, a);
-  prof_end(K_LIN_CARRY, s);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  return run_pass<T, 32, DK, NT, TILES / NT, Pass::kOut>(K_LIN_OUT, a, s);
+  if constexpr (DV >= 64) {
+    if ((int64_t)a.max_segs * a.Hv <= 256) return launch_tiles<T, DK, DV / 32, 1, sizeof(T) == 2 ? 64 : 32>(a, s);
+  }
+  constexpr int NT = sizeof(T) == 2 && DV >= 64 ? 2 : 1;
+  return launch_tiles<T, DK, DV / 16, NT, 32>(a, s);
 }
 
 template <typename T, int DK>

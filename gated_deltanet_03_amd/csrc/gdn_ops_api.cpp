@@ -35,26 +35,31 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 //
 // A segment's workgroup walks its chunks one after another, so (sequence, head)
 // pairs alone fill the 256 CUs only from a few hundred on.  Below that the
-// tokens are cut so that about kTargetWg (segment, head) workgroups exist (two
-// for each CU run together), but not into fewer than kMinSeg tokens: a segment
-// costs four passes over its [dk x dv] fp32 state beside its tokens, and the
-// split two more launches.
-constexpr int64_t kTargetWg = 480, kFullWg = 512, kMinSeg = 128;
+// tokens are cut
+//  * so that about kTargetWg (segment, head) workgroups exist, two for each CU
+//    (14286 ragged tokens x 32 heads bf16: 160 us; 600 of them 186 us);
+//  * but not below sqrt(c * longest) tokens: the output pass of a sequence's last
+//    segment sums the states of all before it, so fewer tokens a segment make
+//    its walk shorter and that sum longer (2048 tokens x 6 heads fp16: 30 us,
+//    32 us with c = 7).  A token costs more in fp32 (2221 ragged tokens x 8 heads:
+//    33 us, 44 us with c = 14).
+constexpr int64_t kTargetWg = 480, kFullWg = 512;
 
 int32_t segment_tokens(const gdn_shape* sh, int64_t total, bool ragged) {
   const int64_t pairs = (int64_t)sh->B * sh->Hv;
   if (pairs == 0 || pairs >= kFullWg) return 0;
   // the longest sequence is not known for ragged input; total bounds it
   const int64_t longest = ragged ? total : sh->T;
-  int64_t seg = (total * sh->Hv + kTargetWg - 1) / kTargetWg;
-  seg = std::max<int64_t>((seg + 63) / 64 * 64, kMinSeg);
+  int64_t seg = std::max<int64_t>((total * sh->Hv + kTargetWg - 1) / kTargetWg,
+                                  (int64_t)std::sqrt((sh->dtype == GDN_F32 ? 7.0 : 14.0) * (double)longest));
+  seg = (seg + 63) / 64 * 64;
   return longest <= 2 * seg ? 0 : (int32_t)seg;
 }
 
 int64_t max_segments(const gdn_shape* sh, int64_t total, bool ragged, int32_t seg) {
   if (seg == 0) return sh->B;
   if (!ragged) return (int64_t)sh->B * ((sh->T + seg - 1) / seg);
-  return total / seg + sh->B;   // every sequence adds at most one partial segment
+  return total / seg + sh->B;   // every sequence adds at most one partial (or empty) segment
 }
 
 size_t decay_bytes(int64_t segs, int32_t Hv) { return align_up((size_t)segs * Hv * sizeof(float), 256); }
