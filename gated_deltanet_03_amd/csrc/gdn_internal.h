@@ -111,7 +111,8 @@ struct LinearArgs {
   float* su;             // [B, cap, R]
   // prefill only
   int32_t seg_tokens, max_segs;
-  float* seg_state;      // [max_segs, Hv, dk, dv]: a segment's own state (the first's with the initial one)
+  float* seg_state;      // [max_segs + B, Hv, dk, dv]: a segment's own state (the first's with the
+                         // initial one), then the initial states, in the kernels' order
   float* seg_decay;      // [max_segs, Hv]: its decay
 };
 

@@ -340,10 +340,11 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
 
   // state tile (t, n): lane holds rows 4g..4g+3 of the tile, column i16
   f32x4 S[NST][NT];
-  auto seg_at = [&](int j, int t, int n) {   // segment states are kept in this order
-    return reinterpret_cast<f32x4*>(p.seg_state + ((size_t)(seg - sj + j) * p.Hv + h) * per) +
+  auto slot_at = [&](int slot, int t, int n) {   // the workspace's states are kept in this order
+    return reinterpret_cast<f32x4*>(p.seg_state + ((size_t)slot * p.Hv + h) * per) +
            (t * (p.dv / 16) + slice * (CW / 16) + tile0 + n) * 64 + lane;
   };
+  auto seg_at = [&](int j, int t, int n) { return slot_at(seg - sj + j, t, n); };
   auto state_at = [&](int t, int n, int e) {
     return (size_t)h * per + (size_t)state_row<DK>(t, 4 * g4 + e) * p.dv + slice * CW + state_col(CW, tile0 + n, i16);
   };
@@ -355,12 +356,20 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
 #pragma unroll
     for (int n = 0; n < NT; ++n) S[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (sj == 0 && s0 != nullptr) {
+    // kOut takes kState's copy: in place, the initial state may be overwritten by
+    // the final one, which another workgroup writes
 #pragma unroll
     for (int t = 0; t < NST; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        if constexpr (PASS == Pass::kOut) {
+          S[t][n] = *slot_at(p.max_segs + s, t, n);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[t][n][e] = s0[state_at(t, n, e)];
+          for (int e = 0; e < 4; ++e) S[t][n][e] = s0[state_at(t, n, e)];
+          if constexpr (STATE) *slot_at(p.max_segs + s, t, n) = S[t][n];
+        }
+      }
   }
   if constexpr (PASS == Pass::kOut) {
     // the state before this segment, from those of the segments before it (the

@@ -68,7 +68,7 @@ size_t linear_workspace(const gdn_shape* sh, int64_t total, bool ragged) {
   const int32_t seg = segment_tokens(sh, total, ragged);
   if (seg == 0) return 0;
   const int64_t n = max_segments(sh, total, ragged, seg);
-  return decay_bytes(n, sh->Hv) + (size_t)n * sh->Hv * sh->dk * sh->dv * 4;
+  return decay_bytes(n, sh->Hv) + (size_t)(n + sh->B) * sh->Hv * sh->dk * sh->dv * 4;
 }
 
 // Token tensors of the linear entry points; fills `ins` (q, k, v, g, initial_state).

@@ -301,3 +301,46 @@ def test_graph_replays_follow_their_inputs():
         torch.cuda.synchronize()
         for a, b in zip(got, (*bufs.values(), *sb.values())):
             assert torch.equal(a, b), i
+
+
+# ------------------------------------------------- paths chosen by size
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("Hv,dk,dv", [(3, 128, 128), (3, 32, 64), (2, 64, 32), (2, 128, 16), (40, 64, 128)])
+def test_prefill_many_segments(dtype, Hv, dk, dv):
+    """Segments by the dozen, in a sequence and beside empty and short ones, with few
+    heads (half the columns a workgroup) and many."""
+    c = make(51, [1700, 0, 1, 1300, 0, 65], 1, Hv, dk, dv, dtype, memory=0.01)
+    o, fin = prefill(c)
+    check(o, fin, c, segs=30)
+    d = dev(c)
+    a = (d["q"], d["k"], d["v"], d["g"])
+    kw = dict(scale=d["scale"], cu_seqlens=d["cu"])
+    state = d["s0"].clone()
+    o2, fin2 = gdn.gdn_linear_prefill(*a, **kw, initial_state=state, final_state=state)      # in place
+    assert torch.equal(o, o2) and torch.equal(fin, fin2)
+    o3, none = gdn.gdn_linear_prefill(*a, **kw, initial_state=d["s0"], output_final_state=False)
+    assert none is None and torch.equal(o, o3)
+
+
+def test_prefill_segments_share_one_initial_state():
+    c = make(52, [800, 700], 1, 2, 64, 64, "f32", memory=0.01)
+    c["s0"] = c["s0"][:1].repeat(2, 1, 1, 1)
+    o, fin = prefill(c)
+    check(o, fin, c, segs=20)
+    d = dev(c)
+    o2, fin2 = gdn.gdn_linear_prefill(d["q"], d["k"], d["v"], d["g"], scale=d["scale"], cu_seqlens=d["cu"],
+                                      initial_state=d["s0"][:1].contiguous())
+    assert torch.equal(o, o2) and torch.equal(fin, fin2)
+
+
+def test_offsets_that_are_malformed_stay_in_bounds():
+    """Overlapping, reversed and out-of-range offsets give some result and touch nothing else."""
+    c = make(53, [900, 900], 1, 2, 32, 32, "bf16", memory=0.01)
+    d = dev(c)
+    for cu in ([0, 5000, 1800], [0, 1800, 0], [900, 100, 1800], [-5, 900, 1700]):
+        bad = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        for f in (gdn.gdn_linear_prefill, gdn.gdn_linear_step):
+            f(d["q"], d["k"], d["v"], d["g"], cu_seqlens=bad, initial_state=d["s0"])
+    torch.cuda.synchronize()
+    o, fin = prefill(c)
+    check(o, fin, c, segs=20)
