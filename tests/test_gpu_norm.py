@@ -148,3 +148,19 @@ def test_element_offsets_past_32_bits():
     y[-1] = 3.0
     h, _ = gdn.gdn_block_norm(y, residual_scale=2.0, out=y)
     assert y.numel() > 2 ** 31 and (h[-1] == 6.0).all() and (h[:3] == 2.0).all() and (h[-3:-1] == 2.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,group", [(17000, 64, 16), (4500, 1000, None), (4099, 4096, 128), (4097, 4099, None)])
+def test_more_rows_than_workgroups(dtype, T, D, group):
+    """Above 4096 workgroups the kernel loops over rows, keeping the weights."""
+    run(T, D, dtype, group=group, act="sigmoid", seed=T)
+
+
+def test_more_rows_than_workgroups_in_place():
+    y = torch.randn(9000, 1024, device=DEV).to(torch.bfloat16)
+    r = torch.randn_like(y)
+    w = torch.ones(1024, device=DEV, dtype=torch.bfloat16)
+    want = gdn.gdn_block_norm(y, residual=r, residual_scale=0.5, post_weight=w, next_weight=w)
+    got = gdn.gdn_block_norm(y, residual=r, residual_scale=0.5, post_weight=w, next_weight=w, out=r)
+    assert got[0] is r and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
