@@ -362,7 +362,7 @@ gdn_status gdn_linear_step(const gdn_shape* shape, const void* q, const void* k,
  * depend on how the sums are split.  draft_probs NULL: the drafts are
  * deterministic (q_i is 1 at x_i and 0 elsewhere).  A draft token outside
  * [0, V) is refused, with q_a = 0 everywhere if draft_probs is NULL.  Weights
- * that are NaN or not positive count as 0; a row whose weights are all 0 draws
+ * that are NaN, infinite or not positive count as 0; a row whose weights are all 0 draws
  * the token -1.  An idle row (draft_count[b] < 0) emits nothing: emit_count[b] = 0,
  * its tokens -1.
  *
