@@ -10,6 +10,10 @@
 // update (unlike the delta rule), so a token's only coupling is the sum over dk
 // of o: over the lanes of a column on the VALU, over the waves through LDS
 // once per TB tokens.
+//
+// Measured at 32 heads of d = 128, bf16: 64 rows of one token 40.5 us (270 MB at
+// 6.6 TB/s back to back, part of it from the last-level cache; 5.5 TB/s with other
+// inputs each time), one row 3.9 us, 8 rows of 1 to 7 tokens with records 9.4 us.
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
