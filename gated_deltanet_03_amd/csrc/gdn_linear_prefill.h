@@ -716,11 +716,13 @@ static hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
 }
 
 // Up to 256 (segment, head) pairs leave CUs idle: half the columns a workgroup,
-// one column tile a wave (2048 tokens x 6 heads fp16: 30 us, 34 us without).
+// one column tile a wave (2048 tokens x 6 heads fp16: 30 us, 34 us without; quarter
+// columns 32 us).  In fp32 the matrix units bound a workgroup, so up to 512 (2221
+// ragged tokens x 8 heads, 368 pairs: 28 us, 36 us without).
 template <typename T, int DK, int DV>
 static hipError_t launch_d(const LinearArgs& a, hipStream_t s) {
   if constexpr (DV >= 64) {
-    if ((int64_t)a.max_segs * a.Hv <= 256) return launch_tiles<T, DK, DV / 32, 1, sizeof(T) == 2 ? 64 : 32>(a, s);
+    if ((int64_t)a.max_segs * a.Hv <= (sizeof(T) == 4 ? 512 : 256)) return launch_tiles<T, DK, DV / 32, 1, sizeof(T) == 2 ? 64 : 32>(a, s);
   }
   constexpr int NT = sizeof(T) == 2 && DV >= 64 ? 2 : 1;
   return launch_tiles<T, DK, DV / 16, NT, 32>(a, s);

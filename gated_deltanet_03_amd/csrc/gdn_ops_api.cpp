@@ -40,9 +40,9 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 //    (14286 ragged tokens x 32 heads bf16: 160 us; 600 of them 186 us);
 //  * but not below sqrt(c * longest) tokens: the output pass of a sequence's last
 //    segment sums the states of all before it, so fewer tokens a segment make
-//    its walk shorter and that sum longer (2048 tokens x 6 heads fp16: 30 us,
-//    32 us with c = 7).  A token costs more in fp32 (2221 ragged tokens x 8 heads:
-//    33 us, 44 us with c = 14).
+//    its walk shorter and that sum longer (2048 tokens x 6 heads fp16: 29 us, 32
+//    with c = 8, 33 with c = 20).  A token costs more in fp32 (2221 ragged tokens
+//    x 8 heads: 28 us, 34 with c = 7; 12000 tokens x 1 head: 64 us, 76 with c = 7).
 constexpr int64_t kTargetWg = 480, kFullWg = 512;
 
 int32_t segment_tokens(const gdn_shape* sh, int64_t total, bool ragged) {
@@ -51,7 +51,7 @@ int32_t segment_tokens(const gdn_shape* sh, int64_t total, bool ragged) {
   // the longest sequence is not known for ragged input; total bounds it
   const int64_t longest = ragged ? total : sh->T;
   int64_t seg = std::max<int64_t>((total * sh->Hv + kTargetWg - 1) / kTargetWg,
-                                  (int64_t)std::sqrt((sh->dtype == GDN_F32 ? 7.0 : 14.0) * (double)longest));
+                                  (int64_t)std::sqrt((sh->dtype == GDN_F32 ? 1.5 : 14.0) * (double)longest));
   seg = (seg + 63) / 64 * 64;
   return longest <= 2 * seg ? 0 : (int32_t)seg;
 }
