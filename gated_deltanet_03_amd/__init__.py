@@ -750,7 +750,7 @@ def gdn_block_norm(y, *, gate=None, gate_act="silu", residual=None, residual_sca
     if out is None:
         out = torch.empty_like(y)
     _, ref = _descriptor(gdn_norm_shape, (y.numel() // D, D, group, _DTYPES[dtype],
-                                          0 if gate is None else _ACTS[gate_act], residual_scale, eps))
+                                          0 if gate is None else _ACTS[gate_act], float(residual_scale), float(eps)))
     stream = _on_gpu(dev)
     st = lib.gdn_block_norm(ref, y.data_ptr(), _addr(gate), _addr(residual), _addr(post_weight),
                             _addr(next_weight), out.data_ptr(), _addr(normed), stream)

@@ -77,6 +77,8 @@ gdn_status check_linear(const gdn_shape* sh, const void* q, const void* k, const
                         float* s_out, int64_t* total, Buf ins[6]) {
   gdn_status st = check_shape(sh, cu, total);
   if (st != GDN_OK) return st;
+  if (*total > (1LL << 30))   // the kernels' token indices run past the end by a few chunks or one segment
+    return fail(GDN_ERR_UNSUPPORTED, "%lld tokens exceed 2^30", (long long)*total);
   if (g_stride != 0 && g_stride != sh->Hv)
     return fail(GDN_ERR_INVALID_ARG, "g_token_stride=%lld must be 0 or Hv=%d", (long long)g_stride, sh->Hv);
   if (*total > 0) {
@@ -122,6 +124,7 @@ size_t gdn_linear_workspace_bytes(const gdn_shape* sh, int32_t ragged) {
   static const int32_t some = 0;
   int64_t total = 0;
   if (check_shape(sh, ragged ? &some : nullptr, &total) != GDN_OK) return (size_t)-1;
+  if (total > (1LL << 30)) return fail(GDN_ERR_UNSUPPORTED, "%lld tokens exceed 2^30", (long long)total), (size_t)-1;
   return linear_workspace(sh, total, ragged != 0);
 }
 

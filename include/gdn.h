@@ -301,7 +301,7 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
  *     o_t     = scale * S_t^T q_t
  *
  * with the shapes, layouts, head map, state and cu_seqlens rules of the gated
- * delta rule above; there is no beta.  `g` holds log decays in fp32:
+ * delta rule above (up to 2^30 tokens); there is no beta.  `g` holds log decays in fp32:
  * g_token_stride = Hv for one value per token and value head ([T_total, Hv]),
  * or 0 for one value per value head ([Hv], the same at every token).
  *

@@ -143,6 +143,7 @@ def test_linear_abi(lib):
     for call in (prefill, step):
         assert call(lib, shape(Hv=5)) == bad and "multiple" in last(lib)
         assert call(lib, shape(dk=48)) == uns
+        assert call(lib, shape(B=1, T=(1 << 30) + 1)) == uns and "2^30" in last(lib)
         assert call(lib, shape(dtype=5)) == bad
         assert call(lib, shape(), gs=3) == bad and "g_token_stride" in last(lib)
         assert call(lib, shape(), k=NULL) == bad and "k is NULL" in last(lib)
@@ -168,6 +169,8 @@ def test_linear_workspace(lib):
     assert prefill(lib, long, ws=A[6], n=need - 1) == gdn.GDN_ERR_INVALID_ARG
     assert prefill(lib, long, ws=ctypes.c_void_p(0x70000008), n=need) == gdn.GDN_ERR_INVALID_ARG
     assert prefill(lib, long, ws=A[1], n=need) == gdn.GDN_ERR_INVALID_ARG and "workspace overlaps k" in last(lib)
+    with pytest.raises(gdn.GdnError, match="2\\^30"):
+        gdn.gdn_linear_workspace_bytes(shape(B=3, T=1 << 29), False)
     with pytest.raises(gdn.GdnError, match="supported head dims"):
         gdn.gdn_linear_workspace_bytes(shape(dk=40), False)
 
