@@ -116,6 +116,8 @@ struct LinearArgs {
   float* seg_decay;      // [max_segs, Hv]: its decay
 };
 
+constexpr int32_t kVerifyRowMax = 65536;   // entries of a row that one workgroup verifies (no workspace)
+
 struct VerifyArgs {
   const void* p;
   const void* q;         // may be null (deterministic drafts)
@@ -146,7 +148,7 @@ struct NormArgs {
 // Opt-in per-kernel event timing (gdn_profile_enable / gdn_profile_collect).
 enum KernelId : int {
   K_PLAN = 0, K_PREP, K_STATE, K_RECURRENT, K_REPLAY, K_COPY,
-  K_LIN_STATE, K_LIN_OUT, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_NORM, kNumKernels
+  K_LIN_STATE, K_LIN_OUT, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_VERIFY_ROW, K_NORM, kNumKernels
 };
 void prof_begin(KernelId id, hipStream_t s);
 void prof_end(KernelId id, hipStream_t s);

@@ -228,6 +228,7 @@ int32_t verify_tile(int32_t V) {
 }
 
 size_t verify_workspace(const gdn_verify_shape* sh) {
+  if (sh->V <= kVerifyRowMax) return 0;
   const int32_t t = verify_tile(sh->V);
   return (size_t)sh->B * ((sh->V + t - 1) / t) * sizeof(double);
 }
@@ -254,9 +255,11 @@ gdn_status gdn_verify_drafts(const gdn_verify_shape* sh, const void* p, const vo
   if (misaligned(x, 4) || misaligned(u, 4) || misaligned(n, 4) || misaligned(tokens, 4) || misaligned(emit, 4))
     return fail(GDN_ERR_INVALID_ARG, "an int32 or fp32 argument is not 4-byte aligned");
   const size_t need = verify_workspace(sh);
-  if (ws == nullptr || ws_bytes < need)
-    return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu required", ws_bytes, need);
-  if (!aligned16(ws)) return fail(GDN_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  if (need > 0) {
+    if (ws == nullptr || ws_bytes < need)
+      return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu required", ws_bytes, need);
+    if (!aligned16(ws)) return fail(GDN_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  }
   const Buf ins[5] = {{p, ((B * (K + 1) - 1) * (size_t)sh->target_row_stride + V) * es, "target_probs"},
                       {q, K > 0 ? ((B * K - 1) * (size_t)sh->draft_row_stride + V) * es : 0, "draft_probs"},
                       {x, B * K * 4, "draft_tokens"},

@@ -1,6 +1,8 @@
 // Verification of drafted tokens against the target's probabilities.
 //
-// Two kernels.  verify_sum: one workgroup per (tile of the vocabulary, row)
+// Up to 65536 entries one kernel, a workgroup a row (verify_row): tiles of one
+// wave's 512 entries are summed, the tile that holds u * sum(w) is found among the
+// at most 128 sums and scanned by one wave.  Beyond, two kernels.  verify_sum: one workgroup per (tile of the vocabulary, row)
 // finds how many drafts the row accepts (a gather of at most K pairs), then sums
 // the tile's weights w = max(p_a - q_a, 0) (or p_a) in 64 bits.  verify_draw:
 // one workgroup per row scans the tiles' sums, finds the tile that holds
@@ -13,8 +15,10 @@
 // place one token in a hundred wrongly.
 //
 // Measured, fp32: 64 rows of 131072 with 7 drafts 13.5 + 5.5 us (64 MB, 4.7 TB/s in
-// the first kernel; 15.1 us with one tile a workgroup), one row of 32003 3.4 + 4.3 us.
-// The token is picked by ballots: with atomics on LDS the second kernel took 25 us.
+// the first kernel; 15.1 us with one tile a workgroup).  The token is picked by
+// ballots: with atomics on LDS the second kernel took 25 us.  A call on one row of
+// 32003: 9.0 us in one kernel, bound by its host time, 13.1 in two; on 64 rows of
+// 65536 12.7 us in one, 13.9 in two.
 #include "gdn_internal.h"
 #include "gdn_rows.h"
 
@@ -303,8 +307,106 @@ __global__ __launch_bounds__(VT) void verify_draw_kernel(VerifyArgs p) {
   if (tid == 0) p.tokens[tok + a] = token;
 }
 
+constexpr int VROW_WAVES = 16, VROW_PASS = VROW_WAVES * 64 * VPT;   // entries a pass of a row's workgroup
+
+template <typename T>
+__global__ __launch_bounds__(64 * VROW_WAVES) void verify_row_kernel(VerifyArgs p) {
+  constexpr int MAXT = kVerifyRowMax / (64 * VPT), AHEAD = 4;
+  static_assert(MAXT == 128, "two tiles a lane");
+  __shared__ double part[MAXT];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const size_t tok = (size_t)b * (p.K + 1);
+  const int n = drafts_of(p, b);
+  const int a = n < 0 ? -1 : accepted<T>(p, b, n);
+  if (tid == 0) p.emit[b] = a + 1;
+  for (int i = tid; i <= p.K; i += 64 * VROW_WAVES)
+    if (i != a) p.tokens[tok + i] = i < a ? p.x[(size_t)b * p.K + i] : -1;
+  if (a < 0) return;
+  const bool refused = a < n;
+  Weights<T> wt(p, b, a, refused);
+  double s0, s1, upto, total;
+  // sums of the tiles, their prefix sums (each lane owns two neighbours) and the total
+  auto sums = [&] {
+    for (int e0 = 0; e0 < p.V; e0 += AHEAD * VROW_PASS) {
+      if (e0 + AHEAD * VROW_PASS <= p.V) {
+        typename Weights<T>::Raw raw[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) wt.fetch(e0 + i * VROW_PASS + tid * VPT, raw[i]);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+          const int e = e0 + i * VROW_PASS + tid * VPT;
+          double w[VPT], s = 0.0;
+          wt.weigh(e, raw[i], w);
+#pragma unroll
+          for (int j = 0; j < VPT; ++j) s += w[j];
+          s = wave_scan64(s);
+          if (lane == 63) part[e / (64 * VPT)] = s;
+        }
+      } else {
+        for (int e = e0 + tid * VPT; e - lane * VPT < p.V; e += VROW_PASS) {   // as long as the wave has entries
+          double w[VPT], s = 0.0;
+          wt.load(e, p.V, w);
+#pragma unroll
+          for (int j = 0; j < VPT; ++j) s += w[j];
+          s = wave_scan64(s);
+          if (lane == 63) part[e / (64 * VPT)] = s;
+        }
+      }
+    }
+    __syncthreads();
+    const int tiles = (p.V + 64 * VPT - 1) / (64 * VPT);
+    s0 = 2 * lane < tiles ? part[2 * lane] : 0.0;
+    s1 = 2 * lane + 1 < tiles ? part[2 * lane + 1] : 0.0;
+    const double upto_all = wave_scan64(s0 + s1);
+    upto = upto_all - (s0 + s1);
+    total = __shfl(upto_all, 63);
+  };
+  sums();
+  if (refused && !(total > 0.0)) {   // p <= q everywhere: draw from p itself
+    wt.qr = nullptr;
+    wt.drop = -1;
+    __syncthreads();
+    sums();
+  }
+  if (wave != 0) return;
+  int token = -1;
+  if (total > 0.0) {
+    const double u = (double)p.u[tok + p.K];
+    const double r = (u > 0.0 ? u : 0.0) * total;
+    const bool h0 = s0 > 0.0 && upto + s0 > r, h1 = s1 > 0.0 && upto + s0 + s1 > r;
+    const uint64_t hit = __ballot(h0 || h1), some = __ballot(s0 > 0.0 || s1 > 0.0);
+    const int src = hit ? (int)__builtin_ctzll(hit) : 63 - (int)__builtin_clzll(some);   // total > 0: some
+    const bool second = hit ? !h0 : s1 > 0.0;
+    const int e = (2 * src + (int)__shfl((int)second, src)) * 64 * VPT + lane * VPT;
+    const double start = __shfl(second ? upto + s0 : upto, src);
+    double w[VPT], s = 0.0;
+    wt.load(e, p.V, w);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s += w[j];
+    double c = start + (wave_scan64(s) - s);
+    int first = -1, last = -1;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (w[j] > 0.0) {
+        last = e + j;
+        c += w[j];
+        if (first < 0 && c > r) first = e + j;
+      }
+    const uint64_t f = __ballot(first >= 0), l = __ballot(last >= 0);
+    if (f) token = __shfl(first, (int)__builtin_ctzll(f));
+    else if (l) token = __shfl(last, 63 - (int)__builtin_clzll(l));
+  }
+  if (lane == 0) p.tokens[tok + a] = token;
+}
+
 template <typename T>
 static hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t s) {
+  if (a.V <= kVerifyRowMax) {
+    prof_begin(K_VERIFY_ROW, s);
+    hipLaunchKernelGGL((verify_row_kernel<T>), dim3(a.B), dim3(64 * VROW_WAVES), 0, s, a);
+    prof_end(K_VERIFY_ROW, s);
+    return hipGetLastError();
+  }
   prof_begin(K_VERIFY_SUM, s);
   if (a.tile == VSUB && (int64_t)a.tiles * a.B > 2048)   // 8 workgroups for each CU
     hipLaunchKernelGGL((verify_sum_kernel<T, 4>), dim3((a.tiles + 3) / 4, a.B), dim3(VT), 0, s, a);

@@ -376,7 +376,7 @@ gdn_status gdn_linear_step(const gdn_shape* shape, const void* q, const void* k,
  *                the number of its tokens whose state updates are to be kept,
  *                i.e. the replay_count of gdn_replay_state_updates.
  *  workspace     gdn_verify_workspace_bytes() bytes, 16-byte aligned, contents
- *                on entry ignored.
+ *                on entry ignored; may be NULL where that is 0.
  * K >= 0 (K = 0 is plain sampling), V >= 1; the probabilities need only the
  * alignment of their type.
  */

@@ -144,3 +144,48 @@ def test_row_offsets_past_32_bits():
     tokens, emit = gdn.gdn_verify_drafts(p, None, x, u)
     assert (emit == 16).all() and (tokens[:, 15] == V - 1).all() and (tokens[:, :15] == 3).all()
     assert np.prod(p.shape) > 2 ** 31
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [511, 512, 513, 8192, 32768, 40000, 65535, 65536, 65537, 70001])
+def test_around_the_sizes_that_change_the_path(dtype, V):
+    """One workgroup a row up to 65536 entries, two kernels beyond."""
+    need = gdn.load_library().gdn_verify_workspace_bytes(
+        gdn.ctypes.byref(gdn.gdn_verify_shape(5, 3, V, gdn._DTYPES[TYPES[dtype]], V, V)))
+    assert (need > 0) == (V > 65536)
+    check(*case(V, 5, 3, V, dtype))
+    check(*case(V + 1, 5, 3, V, dtype, onehot=True))
+
+
+def test_two_kernels_borders_rests_and_graph():
+    """The small cases above again where a row takes two kernels."""
+    V = 131072
+    p = torch.full((6, 2, V), 1.0 / V)
+    q = torch.zeros(6, 1, V)
+    q[:, :, 5] = 1.0
+    x = torch.full((6, 1), 5, dtype=torch.int32)
+    u = torch.zeros(6, 2)
+    u[:, 0] = 0.9
+    u[:, 1] = torch.tensor([0.0, 1.0 - 2.0 ** -24, 0.5, 0.25, 1.0 / (V - 1), 0.75])
+    tokens, _ = check(p, q, x, u, None)
+    assert tokens[0, 0] == 0 and tokens[1, 0] == V - 1
+    q = p[:, :1] * 2                                    # nothing is left of max(p - q, 0)
+    p[2] = 0.0
+    p[3, :, ::2] = float("nan")
+    check(p, q, x, u, None)
+    p, q, x, u, n = (t.to(DEV) for t in case(11, 7, 3, 70001, "f32"))
+    ws = torch.full((gdn.load_library().gdn_verify_workspace_bytes(
+        gdn.ctypes.byref(gdn.gdn_verify_shape(7, 3, 70001, 0, 70001, 70001))),), 255, dtype=torch.uint8, device=DEV)
+    tokens, emit = torch.zeros(7, 4, dtype=torch.int32, device=DEV), torch.zeros(7, dtype=torch.int32, device=DEV)
+    kw = dict(draft_count=n, tokens=tokens, emit_count=emit, workspace=ws)
+    gdn.gdn_verify_drafts(p, q, x, u, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_verify_drafts(p, q, x, u, **kw)
+    for _ in range(3):
+        u.copy_(torch.rand_like(u))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = tokens.clone(), emit.clone()
+        want = gdn.gdn_verify_drafts(p, q, x, u, draft_count=n)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

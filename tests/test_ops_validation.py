@@ -187,10 +187,11 @@ def test_verify_abi(lib):
     assert call(V=1 << 25, ps=1 << 25, qs=1 << 25) == uns
     assert call(p=NULL) == bad and call(x=NULL) == bad and call(t=NULL) == bad
     assert call(p=ctypes.c_void_p(0x10000002)) == bad and "aligned" in last(lib)
-    assert call(ws=NULL) == bad and call(wsb=8) == bad and "workspace" in last(lib)
+    long = dict(V=100000, ps=100000, qs=100000)
+    assert call(ws=NULL, **long) == bad and call(wsb=8, **long) == bad and "workspace" in last(lib)
     assert call(t=A[3]) == bad and "tokens overlaps uniforms" in last(lib)
     assert call(e=A[4]) == bad and "emit_count overlaps tokens" in last(lib)
-    assert call(ws=A[0]) == bad and "workspace overlaps target_probs" in last(lib)
+    assert call(ws=A[0], **long) == bad and "workspace overlaps target_probs" in last(lib)
 
 
 def test_norm_abi(lib):
