@@ -307,7 +307,7 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
  *
  * Precision: o is rounded once to the input dtype; for 16-bit inputs the
  * products with the state and with the in-chunk scores use those rounded to 16
- * bits, while the state itself is updated from unrounded terms (fp32).
+ * bits, while the final state is summed from terms of fp32 accuracy.
  *
  * Precondition of the prefill: g <= 0 (g = -infinity forgets everything before
  * the token).  The step takes g of any sign.

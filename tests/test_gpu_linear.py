@@ -14,6 +14,9 @@ values (the oracle's ``magnitudes``):
 * prefill, o: for 16-bit inputs the state and the scores are rounded once as
   operands, e A for both together, and o once, e |o|; all else as above plus the
   sum over dk and the decays' exponentials: (4 n + 80 + dk) 2^-24 A.
+Where the outputs have a pass of their own, its bf16 state is summed from two parts
+of the decayed v, 2^-16 A more: 1 / 256 of e A, which no sum of roundings of mixed
+signs comes near.
 fp16 values below its normal range are off by up to 2^-25 instead of e |o|.
 """
 
