@@ -293,13 +293,17 @@ __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
     part[0].lo = f32x4{x[0], x[1], x[2], x[3]};
     part[0].hi = f32x4{x[4], x[5], x[6], x[7]};
   } else {
+    typedef T T2 __attribute__((ext_vector_type(2)));   // pairs: one conversion instruction for two
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float r = x[j];
+    for (int j = 0; j < 8; j += 2) {
+      f32x2 r = {x[j], x[j + 1]};
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        part[n].v[j] = Elem<T>::from_f(r);
-        r -= Elem<T>::to_f(part[n].v[j]);
+        const T2 h = __builtin_convertvector(r, T2);
+        part[n].v[j] = h[0];
+        part[n].v[j + 1] = h[1];
+        r -= __builtin_convertvector(h, f32x2);
       }
     }
   }
@@ -668,13 +672,10 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
     }
     lds_barrier();
   };
-  if constexpr (DEEP) {
-    for (int c0 = t0; c0 < t1; c0 += 2 * C) {
-      chunk(c0, 0, xb, xa);
-      if (c0 + C < t1) chunk(c0 + C, 1, xa, xb);
-    }
-  } else {
-    for (int c0 = t0, par = 0; c0 < t1; c0 += C, par ^= 1) chunk(c0, par, xa, xa);
+  Set& other = DEEP ? xb : xa;
+  for (int c0 = t0; c0 < t1; c0 += 2 * C) {
+    chunk(c0, 0, other, xa);
+    if (c0 + C < t1) chunk(c0 + C, 1, xa, other);
   }
 
   if constexpr (STATE) {
