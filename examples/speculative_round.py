@@ -27,7 +27,7 @@ class Model:
 
         def w(*shape):
             return (torch.randn(*shape, generator=gen, device=device) * shape[0] ** -0.5).to(dtype)
-        self.V, self.Hq, self.Hv, self.dk, self.dv, self.D, self.dtype, self.device = V, Hq, Hv, dk, dv, D, dtype, device
+        self.V, self.Hq, self.Hv, self.D, self.device = V, Hq, Hv, D, device
         self.embedding = torch.randn(V, D, generator=gen, device=device).to(dtype)
         x = self.embedding                                      # one block: its inputs depend on the token alone
         self.q = (x @ w(D, Hq * dk)).view(V, Hq, dk)

@@ -44,7 +44,7 @@
 // there and -infinity needs no special case.
 //
 // What bounds it: 14286 ragged tokens x 32 heads, d = 128, bf16 take 62 us (state)
-// and 96 us (outputs), where a copy of the same bytes would take 40 and 75.  In
+// and 97 us (outputs), where a copy of the same bytes would take 40 and 75.  In
 // the output pass a 32-token chunk of a workgroup takes 5.6 k cycles, two
 // workgroups a CU: 0.6 k to issue the loads, 0.9 k scores, 0.6 k S^T Q, 1.3 k
 // update, 0.7 k V^T P^T and stores, 0.5 k staging, 0.8 k barriers.  VALU, MFMA and
@@ -82,7 +82,8 @@ __device__ __forceinline__ float max_all(float x) {   // over the wave, x >= 0
 
 __device__ __forceinline__ double lane64(double x, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
@@ -285,7 +286,8 @@ __device__ __forceinline__ float frag_get(const Frag<T>& f, int i) {
 // Parts of the decayed v of a fragment: one fp32; bf16 three, or two where only
 // outputs follow; fp16 two.
 enum class Pass { kState, kOut, kWhole };   // segment states; outputs from given states; both (no segments)
-template <typename T, Pass P> constexpr int kParts = sizeof(T) == 4 ? 1 : (__is_same(T, __bf16) && P != Pass::kOut ? 3 : 2);
+template <typename T, Pass P>
+constexpr int kParts = sizeof(T) == 4 ? 1 : (__is_same(T, __bf16) && P != Pass::kOut ? 3 : 2);
 
 template <typename T, int N>
 __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
@@ -424,7 +426,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
   struct Set {
     uint4 k[NKL], q[STATE ? 1 : NKL], v[NVL];
   };
-    constexpr bool DEEP = !STATE && 2 * NKL + NVL <= 8;   // the state pass: slower with it (74 us against 62)
+  constexpr bool DEEP = !STATE && 2 * NKL + NVL <= 8;   // the state pass: slower with it (74 us against 62)
   const uint32_t krow_b = (uint32_t)(krow * sizeof(T)), vrow_b = (uint32_t)(vrow * sizeof(T));
   const uint32_t koff = (uint32_t)(tid / KP) * krow_b, voff = (uint32_t)(tid / VP) * vrow_b;
   auto piece = [](const T* base, uint32_t off) {
@@ -562,7 +564,8 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         Frag<T> sf[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          f32x4 lo = S[DK >= 32 ? 2 * b : 0][n], hi = DK >= 32 ? S[DK >= 32 ? 2 * b + 1 : 0][n] : f32x4{0.f, 0.f, 0.f, 0.f};
+          f32x4 lo = S[DK >= 32 ? 2 * b : 0][n], hi = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (DK >= 32) hi = S[2 * b + 1][n];
           if constexpr (__is_same(T, _Float16)) {
             lo *= up;
             hi *= up;
@@ -723,7 +726,9 @@ static hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
 template <typename T, int DK, int DV>
 static hipError_t launch_d(const LinearArgs& a, hipStream_t s) {
   if constexpr (DV >= 64) {
-    if ((int64_t)a.max_segs * a.Hv <= (sizeof(T) == 4 ? 512 : 256)) return launch_tiles<T, DK, DV / 32, 1, sizeof(T) == 2 ? 64 : 32>(a, s);
+    constexpr int COUT = sizeof(T) == 2 ? 64 : 32;
+    if ((int64_t)a.max_segs * a.Hv <= (sizeof(T) == 4 ? 512 : 256))
+      return launch_tiles<T, DK, DV / 32, 1, COUT>(a, s);
   }
   constexpr int NT = sizeof(T) == 2 && DV >= 64 ? 2 : 1;
   return launch_tiles<T, DK, DV / 16, NT, 32>(a, s);

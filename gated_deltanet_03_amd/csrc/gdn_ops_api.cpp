@@ -287,7 +287,8 @@ gdn_status gdn_verify_drafts(const gdn_verify_shape* sh, const void* p, const vo
 gdn_status gdn_block_norm(const gdn_norm_shape* sh, const void* y, const void* gate, const void* res,
                           const void* wpost, const void* wnext, void* h, void* normed, void* stream) {
   if (sh == nullptr) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
-  if (sh->T < 0 || sh->D < 1) return fail(GDN_ERR_INVALID_ARG, "T=%lld must be >= 0 and D=%d >= 1", (long long)sh->T, sh->D);
+  if (sh->T < 0 || sh->D < 1)
+    return fail(GDN_ERR_INVALID_ARG, "T=%lld must be >= 0 and D=%d >= 1", (long long)sh->T, sh->D);
   if (sh->dtype != GDN_F32 && sh->dtype != GDN_F16 && sh->dtype != GDN_BF16)
     return fail(GDN_ERR_INVALID_ARG, "dtype %d is not a gdn_dtype", sh->dtype);
   if (sh->gate_act < GDN_ACT_NONE || sh->gate_act > GDN_ACT_SIGMOID)

@@ -2,13 +2,16 @@
 //
 // Up to 65536 entries one kernel, a workgroup a row (verify_row): tiles of one
 // wave's 512 entries are summed, the tile that holds u * sum(w) is found among the
-// at most 128 sums and scanned by one wave.  Beyond, two kernels.  verify_sum: one workgroup per (tile of the vocabulary, row)
-// finds how many drafts the row accepts (a gather of at most K pairs), then sums
-// the tile's weights w = max(p_a - q_a, 0) (or p_a) in 64 bits.  verify_draw:
-// one workgroup per row scans the tiles' sums, finds the tile that holds
-// u * sum(w), and scans that tile alone.  Only one row of p and one of q are
-// read; the second kernel re-reads one tile from the cache.  Bound by memory for
-// a batch, by the latency of two launches for one row.
+// at most 128 sums and scanned by one wave.
+//
+// Beyond, two kernels.  verify_sum: one workgroup per (tiles of the vocabulary,
+// row) finds how many drafts the row accepts (a gather of at most K pairs), then
+// sums the tiles' weights w = max(p_a - q_a, 0) (or p_a).  verify_draw: one
+// workgroup per row scans the tiles' sums, finds the tile that holds u * sum(w),
+// and scans that tile alone.
+//
+// Only one row of p and one of q are read; one tile is read again, from the
+// cache.  Bound by memory for a batch, by the call's host time for one row.
 //
 // Sums in 64 bits: a vocabulary of 10^5 entries puts the borders between tokens
 // 10^-5 apart, and sums in 32 bits, whose order depends on the split, would
