@@ -20,7 +20,8 @@
 //     operands are contiguous 16-byte reads);
 //   * the scores come out as P^T = K Q^T, in the form of an operand of V^T P^T;
 //     each wave computes some tiles and hands them to the others through LDS in
-//     fragment order;
+//     fragment order and fp32 (for fp16 they are brought into its range by a power
+//     of two a query when they are read: q . k alone may be far outside of it);
 //   * o^T is accumulated, so a lane holds adjacent columns of one token and
 //     writes them with one access;
 //   * K^T and V operands (contraction over tokens) come from transpose reads of
@@ -69,15 +70,19 @@ __device__ __forceinline__ s16x4 lds_read_tr(const void* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
+__device__ __forceinline__ float max_groups(float x) {   // over the lanes of equal lane % 16, x >= 0
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 __device__ __forceinline__ float max_all(float x) {   // over the wave, x >= 0
   x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0xb1, 0xf, 0xf, false));    // lane ^ 1
   x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x4e, 0xf, 0xf, false));    // lane ^ 2
   x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x141, 0xf, 0xf, false));   // the other four of 8
   x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x140, 0xf, 0xf, false));   // the other eight of 16
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return max_groups(x);
 }
 
 __device__ __forceinline__ double lane64(double x, int lane) {
@@ -171,8 +176,11 @@ struct Decays {
   __align__(16) float lo[O];
   __align__(16) float eg[O];             // e^{G_i}
   __align__(16) float row[O];            // e^{G_i - G_s}, s the last token before i's tile
-  __align__(16) float col[STATE ? 1 : RT - 1][O];   // [t - 1][j] = e^{G_{16t-1} - G_j}, j < 16t
+  __align__(16) float col[STATE ? 4 : 8 * RT * (RT - 1)];   // at col_at(t) + j: e^{G_{16t-1} - G_j}, j < 16t
 };
+
+// First of the 16t column factors of query tile t >= 1.
+__device__ __forceinline__ constexpr int col_at(int t) { return 8 * t * (t - 1); }
 
 // One wave: the decays of a chunk from lane i's log decay (0 past the end);
 // returns their sum.
@@ -190,7 +198,7 @@ __device__ __forceinline__ double fill_decays(float g, Decays<C, STATE>& d) {
     for (int t = 1; t < RT; ++t) {
       const double at = lane64(x, 16 * t - 1);
       if (lane >= 16 * t) start = at;
-      if (lane < 16 * t) d.col[t - 1][lane] = __expf((float)(at - x));
+      if (lane < 16 * t) d.col[col_at(t) + lane] = __expf((float)(at - x));
     }
     if (lane < C) {
       const float hi = rintf((float)x * 64.f) * 0.015625f;
@@ -228,7 +236,7 @@ struct Smem {
   __align__(16) T k[C * Tile<T, DK>::STRIDE];
   __align__(16) T v[C * Tile<T, CW>::STRIDE];
   __align__(16) T q[STATE ? 8 : C * Tile<T, DK>::STRIDE];
-  __align__(16) T p[STATE ? 8 : p_frag(C / 16, 0) * 512];
+  __align__(16) float p[STATE ? 4 : p_frag(C / 16, 0) * 512];
   Decays<C, STATE> d[2];
 };
 
@@ -524,7 +532,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         // lane holds (key 16j + 4g + e, query 16i + i16)
         if (j < i) {
           const float row = D.row[16 * i + i16];
-          const f32x4 col = *reinterpret_cast<const f32x4*>(&D.col[i - 1][16 * j + 4 * g4]);
+          const f32x4 col = *reinterpret_cast<const f32x4*>(&D.col[col_at(i) + 16 * j + 4 * g4]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) pt[e] *= row * col[e];
         } else {
@@ -538,9 +546,9 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
           }
         }
         // half a fragment; the last row tile's other half is 0
-        T* half = &sm.p[p_frag(i, j >> 1) * 512 + lane * 8 + 4 * (j & 1)];
-        store4<T>(half, pt[0], pt[1], pt[2], pt[3]);
-        if (j == i && (j & 1) == 0) store4<T>(half + 4, 0.f, 0.f, 0.f, 0.f);
+        float* half = &sm.p[p_frag(i, j >> 1) * 512 + 256 * (j & 1) + lane * 4];
+        *reinterpret_cast<f32x4*>(half) = pt;
+        if (j == i && (j & 1) == 0) *reinterpret_cast<f32x4*>(half + 256) = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       // the state's part of o; fp16 operands scaled by a power of two into its range
       int sh = 0;
@@ -651,12 +659,35 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
       T* orow = static_cast<T*>(p.o) + ((size_t)c0 + i16) * vrow + (size_t)h * p.dv + slice * CW;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
+        f32x4 pt[NTB][2];
+#pragma unroll
+        for (int b = 0; b <= i / 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            pt[b][e] = *reinterpret_cast<const f32x4*>(&sm.p[p_frag(i, b) * 512 + 256 * e + lane * 4]);
+        // fp16: each query's scores are brought into range by a power of two
+        float up = 1.f, down = 1.f;
+        if constexpr (__is_same(T, _Float16)) {
+          float m = 0.f;
+#pragma unroll
+          for (int b = 0; b <= i / 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(pt[b][0][e]), fabsf(pt[b][1][e])));
+          const int sh = shift_for(max_groups(m));
+          up = ldexpf(1.f, sh);
+          down = ldexpf(1.f, -sh);
+        }
+        f32x4 pv[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) pv[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b <= i / 2; ++b) {
-          const Frag<T> pf = load_frag_native<T>(&sm.p[p_frag(i, b) * 512 + lane * 8]);
+          const Frag<T> pf = make_frag<T>(up * pt[b][0], up * pt[b][1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<T>(acc[i][n], vf[b][n], pf);
+          for (int n = 0; n < NT; ++n) mma<T>(pv[n], vf[b][n], pf);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[i][n] += down * pv[n];
         // lane holds token 16i + i16, columns state_col(4g..4g+3) of each tile
         if (16 * i + i16 < len) {
           T* at = orow + (size_t)(16 * i) * vrow;

@@ -1,0 +1,81 @@
+"""Linear attention with inputs of any size: scores, values and states outside of a
+16-bit type's range, columns of very different sizes, values that are no numbers.
+
+The bounds are those of test_gpu_linear.py (e half a step of the type relative to the
+value, A the same sums over absolute values): o is off by e |o| + e A for the operands
+plus the fp32 sums' (4 n + 80 + dk) 2^-24 A, the state by (4 n + 80) 2^-24 A.
+"""
+
+import pytest
+import torch
+
+from test_gpu_linear import DEV, E, TYPES, U, close, make, prefill
+import gated_deltanet_03_amd as gdn
+
+pytestmark = pytest.mark.gpu
+
+# Heads and lengths that take the three passes: one without segments, with half the columns a
+# workgroup and with all of them, and both of the split form.
+SHAPES = [([40, 20, 1, 60], 2, 4, 64, 64), ([64, 30, 33], 1, 88, 128, 128), ([257, 1, 130, 64], 2, 128, 64, 128),
+          ([1500], 1, 2, 128, 128), ([700, 33], 2, 40, 64, 128)]
+
+
+def oracle(c):
+    """The definition in 64 bits, token by token over all sequences: o, final and the same over absolute values."""
+    d = {x: c[x].to(DEV).double() for x in ("q", "k", "v", "g")}
+    cu, Hv = c["cu"].tolist(), c["Hv"]
+    rep, N = Hv // c["Hq"], len(c["cu"]) - 1
+    dk, dv, T = d["q"].shape[-1], d["v"].shape[-1], d["v"].shape[0]
+    got = []
+    for f in (lambda x: x, torch.abs):
+        q, k, v = f(d["q"]).repeat_interleave(rep, 1), f(d["k"]).repeat_interleave(rep, 1), f(d["v"])
+        a = d["g"].expand(T, Hv).exp()
+        S = torch.zeros(N, Hv, dk, dv, dtype=torch.float64, device=DEV)
+        if c["s0"] is not None:
+            S += f(c["s0"].to(DEV).double())
+        o = torch.zeros(T, Hv, dv, dtype=torch.float64, device=DEV)
+        for t in range(max(cu[i + 1] - cu[i] for i in range(N))):
+            live = [i for i in range(N) if cu[i] + t < cu[i + 1]]
+            at = torch.tensor([cu[i] + t for i in live], device=DEV)
+            i = torch.tensor(live, device=DEV)
+            S[i] = a[at][:, :, None, None] * S[i] + k[at][..., None] * v[at][:, :, None, :]
+            o[at] = f(torch.tensor(c["scale"], dtype=torch.float64, device=DEV)) * (q[at][..., None] * S[i]).sum(-2)
+        got += [o.cpu().numpy(), S.cpu().numpy()]
+    return got
+
+
+def check(o, final, c, segs=0):
+    ref, fin, mag, fmag = oracle(c)
+    e, dk = E[o.dtype], c["q"].shape[-1]
+    n = 4 * (int(c["cu"].diff().max()) // 32 + 1 + segs) + 80
+    close(o, ref, e * abs(ref) + (0 if e == U else e) * mag + (n + dk) * U * mag, "o")
+    close(final, fin, n * U * fmag, "final")
+
+
+@pytest.mark.parametrize("lengths,Hq,Hv,dk,dv", SHAPES)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size,scale", [(300.0, 1e-6), (30.0, 1e-3), (1e-3, 1e4), (1e-4, 1e6)])
+def test_scores_out_of_fp16_range(dtype, size, scale, lengths, Hq, Hv, dk, dv):
+    """|q . k| up to 10^6 .. 10^7 (aligned keys) and down to 10^-7, with o in range."""
+    c = make(61, lengths, Hq, Hv, dk, dv, dtype, state=False, memory=0.05)
+    g = torch.Generator().manual_seed(62)
+    base = torch.randn(1, Hq, dk, generator=g)
+    for x in "qk":       # one direction and noise
+        c[x] = (size * (base + 0.3 * torch.randn(sum(lengths), Hq, dk, generator=g))).to(TYPES[dtype])
+    c["v"] = (0.1 * c["v"].float()).to(TYPES[dtype])
+    c["scale"] = scale
+    o, fin = prefill(c)
+    assert torch.isfinite(o).all() and torch.isfinite(fin).all()
+    check(o, fin, c, segs=20)
+
+
+def test_equal_large_keys_agree_with_the_step():
+    T, d = 40, 128
+    q = torch.full((T, 1, d), 23.0, dtype=torch.float16, device=DEV)     # q . k = 67712
+    v = torch.full((T, 1, d), 0.1, dtype=torch.float16, device=DEV)
+    g = torch.full((1,), -20.0, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    o, fin = gdn.gdn_linear_prefill(q, q, v, g, cu_seqlens=cu)
+    os, fs, _ = gdn.gdn_linear_step(q, q, v, g, cu_seqlens=cu)
+    assert ((o.float() - os.float()).abs() <= 4 * E[torch.float16] * os.float().abs()).all()
+    assert ((fin - fs).abs() <= 1e-5 * fs.abs()).all()
