@@ -32,9 +32,11 @@
 //
 // The state's update uses e^{G_C - G_j} v_j split into parts of the input type
 // (three for bf16, two scaled ones for fp16), so the carried state keeps fp32
-// accuracy; the state and the scores are rounded to 16 bits where they are
-// operands of o.  kOut's own walk, which ends in no final state, takes two bf16
-// parts (2^-16 of a term, far below the operands' 2^-8).
+// accuracy.  The state and the scores are two parts each where they are operands of
+// o (2^-16 of a term for bf16, 2^-22 for fp16: o is rounded once, at its end; one
+// part each made its error 1.4 times that rounding and took 155 us instead of 178
+// on the 14286 tokens below).  kOut's own walk, which ends in no final state, takes
+// two bf16 parts of the decayed v (2^-16 again).
 //
 // Log decays are summed in 64 bits.  A decay between two tokens of one 16-token
 // tile is the exponential of a difference of coarse parts (multiples of 1/64,
@@ -297,6 +299,10 @@ enum class Pass { kState, kOut, kWhole };   // segment states; outputs from give
 template <typename T, Pass P>
 constexpr int kParts = sizeof(T) == 4 ? 1 : (__is_same(T, __bf16) && P != Pass::kOut ? 3 : 2);
 
+// Parts of the state and of the scores as operands of o.
+template <typename T>
+constexpr int kOperandParts = sizeof(T) == 4 ? 1 : 2;
+
 template <typename T, int N>
 __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
   if constexpr (sizeof(T) == 4) {
@@ -319,6 +325,12 @@ __device__ __forceinline__ void split(const float* x, Frag<T>* part) {
   }
 }
 
+template <typename T, int N>
+__device__ __forceinline__ void split(const f32x4& lo, const f32x4& hi, Frag<T>* part) {
+  const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  split<T, N>(x, part);
+}
+
 template <typename T, int C, int DK, int NT, int NW, Pass PASS>
 __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) {
   constexpr bool STATE = PASS == Pass::kState;
@@ -332,7 +344,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
   constexpr int NKL = (C * KP + THREADS - 1) / THREADS, NVL = (C * VP + THREADS - 1) / THREADS;
   constexpr int KR = THREADS / KP, VR = THREADS / VP;         // rows between a thread's pieces
   static_assert(THREADS % KP == 0 && THREADS % VP == 0, "");
-  constexpr int NP = kParts<T, PASS>;
+  constexpr int NP = kParts<T, PASS>, OP = kOperandParts<T>;
   __shared__ SM sm;
 
   // XCD-aware order: the workgroups that share one segment's keys get ids equal mod 8
@@ -569,7 +581,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         for (int n = 0; n < NT; ++n) acc[i][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int b = 0; b < NKB; ++b) {
-        Frag<T> sf[NT];
+        Frag<T> sf[NT][OP];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           f32x4 lo = S[DK >= 32 ? 2 * b : 0][n], hi = {0.f, 0.f, 0.f, 0.f};
@@ -578,16 +590,18 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
             lo *= up;
             hi *= up;
           }
-          sf[n] = make_frag<T>(lo, hi);
+          split<T, OP>(lo, hi, sf[n]);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const Frag<T> qf = row_frag<T, DK>(sm.q, i, b);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if constexpr (DK >= 32) mma<T>(acc[i][n], sf[n], qf);
-            else mma_lo<T>(acc[i][n], sf[n], qf);
-          }
+          for (int q = 0; q < OP; ++q)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (DK >= 32) mma<T>(acc[i][n], sf[n][q], qf);
+              else mma_lo<T>(acc[i][n], sf[n][q], qf);
+            }
         }
       }
 #pragma unroll
@@ -682,9 +696,12 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         for (int n = 0; n < NT; ++n) pv[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b <= i / 2; ++b) {
-          const Frag<T> pf = make_frag<T>(up * pt[b][0], up * pt[b][1]);
+          Frag<T> pf[OP];
+          split<T, OP>(up * pt[b][0], up * pt[b][1], pf);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma<T>(pv[n], vf[b][n], pf);
+          for (int q = 0; q < OP; ++q)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma<T>(pv[n], vf[b][n], pf[q]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[i][n] += down * pv[n];

@@ -306,8 +306,9 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
  * or 0 for one value per value head ([Hv], the same at every token).
  *
  * Precision: o is rounded once to the input dtype; for 16-bit inputs the
- * products with the state and with the in-chunk scores use those rounded to 16
- * bits, while the final state is summed from terms of fp32 accuracy.
+ * products with the state and with the in-chunk scores use those in two parts of
+ * the input type (2^-16 of a term for bf16, 2^-22 for fp16), and the final state is
+ * summed from terms of fp32 accuracy.
  *
  * Precondition of the prefill: g <= 0 (g = -infinity forgets everything before
  * the token).  The step takes g of any sign.

@@ -1,9 +1,10 @@
 """Linear attention with inputs of any size: scores, values and states outside of a
 16-bit type's range, columns of very different sizes, values that are no numbers.
 
-The bounds are those of test_gpu_linear.py (e half a step of the type relative to the
-value, A the same sums over absolute values): o is off by e |o| + e A for the operands
-plus the fp32 sums' (4 n + 80 + dk) 2^-24 A, the state by (4 n + 80) 2^-24 A.
+Where a test derives no bound of its own, they are those of test_gpu_linear.py (e half a
+step of the type relative to the value, A the same sums over absolute values): o is off
+by e |o| + e A for the operands plus the fp32 sums' (4 n + 80 + dk) 2^-24 A, the state by
+(4 n + 80) 2^-24 A.
 """
 
 import pytest
@@ -79,3 +80,18 @@ def test_equal_large_keys_agree_with_the_step():
     os, fs, _ = gdn.gdn_linear_step(q, q, v, g, cu_seqlens=cu)
     assert ((o.float() - os.float()).abs() <= 4 * E[torch.float16] * os.float().abs()).all()
     assert ((fin - fs).abs() <= 1e-5 * fs.abs()).all()
+
+
+@pytest.mark.parametrize("lengths,Hq,Hv,dk,dv", SHAPES + [([600, 40], 1, 3, 16, 16)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_outputs_are_rounded_once(dtype, lengths, Hq, Hv, dk, dv):
+    """The state and the scores enter o in two parts of the input type, each with what the part
+    before it left: off by (2 e^2) A together, where the state of the output pass itself is summed
+    from two parts of the decayed v, e^2 A more; fp16 also by its smallest step, 2^-25 where the
+    largest of a column or query is at least 2^13: 2 times 2^-38 of A's largest, dk or 64 of them."""
+    c = make(63, lengths, Hq, Hv, dk, dv, dtype, memory=0.05)
+    o, fin = prefill(c)
+    ref, _, mag, _ = oracle(c)
+    e = E[o.dtype]
+    n = 4 * (max(lengths) // 32 + 21) + 80 + dk
+    close(o, ref, e * abs(ref) + (3 * e * e + n * U + (dk + 64) * 2.0 ** -38) * mag, "o")
