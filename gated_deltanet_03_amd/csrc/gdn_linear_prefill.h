@@ -31,12 +31,13 @@
 // after it, V^T P^T on registers once the next tiles are stored.
 //
 // The state's update uses e^{G_C - G_j} v_j split into parts of the input type
-// (three for bf16, two scaled ones for fp16), so the carried state keeps fp32
-// accuracy.  The state and the scores are two parts each where they are operands of
-// o (2^-16 of a term for bf16, 2^-22 for fp16: o is rounded once, at its end; one
-// part each made its error 1.4 times that rounding and took 155 us instead of 178
-// on the 14286 tokens below).  kOut's own walk, which ends in no final state, takes
-// two bf16 parts of the decayed v (2^-16 again).
+// (three for bf16, two for fp16), so the carried state keeps fp32 accuracy.  The
+// state and the scores are two parts each where they are operands of o (2^-16 of a
+// term for bf16, 2^-22 for fp16: o is rounded once, at its end; one part each made
+// its error 1.4 times that rounding and took 155 us instead of 178 on the 14286
+// tokens below).  kOut's own walk, which ends in no final state, takes two bf16
+// parts of the decayed v (2^-16 again).  For fp16 a power of two brings each column
+// of these operands into its range, so that no column depends on its neighbours.
 //
 // Log decays are summed in 64 bits.  A decay between two tokens of one 16-token
 // tile is the exponential of a difference of coarse parts (multiples of 1/64,
@@ -79,14 +80,6 @@ __device__ __forceinline__ float max_groups(float x) {   // over the lanes of eq
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-__device__ __forceinline__ float max_all(float x) {   // over the wave, x >= 0
-  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0xb1, 0xf, 0xf, false));    // lane ^ 1
-  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x4e, 0xf, 0xf, false));    // lane ^ 2
-  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x141, 0xf, 0xf, false));   // the other four of 8
-  x = fmaxf(x, __builtin_amdgcn_update_dpp(0.f, x, 0x140, 0xf, 0xf, false));   // the other eight of 16
-  return max_groups(x);
-}
-
 __device__ __forceinline__ double lane64(double x, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, x);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
@@ -99,6 +92,10 @@ __device__ __forceinline__ int shift_for(float m) {
   if (!(m > 0.f) || m > 3.0e38f) return 0;
   const int e = 14 - ilogbf(m);
   return e < -100 ? -100 : (e > 100 ? 100 : e);
+}
+
+__device__ __forceinline__ f32x4 shifted(const f32x4& x, int sh) {   // x * 2^sh
+  return f32x4{ldexpf(x[0], sh), ldexpf(x[1], sh), ldexpf(x[2], sh), ldexpf(x[3], sh)};
 }
 
 // Segment `seg`: its sequence and tokens, its number in the sequence and whether
@@ -562,19 +559,19 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         *reinterpret_cast<f32x4*>(half) = pt;
         if (j == i && (j & 1) == 0) *reinterpret_cast<f32x4*>(half + 256) = f32x4{0.f, 0.f, 0.f, 0.f};
       }
-      // the state's part of o; fp16 operands scaled by a power of two into its range
-      int sh = 0;
+      // the state's part of o; fp16: each column is brought into range by a power of two
+      int sh[NT];
       if constexpr (__is_same(T, _Float16)) {
-        float m = 0.f;
 #pragma unroll
-        for (int t = 0; t < NST; ++t)
+        for (int n = 0; n < NT; ++n) {
+          float m = 0.f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int t = 0; t < NST; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(S[t][n][e]));
-        sh = shift_for(max_all(m));
+          sh[n] = shift_for(max_groups(m));
+        }
       }
-      const float up = ldexpf(1.f, sh), down = ldexpf(1.f, -sh);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -587,8 +584,8 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
           f32x4 lo = S[DK >= 32 ? 2 * b : 0][n], hi = {0.f, 0.f, 0.f, 0.f};
           if constexpr (DK >= 32) hi = S[2 * b + 1][n];
           if constexpr (__is_same(T, _Float16)) {
-            lo *= up;
-            hi *= up;
+            lo = shifted(lo, sh[n]);
+            hi = shifted(hi, sh[n]);
           }
           split<T, OP>(lo, hi, sf[n]);
         }
@@ -605,17 +602,21 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         }
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const float eg = D.eg[16 * i + i16] * down;
+      for (int n = 0; n < NT; ++n) {
+        f32x4 down = {1.f, 1.f, 1.f, 1.f};   // a lane's outputs are columns 4g.. of a tile
+        if constexpr (__is_same(T, _Float16)) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[i][n] *= eg;
+          for (int e = 0; e < 4; ++e) down[e] = ldexpf(1.f, -__shfl(sh[n], 4 * g4 + e));
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i][n] *= D.eg[16 * i + i16] * down;
       }
     }
 
     // S = gamma S + K^T (w v)
     if (STATE || more || PASS == Pass::kWhole) {
       float x[NTB][NT][8];
-      float m = 0.f;
+      float m[NT] = {};   // fp16: each column is brought into range by a power of two
 #pragma unroll
       for (int b = 0; b < NTB; ++b) {
         const f32x4 w0 = *reinterpret_cast<const f32x4*>(&D.w[32 * b + 4 * g4]);
@@ -625,20 +626,20 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             x[b][n][j] = (j < 4 ? w0[j & 3] : w1[j & 3]) * frag_get<T>(vf[b][n], j);
-            m = fmaxf(m, fabsf(x[b][n][j]));
+            if constexpr (__is_same(T, _Float16)) m[n] = fmaxf(m[n], fabsf(x[b][n][j]));
           }
       }
-      float up = 1.f, down = 1.f;
-      if constexpr (__is_same(T, _Float16)) {
-        const int sh = shift_for(max_all(m));
-        up = ldexpf(1.f, sh);
-        down = ldexpf(1.f, -sh);
+      int sh[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float gamma = D.gamma[0];
+        if constexpr (__is_same(T, _Float16)) {
+          sh[n] = shift_for(max_groups(m[n]));
+          gamma = ldexpf(gamma, sh[n]);
+        }
+#pragma unroll
+        for (int t = 0; t < NST; ++t) S[t][n] *= gamma;
       }
-      const float gamma = D.gamma[0] * up;
-#pragma unroll
-      for (int t = 0; t < NST; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) S[t][n] *= gamma;
 #pragma unroll
       for (int b = 0; b < NTB; ++b) {
         Frag<T> part[NT][NP];
@@ -646,7 +647,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         for (int n = 0; n < NT; ++n) {
           if constexpr (__is_same(T, _Float16)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[b][n][j] *= up;
+            for (int j = 0; j < 8; ++j) x[b][n][j] = ldexpf(x[b][n][j], sh[n]);
           }
           split<T, NP>(x[b][n], part[n]);
         }
@@ -663,7 +664,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
 #pragma unroll
         for (int t = 0; t < NST; ++t)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) S[t][n] *= down;
+          for (int n = 0; n < NT; ++n) S[t][n] = shifted(S[t][n], -sh[n]);
       }
     }
     lds_barrier();   // the tiles are read, P is written
@@ -680,16 +681,14 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
           for (int e = 0; e < 2; ++e)
             pt[b][e] = *reinterpret_cast<const f32x4*>(&sm.p[p_frag(i, b) * 512 + 256 * e + lane * 4]);
         // fp16: each query's scores are brought into range by a power of two
-        float up = 1.f, down = 1.f;
+        int sh = 0;
         if constexpr (__is_same(T, _Float16)) {
           float m = 0.f;
 #pragma unroll
           for (int b = 0; b <= i / 2; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(pt[b][0][e]), fabsf(pt[b][1][e])));
-          const int sh = shift_for(max_groups(m));
-          up = ldexpf(1.f, sh);
-          down = ldexpf(1.f, -sh);
+          sh = shift_for(max_groups(m));
         }
         f32x4 pv[NT];
 #pragma unroll
@@ -697,14 +696,15 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
 #pragma unroll
         for (int b = 0; b <= i / 2; ++b) {
           Frag<T> pf[OP];
-          split<T, OP>(up * pt[b][0], up * pt[b][1], pf);
+          if constexpr (__is_same(T, _Float16)) split<T, OP>(shifted(pt[b][0], sh), shifted(pt[b][1], sh), pf);
+          else split<T, OP>(pt[b][0], pt[b][1], pf);
 #pragma unroll
           for (int q = 0; q < OP; ++q)
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma<T>(pv[n], vf[b][n], pf[q]);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[i][n] += down * pv[n];
+        for (int n = 0; n < NT; ++n) acc[i][n] += __is_same(T, _Float16) ? shifted(pv[n], -sh) : pv[n];
         // lane holds token 16i + i16, columns state_col(4g..4g+3) of each tile
         if (16 * i + i16 < len) {
           T* at = orow + (size_t)(16 * i) * vrow;

@@ -308,7 +308,8 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
  * Precision: o is rounded once to the input dtype; for 16-bit inputs the
  * products with the state and with the in-chunk scores use those in two parts of
  * the input type (2^-16 of a term for bf16, 2^-22 for fp16), and the final state is
- * summed from terms of fp32 accuracy.
+ * summed from terms of fp32 accuracy (fp16: of 2^-22, but no finer than 2^-38 of the
+ * largest decayed v of the same column in the same chunk).
  *
  * Precondition of the prefill: g <= 0 (g = -infinity forgets everything before
  * the token).  The step takes g of any sign.

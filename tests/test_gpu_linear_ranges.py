@@ -95,3 +95,24 @@ def test_outputs_are_rounded_once(dtype, lengths, Hq, Hv, dk, dv):
     e = E[o.dtype]
     n = 4 * (max(lengths) // 32 + 21) + 80 + dk
     close(o, ref, e * abs(ref) + (3 * e * e + n * U + (dk + 64) * 2.0 ** -38) * mag, "o")
+
+
+@pytest.mark.parametrize("lengths,Hq,Hv,dk,dv", SHAPES + [([600, 40], 1, 3, 16, 16)])
+def test_fp16_columns_of_different_sizes(lengths, Hq, Hv, dk, dv):
+    """A column of v or of the state keeps its accuracy whatever stands beside it."""
+    c = make(65, lengths, Hq, Hv, dk, dv, "f16", memory=0.05)
+    for x in ("v", "s0"):
+        c[x] = c[x].float()
+        c[x][..., ::2] *= 100.0
+        c[x][..., 1::2] *= 1e-5
+    c["v"] = c["v"].half()
+    o, fin = prefill(c)
+    check(o, fin, c, segs=20)
+    c["v"][..., 1::2] *= 1e5
+    c["s0"][..., 1::2] *= 1e5
+    c["s0"][..., ::2] *= 1e12          # these columns of o are beyond fp16
+    o, fin = prefill(c)
+    ref, want, mag, fmag = oracle(c)
+    e, n = E[torch.float16], 4 * (max(lengths) // 32 + 21) + 80
+    close(o[..., 1::2], ref[..., 1::2], (e * (abs(ref) + mag) + (n + dk) * U * mag)[..., 1::2], "o")
+    close(fin, want, n * U * fmag, "final")
