@@ -328,8 +328,24 @@ __device__ __forceinline__ void split(const f32x4& lo, const f32x4& hi, Frag<T>*
   split<T, N>(x, part);
 }
 
+// A fragment of f(index) in each slot.
+template <typename T, typename F>
+__device__ __forceinline__ Frag<T> make_slots(F f) {
+  Frag<T> y;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = f(j);
+    if constexpr (sizeof(T) == 2) y.v[j] = Elem<T>::from_f(v);
+    else if (j < 4) y.lo[j & 3] = v;
+    else y.hi[j & 3] = v;
+  }
+  return y;
+}
+
+// Two waves a SIMD; one for the narrow output pass with few workgroups (at most two of two
+// waves a CU), which keeps a 64-token chunk on its way in 72 registers.
 template <typename T, int C, int DK, int NT, int NW, Pass PASS>
-__global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) {
+__global__ __launch_bounds__(64 * NW, (PASS == Pass::kOut && C == 64 && NW <= 2 ? 1 : 2)) void linear_chunk_kernel(LinearArgs p) {
   constexpr bool STATE = PASS == Pass::kState;
   using SM = Smem<T, C, DK, NT, NW, STATE>;
   constexpr int CW = SM::CW, THREADS = 64 * NW;
@@ -670,6 +686,35 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
     lds_barrier();   // the tiles are read, P is written
     if (more) stage(c0 + C, next);
 
+    // V^T P^T runs over whole blocks of 32 tokens with P = 0 after the query: 0 times an
+    // infinity or a NaN would carry it back to the queries before it.  Such values (rare;
+    // found by a product with 0) are taken out of V here, and what they reach is set to NaN
+    // below.
+    uint64_t lost = 0;
+    uint32_t lost_v[NTB][NT];   // bit j: slot j of this lane
+    if constexpr (!STATE) {
+      f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int b = 0; b < NTB; ++b)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma<T>(zero, vf[b][n], zero_frag<T>());
+      lost = __ballot(zero[0] + zero[1] + zero[2] + zero[3] != 0.f);
+      if (__builtin_expect(lost != 0, 0)) {
+#pragma unroll
+        for (int b = 0; b < NTB; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            lost_v[b][n] = 0;
+            const Frag<T> raw = vf[b][n];
+            vf[b][n] = make_slots<T>([&](int j) {
+              const float x = frag_get<T>(raw, j);
+              const bool fine = fabsf(x) < __builtin_inff();
+              lost_v[b][n] |= (fine ? 0u : 1u) << j;
+              return fine ? x : 0.f;
+            });
+          }
+      }
+    }
     if constexpr (!STATE) {
       T* orow = static_cast<T*>(p.o) + ((size_t)c0 + i16) * vrow + (size_t)h * p.dv + slice * CW;
 #pragma unroll
@@ -705,6 +750,22 @@ __global__ __launch_bounds__(64 * NW, 2) void linear_chunk_kernel(LinearArgs p) 
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[i][n] += __is_same(T, _Float16) ? shifted(pv[n], -sh) : pv[n];
+        if (__builtin_expect(lost != 0, 0)) {   // counts the values taken out up to each query
+          int last = lane;
+          asm volatile("" : "+v"(last));        // (its masks are not kept in registers over the chunks)
+          last = 16 * i + (last & 15) - 4 * (last >> 4);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            f32x4 hits = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int b = 0; b <= i / 2; ++b)
+              mma<T>(hits, make_slots<T>([&](int j) { return lost_v[b][n] >> j & 1 ? 1.f : 0.f; }),
+                     make_slots<T>([&](int j) { return 32 * b + (j < 4 ? j : 12 + j) <= last ? 1.f : 0.f; }));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (hits[e] > 0.f) acc[i][n][e] = __builtin_nanf("");
+          }
+        }
         // lane holds token 16i + i16, columns state_col(4g..4g+3) of each tile
         if (16 * i + i16 < len) {
           T* at = orow + (size_t)(16 * i) * vrow;

@@ -311,6 +311,10 @@ gdn_status gdn_state_snapshot(const float* src, float* dst, int64_t num_states, 
  * summed from terms of fp32 accuracy (fp16: of 2^-22, but no finer than 2^-38 of the
  * largest decayed v of the same column in the same chunk).
  *
+ * Infinities and NaN touch later tokens only: one in v makes its column of o NaN or
+ * infinite from its token on and that column of the state, one in k the outputs
+ * from its token on and its row of the state, one in q its token's outputs.
+ *
  * Precondition of the prefill: g <= 0 (g = -infinity forgets everything before
  * the token).  The step takes g of any sign.
  */

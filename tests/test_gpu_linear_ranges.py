@@ -116,3 +116,36 @@ def test_fp16_columns_of_different_sizes(lengths, Hq, Hv, dk, dv):
     e, n = E[torch.float16], 4 * (max(lengths) // 32 + 21) + 80
     close(o[..., 1::2], ref[..., 1::2], (e * (abs(ref) + mag) + (n + dk) * U * mag)[..., 1::2], "o")
     close(fin, want, n * U * fmag, "final")
+
+
+@pytest.mark.parametrize("lengths,Hq,Hv,dk,dv", SHAPES + [([600, 40], 1, 3, 16, 16)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_values_that_are_no_numbers_reach_later_tokens_only(dtype, value, lengths, Hq, Hv, dk, dv):
+    """An infinity or NaN in v: its column of o and of the state from its token on, and nothing else."""
+    c = make(66, lengths, Hq, Hv, dk, dv, dtype, memory=0.05)
+    clean, fin = prefill(c)
+    assert torch.isfinite(clean).all() and torch.isfinite(fin).all()
+    hurt, final = torch.zeros_like(clean, dtype=torch.bool), torch.zeros_like(fin, dtype=torch.bool)
+    cu = c["cu"].tolist()
+    for s, (a, b) in enumerate(zip(cu, cu[1:])):
+        for at, h, col in ((a + (b - a) // 2, 0, 1), (b - 1, Hv - 1, dv - 1), (a + (b - a) // 3, Hv // 2, dv // 2)):
+            c["v"][at, h, col] = value
+            hurt[at:b, h, col] = True
+            final[s, h, :, col] = True
+    o, f = prefill(c)
+    assert torch.equal(o[~hurt], clean[~hurt]) and not torch.isfinite(o[hurt]).any()
+    assert torch.equal(f[~final], fin[~final]) and not torch.isfinite(f[final]).any()
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_queries_and_keys_that_are_no_numbers(which):
+    c = make(67, [150, 30], 1, 2, 64, 64, "bf16", memory=0.05)
+    clean, fin = prefill(c)
+    c[which][70, 0, 3] = float("nan")
+    o, f = prefill(c)
+    last = 71 if which == "q" else 150
+    assert torch.equal(o[:70], clean[:70]) and torch.equal(o[last:], clean[last:]) and torch.isnan(o[70:last]).all()
+    rows = torch.tensor([r for r in range(64) if which == "q" or r != 3], device=DEV)
+    assert torch.equal(f[:, :, rows], fin[:, :, rows]) and torch.equal(f[1], fin[1])
+    assert which == "q" or torch.isnan(f[0, :, 3]).all()
