@@ -116,6 +116,8 @@ struct LinearArgs {
   float* seg_decay;      // [max_segs, Hv]: its decay
 };
 
+constexpr uint32_t kLaunchThreads = 0xffffffffu;   // threads of one launch, at most
+
 constexpr int32_t kVerifyRowMax = 65536;   // entries of a row that one workgroup verifies (no workspace)
 
 struct VerifyArgs {
@@ -140,7 +142,7 @@ struct NormArgs {
   const void* wnext;
   void* h;
   void* normed;
-  int64_t T;
+  int64_t T, row0;       // rows, and the first of this launch
   int32_t D, group, act;
   float scale, eps;
 };

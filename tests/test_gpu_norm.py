@@ -164,3 +164,15 @@ def test_more_rows_than_workgroups_in_place():
     want = gdn.gdn_block_norm(y, residual=r, residual_scale=0.5, post_weight=w, next_weight=w)
     got = gdn.gdn_block_norm(y, residual=r, residual_scale=0.5, post_weight=w, next_weight=w, out=r)
     assert got[0] is r and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_more_rows_than_one_launch_takes():
+    """A workgroup of 1024 threads a row: 2^22 rows are 2^32 threads."""
+    T, D = 2 ** 22 + 3, 8200
+    y = torch.ones(T, D, dtype=torch.bfloat16, device=DEV)
+    y[-3:] = 3.0
+    y[2 ** 22 - 2:2 ** 22] = 5.0
+    h, _ = gdn.gdn_block_norm(y, residual_scale=2.0, out=y)
+    for at, want in ((slice(0, 2), 2.0), (slice(2 ** 22 - 4, 2 ** 22 - 2), 2.0), (slice(2 ** 22 - 2, 2 ** 22), 10.0),
+                     (slice(-3, None), 6.0)):
+        assert (h[at] == want).all()
