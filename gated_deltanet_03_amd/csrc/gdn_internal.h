@@ -105,6 +105,7 @@ struct LinearArgs {
   int32_t B, T, total;
   int32_t Hq, Hv, dk, dv;
   float scale;
+  int32_t first;         // (segment, key head) pair (step: (row, head) pair) of this launch's first workgroup
   // step only
   int32_t cap;
   const int32_t* counts;

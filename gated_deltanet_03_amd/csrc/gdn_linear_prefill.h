@@ -58,6 +58,8 @@
 // column tile a wave (twice the waves and LDS reads) takes 122 us, four 119 us.
 #pragma once
 
+#include <algorithm>
+
 #include "gdn_device.h"
 #include "gdn_internal.h"
 #include "gdn_mfma.h"
@@ -362,7 +364,7 @@ __global__ __launch_bounds__(64 * NW, (PASS == Pass::kOut && C == 64 && NW <= 2 
 
   // XCD-aware order: the workgroups that share one segment's keys get ids equal mod 8
   const int G = p.Hv / p.Hq, nsl = p.dv / CW, share = G * nsl;
-  const int unit = (int)(blockIdx.x >> 3) / share * 8 + (int)(blockIdx.x & 7);
+  const int unit = p.first + (int)(blockIdx.x >> 3) / share * 8 + (int)(blockIdx.x & 7);
   if (unit >= p.max_segs * p.Hq) return;
   const int seg = unit / p.Hq, hk = unit % p.Hq, sub = (int)(blockIdx.x >> 3) % share;
   const int h = hk * G + sub / nsl, slice = sub % nsl;
@@ -810,10 +812,15 @@ __global__ __launch_bounds__(64 * NW, (PASS == Pass::kOut && C == 64 && NW <= 2 
 
 template <typename T, int C, int DK, int NT, int NW, Pass P>
 static hipError_t run_pass(KernelId id, const LinearArgs& a, hipStream_t s) {
-  const long long units = (long long)a.max_segs * a.Hq;
-  const dim3 grid((unsigned)((units + 7) / 8 * 8 * (a.Hv / a.Hq) * (a.dv / (16 * NT * NW))));
+  const int64_t units = ((int64_t)a.max_segs * a.Hq + 7) / 8 * 8;
+  const int64_t share = (a.Hv / a.Hq) * (a.dv / (16 * NT * NW)), most = kLaunchThreads / (64 * NW) / share / 8 * 8;
   prof_begin(id, s);
-  hipLaunchKernelGGL((linear_chunk_kernel<T, C, DK, NT, NW, P>), grid, dim3(64 * NW), 0, s, a);
+  for (int64_t u = 0; u < units; u += most) {
+    LinearArgs b = a;
+    b.first = (int32_t)u;
+    hipLaunchKernelGGL((linear_chunk_kernel<T, C, DK, NT, NW, P>), dim3((unsigned)(std::min(most, units - u) * share)),
+                       dim3(64 * NW), 0, s, b);
+  }
   prof_end(id, s);
   return hipGetLastError();
 }

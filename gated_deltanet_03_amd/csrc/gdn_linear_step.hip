@@ -14,6 +14,8 @@
 // Measured at 32 heads of d = 128, bf16: 64 rows of one token 40.5 us (270 MB at
 // 6.6 TB/s back to back, part of it from the last-level cache; 5.5 TB/s with other
 // inputs each time), one row 3.9 us, 8 rows of 1 to 7 tokens with records 9.4 us.
+#include <algorithm>
+
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
@@ -41,7 +43,7 @@ __global__ __launch_bounds__(64 * (DK >= 32 ? DK / 32 : 1)) void linear_step_ker
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int cg = lane % CPL, rg = lane / CPL;
   const int nsl = p.dv / CW;
-  const int slice = (int)(blockIdx.x % nsl), pair = (int)(blockIdx.x / nsl);
+  const int slice = (int)(blockIdx.x % nsl), pair = p.first + (int)(blockIdx.x / nsl);
   const int b = pair / p.Hv, h = pair % p.Hv, G = p.Hv / p.Hq, hk = h / G;
   const int col = slice * CW + cg * 4, row0 = wave * (DK / NW) + rg * RPL;
   const size_t sidx = (size_t)row0 * p.dv + col;
@@ -123,8 +125,13 @@ __global__ __launch_bounds__(64 * (DK >= 32 ? DK / 32 : 1)) void linear_step_ker
 template <typename T, int DK, int CW>
 static void launch_step_w(const LinearArgs& a, hipStream_t s) {
   constexpr int NW = DK >= 32 ? DK / 32 : 1;
-  hipLaunchKernelGGL((linear_step_kernel<T, DK, CW>), dim3((unsigned)((size_t)a.B * a.Hv * (a.dv / CW))), dim3(64 * NW),
-                     0, s, a);
+  const int64_t pairs = (int64_t)a.B * a.Hv, nsl = a.dv / CW, most = kLaunchThreads / (64 * NW) / nsl;
+  for (int64_t first = 0; first < pairs; first += most) {
+    LinearArgs b = a;
+    b.first = (int32_t)first;
+    hipLaunchKernelGGL((linear_step_kernel<T, DK, CW>), dim3((unsigned)(std::min(most, pairs - first) * nsl)),
+                       dim3(64 * NW), 0, s, b);
+  }
 }
 
 template <typename T, int DK>

@@ -149,3 +149,21 @@ def test_queries_and_keys_that_are_no_numbers(which):
     rows = torch.tensor([r for r in range(64) if which == "q" or r != 3], device=DEV)
     assert torch.equal(f[:, :, rows], fin[:, :, rows]) and torch.equal(f[1], fin[1])
     assert which == "q" or torch.isnan(f[0, :, 3]).all()
+
+
+@pytest.mark.parametrize("call,Hv,dk", [("gdn_linear_prefill", 129, 16), ("gdn_linear_step", 65, 128)])
+def test_more_pairs_than_one_launch_takes(call, Hv, dk):
+    """65535 one-token rows: 512 and 1024 threads a (row, head) pair are 2^32 threads and more."""
+    B, dv = 65535, 128
+    gen = torch.Generator(device=DEV).manual_seed(71)
+    q = torch.randn(B, 1, 1, dk, device=DEV, generator=gen, dtype=torch.bfloat16)
+    k = torch.randn(B, 1, 1, dk, device=DEV, generator=gen, dtype=torch.bfloat16)
+    v = torch.randn(B, 1, Hv, dv, device=DEV, generator=gen, dtype=torch.bfloat16)
+    o = torch.full_like(v, 7.0)
+    getattr(gdn, call)(q, k, v, torch.zeros(Hv, device=DEV), scale=1.0, o=o, output_final_state=False)
+    e = E[torch.bfloat16]
+    for rows in torch.arange(B, device=DEV).split(4096):   # o = (q . k) v: the score in parts, products in fp32
+        a, b = q[rows, 0].double(), k[rows, 0].double()
+        s, size = (a * b).sum(-1, keepdim=True), (a * b).abs().sum(-1, keepdim=True)
+        want, x = s * v[rows, 0].double(), v[rows, 0].double().abs()
+        assert ((o[rows, 0].double() - want).abs() <= e * want.abs() + (3 * e * e + (dk + 80) * U) * size * x).all()
