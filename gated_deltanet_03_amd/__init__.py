@@ -499,6 +499,9 @@ def _descriptor(cls, key):
     same few descriptors over and over; they are kept by value."""
     hit = _kept.get((cls, key))
     if hit is None:
+        for (name, kind), x in zip(cls._fields_, key):
+            if kind is ctypes.c_int32 and x >= 1 << 31:   # ctypes would keep its low bits
+                raise ValueError(f"{name}={x} does not fit 32 bits")
         if len(_kept) >= 1024:
             _kept.clear()
         sh = cls(*key)

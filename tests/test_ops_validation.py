@@ -212,3 +212,17 @@ def test_norm_abi(lib):
     assert call(h=ctypes.c_void_p(0x10000010)) == bad and "h overlaps y" in last(lib)
     assert call(wn=A[2], n=A[0]) == bad and "normed overlaps y" in last(lib)
     assert call(wn=A[2], n=A[1]) == bad and "normed overlaps h" in last(lib)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The C structs hold 32-bit sizes: a larger one must not be cut to its low bits."""
+    def n(*s, dtype=torch.bfloat16):
+        return torch.empty(*s, dtype=dtype, device="meta")
+    big = 2 ** 32 + 32
+    with pytest.raises(ValueError, match="V=4294967328 does not fit 32 bits"):
+        gdn.gdn_verify_drafts(n(1, 1, big), None, n(1, 0, dtype=torch.int32), n(1, 1, dtype=torch.float32))
+    with pytest.raises(ValueError, match="D=4294967328 does not fit 32 bits"):
+        gdn.gdn_block_norm(n(1, big))
+    for call in (gdn.gdn_linear_prefill, gdn.gdn_linear_step):
+        with pytest.raises(ValueError, match="T=4294967328 does not fit 32 bits"):
+            call(n(1, big, 1, 16), n(1, big, 1, 16), n(1, big, 1, 16), n(1, dtype=torch.float32))
