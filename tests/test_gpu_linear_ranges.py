@@ -167,3 +167,38 @@ def test_more_pairs_than_one_launch_takes(call, Hv, dk):
         s, size = (a * b).sum(-1, keepdim=True), (a * b).abs().sum(-1, keepdim=True)
         want, x = s * v[rows, 0].double(), v[rows, 0].double().abs()
         assert ((o[rows, 0].double() - want).abs() <= e * want.abs() + (3 * e * e + (dk + 80) * U) * size * x).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dk", [64, 128])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("Hq,Hv", [(61, 122), (33, 264)])
+def test_one_pass_of_whole_sequences(dtype, dk, dv, Hq, Hv):
+    """No segments: below 256 (sequence, head) pairs half the columns a workgroup, above 512 all of them."""
+    B, T = 2, 250
+    c = make(72, [T] * B, Hq, Hv, dk, dv, dtype, memory=0.05)
+    sh = gdn.gdn_shape(B, T, Hq, Hv, dk, dv, 1.0, gdn._DTYPES[TYPES[dtype]])
+    assert gdn.gdn_linear_workspace_bytes(sh, False) == 0
+    d = {x: c[x].to(DEV).view(B, T, *c[x].shape[1:]) for x in "qkvg"}
+    args, s0 = [d[x] for x in "qkvg"], c["s0"].to(DEV)
+    o, fin = gdn.gdn_linear_prefill(*args, scale=c["scale"], initial_state=s0)
+    check(o.flatten(0, 1), fin, c)
+    state = s0.clone()
+    o2, fin2 = gdn.gdn_linear_prefill(*args, scale=c["scale"], initial_state=state, final_state=state)
+    assert torch.equal(o, o2) and torch.equal(fin, fin2)
+    one = s0[:1].contiguous()
+    o3, fin3 = gdn.gdn_linear_prefill(*args, scale=c["scale"], initial_state=one)
+    assert torch.equal(o[0], o3[0]) and torch.equal(fin[0], fin3[0])
+    c["s0"] = c["s0"][:1].repeat(B, 1, 1, 1)
+    check(o3.flatten(0, 1), fin3, c)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_one_pass_of_ragged_sequences(dtype):
+    """512 pairs and more: a long sequence beside empty and short ones, in one pass."""
+    lengths = [450, 0, 1, 65, 0, 31] * 3
+    c = make(73, lengths, 16, 32, 128, 128, dtype, "head", memory=0.05)
+    sh = gdn.gdn_shape(len(lengths), sum(lengths), 16, 32, 128, 128, 1.0, gdn._DTYPES[TYPES[dtype]])
+    assert gdn.gdn_linear_workspace_bytes(sh, True) == 0
+    o, fin = prefill(c)
+    check(o, fin, c)
