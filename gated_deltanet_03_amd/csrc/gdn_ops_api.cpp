@@ -34,24 +34,29 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 // Tokens per segment of the split prefill, 0 for one segment per sequence.
 //
 // A segment's workgroup walks its chunks one after another, so (sequence, head)
-// pairs alone fill the 256 CUs only from a few hundred on.  Below that the
-// tokens are cut
-//  * so that about kTargetWg (segment, head) workgroups exist, two for each CU
-//    (14286 ragged tokens x 32 heads bf16: 160 us; 600 of them 186 us);
+// pairs alone fill the 256 CUs only from a few hundred on.  From kSlots pairs on,
+// two workgroups for each CU, nothing is cut; below that the tokens are cut
+//  * into kParts even parts of all heads' tokens, somewhat fewer than kSlots:
+//    sequences end inside of parts, so there are up to B * Hv workgroups more, and
+//    a second round of a few workgroups costs most of a first one.  Over eleven random
+//    lists of 2 to 6 sequences, 8000 to 21000 tokens in all, 8 to 32 heads, mostly
+//    d = 128 bf16, 384 / 448 / 480 / 512 / 576 parts took 1.13, 1.04, 1.02, 1.03,
+//    1.14 of the best for each;
 //  * but not below sqrt(c * longest) tokens: the output pass of a sequence's last
 //    segment sums the states of all before it, so fewer tokens a segment make
-//    its walk shorter and that sum longer (2048 tokens x 6 heads fp16: 29 us, 32
-//    with c = 8, 33 with c = 20).  A token costs more in fp32 (2221 ragged tokens
-//    x 8 heads: 28 us, 34 with c = 7; 12000 tokens x 1 head: 64 us, 76 with c = 7).
-constexpr int64_t kTargetWg = 480, kFullWg = 512;
+//    its walk shorter and that sum longer.  Over twelve lists of 1000 to 30000
+//    16-bit tokens c = 4, 6, 8, 14, 20 took 1.01, 1.01, 1.03, 1.05, 1.10 of the
+//    best for each, over eight fp32 lists, where a token costs more,
+//    c = 0.5, 1.5, 3, 5, 7 took 1.02, 1.02, 1.02, 1.06, 1.07.
+constexpr int64_t kSlots = 512, kParts = 480;
 
 int32_t segment_tokens(const gdn_shape* sh, int64_t total, bool ragged) {
   const int64_t pairs = (int64_t)sh->B * sh->Hv;
-  if (pairs == 0 || pairs >= kFullWg) return 0;
+  if (pairs == 0 || pairs >= kSlots) return 0;
   // the longest sequence is not known for ragged input; total bounds it
   const int64_t longest = ragged ? total : sh->T;
-  int64_t seg = std::max<int64_t>((total * sh->Hv + kTargetWg - 1) / kTargetWg,
-                                  (int64_t)std::sqrt((sh->dtype == GDN_F32 ? 1.5 : 14.0) * (double)longest));
+  int64_t seg = std::max<int64_t>((total * sh->Hv + kParts - 1) / kParts,
+                                  (int64_t)std::sqrt((sh->dtype == GDN_F32 ? 1.5 : 5.0) * (double)longest));
   seg = (seg + 63) / 64 * 64;
   return longest <= 2 * seg ? 0 : (int32_t)seg;
 }
