@@ -4,7 +4,7 @@
 // wave's 512 entries are summed, the tile that holds u * sum(w) is found among the
 // at most 128 sums and scanned by one wave.
 //
-// Beyond, two kernels.  verify_sum: one workgroup per (tiles of the vocabulary,
+// Beyond, two kernels.  verify_sum: one workgroup per (tile of the vocabulary,
 // row) finds how many drafts the row accepts (a gather of at most K pairs), then
 // sums the tiles' weights w = max(p_a - q_a, 0) (or p_a).  verify_draw: one
 // workgroup per row scans the tiles' sums, finds the tile that holds u * sum(w),
@@ -17,11 +17,11 @@
 // 10^-5 apart, and sums in 32 bits, whose order depends on the split, would
 // place one token in a hundred wrongly.
 //
-// Measured, fp32: 64 rows of 131072 with 7 drafts 13.5 + 5.5 us (64 MB, 4.7 TB/s in
-// the first kernel; 15.1 us with one tile a workgroup).  The token is picked by
-// ballots: with atomics on LDS the second kernel took 25 us.  A call on one row of
-// 32003: 9.0 us in one kernel, bound by its host time, 13.1 in two; on 64 rows of
-// 65536 12.7 us in one, 13.9 in two.
+// Calls measured, fp32, inputs new to the caches: one row of 32003 8.7 us in one
+// kernel, bound by its host time, 12.1 in two; 64 rows of 32768 8.6 and 11.7, of 65536
+// 12.6 and 12.8, 128 rows of 65536 15.7 and 17.8.  64 rows of 131072 take 18.0 us
+// (64 MB), 18.4 with four tiles a workgroup; 256 rows of them 49.3 and 52.7.  The
+// token is picked by ballots: with atomics on LDS the second kernel took 25 us.
 #include "gdn_internal.h"
 #include "gdn_rows.h"
 
@@ -182,48 +182,25 @@ __device__ __forceinline__ double tile_sum(const Weights<T>& wt, const VerifyArg
   return s;
 }
 
-// S neighbouring tiles per workgroup: 1 where there are few (one row spreads over
-// many workgroups), 4 for a batch, whose loads are then in flight together.
-template <typename T, int S>
+template <typename T>
 __global__ __launch_bounds__(VT) void verify_sum_kernel(VerifyArgs p) {
-  __shared__ double lds[S][VT / 64];
-  const int tile0 = (int)blockIdx.x * S, b = blockIdx.y, tid = threadIdx.x;
+  __shared__ double lds[VT / 64];
+  const int tile = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int n = drafts_of(p, b);
   if (n < 0) {
-    if (tile0 == 0 && tid == 0) p.emit[b] = 0;
+    if (tile == 0 && tid == 0) p.emit[b] = 0;
     return;
   }
   const int a = accepted<T>(p, b, n);
-  if (tile0 == 0 && tid == 0) p.emit[b] = a + 1;
-  const Weights<T> wt(p, b, a, a < n);
-  double s[S];
-  if (S > 1 && (int64_t)(tile0 + S) * VSUB <= p.V) {   // S > 1: tiles of VSUB entries
-    typename Weights<T>::Raw raw[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) wt.fetch((tile0 + i) * VSUB + tid * VPT, raw[i]);
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      double w[VPT];
-      wt.weigh((tile0 + i) * VSUB + tid * VPT, raw[i], w);
-      s[i] = 0.0;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) s[i] += w[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < S; ++i) s[i] = tile0 + i < p.tiles ? tile_sum(wt, p, tile0 + i) : 0.0;
-  }
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    s[i] = wave_scan64(s[i]);
-    if ((tid & 63) == 63) lds[i][tid >> 6] = s[i];
-  }
+  if (tile == 0 && tid == 0) p.emit[b] = a + 1;
+  const double s = wave_scan64(tile_sum(Weights<T>(p, b, a, a < n), p, tile));
+  if ((tid & 63) == 63) lds[tid >> 6] = s;
   __syncthreads();
-  if (tid < S && tile0 + tid < p.tiles) {
+  if (tid == 0) {
     double total = 0.0;
 #pragma unroll
-    for (int w = 0; w < VT / 64; ++w) total += lds[tid][w];
-    p.part[(size_t)b * p.tiles + tile0 + tid] = total;
+    for (int w = 0; w < VT / 64; ++w) total += lds[w];
+    p.part[(size_t)b * p.tiles + tile] = total;
   }
 }
 
@@ -411,10 +388,7 @@ static hipError_t launch_verify_t(const VerifyArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   prof_begin(K_VERIFY_SUM, s);
-  if (a.tile == VSUB && (int64_t)a.tiles * a.B > 2048)   // 8 workgroups for each CU
-    hipLaunchKernelGGL((verify_sum_kernel<T, 4>), dim3((a.tiles + 3) / 4, a.B), dim3(VT), 0, s, a);
-  else
-    hipLaunchKernelGGL((verify_sum_kernel<T, 1>), dim3(a.tiles, a.B), dim3(VT), 0, s, a);
+  hipLaunchKernelGGL((verify_sum_kernel<T>), dim3(a.tiles, a.B), dim3(VT), 0, s, a);
   prof_end(K_VERIFY_SUM, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
