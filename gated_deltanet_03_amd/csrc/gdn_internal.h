@@ -151,7 +151,7 @@ struct NormArgs {
 // Opt-in per-kernel event timing (gdn_profile_enable / gdn_profile_collect).
 enum KernelId : int {
   K_PLAN = 0, K_PREP, K_STATE, K_RECURRENT, K_REPLAY, K_COPY,
-  K_LIN_STATE, K_LIN_OUT, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_VERIFY_ROW, K_NORM, kNumKernels
+  K_LIN_STATE, K_LIN_OUT, K_LIN_WHOLE, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_VERIFY_ROW, K_NORM, kNumKernels
 };
 void prof_begin(KernelId id, hipStream_t s);
 void prof_end(KernelId id, hipStream_t s);

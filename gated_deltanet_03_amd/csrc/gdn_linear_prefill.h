@@ -830,7 +830,7 @@ static hipError_t run_pass(KernelId id, const LinearArgs& a, hipStream_t s) {
 template <typename T, int DK, int TILES, int NT, int COUT>
 static hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
   constexpr int C = sizeof(T) == 2 ? 64 : 32;
-  if (a.seg_tokens == 0) return run_pass<T, C, DK, 1, TILES, Pass::kWhole>(K_LIN_OUT, a, s);
+  if (a.seg_tokens == 0) return run_pass<T, C, DK, 1, TILES, Pass::kWhole>(K_LIN_WHOLE, a, s);
   const hipError_t e = run_pass<T, C, DK, 1, TILES, Pass::kState>(K_LIN_STATE, a, s);
   return e == hipSuccess ? run_pass<T, COUT, DK, NT, TILES / NT, Pass::kOut>(K_LIN_OUT, a, s) : e;
 }

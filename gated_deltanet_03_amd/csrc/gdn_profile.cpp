@@ -17,9 +17,9 @@ namespace {
 
 const char* const kNames[kNumKernels] = {"chunk_plan_kernel", "chunk_prep_kernel", "chunk_state_kernel",
                                           "recurrent_step_kernel", "replay_kernel", "copy_kernel",
-                                          "linear_state_kernel", "linear_out_kernel",
-                                          "linear_step_kernel", "verify_sum_kernel", "verify_draw_kernel", "verify_row_kernel",
-                                          "block_norm_kernel"};
+                                          "linear_chunk_kernel (state)", "linear_chunk_kernel (outputs)",
+                                          "linear_chunk_kernel (whole)", "linear_step_kernel", "verify_sum_kernel",
+                                          "verify_draw_kernel", "verify_row_kernel", "block_norm_kernel"};
 
 struct Rec {
   int id;
