@@ -484,11 +484,17 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (1.0 us less a call);
+# torch keeps that query to itself, so the public one stands in where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on_gpu(dev):
     """The library reads device memory only; a host pointer would fault the GPU."""
     if dev.type != "cuda":
         raise ValueError(f"tensors are on {dev}, expected a GPU")
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _raw_stream(dev.index)
 
 
 _kept = {}
