@@ -364,8 +364,9 @@ gdn_status gdn_linear_step(const gdn_shape* shape, const void* q, const void* k,
  *   as the lowest index v with  sum_{j <= v} w_j > u[b,K] * sum_j w_j
  *   (the last v with w_v > 0 if rounding leaves none).
  *
- * Products, differences and sums are taken in 64 bits, so the result does not
- * depend on how the sums are split.  draft_probs NULL: the drafts are
+ * Products, differences and sums are taken in 64 bits; the sums' order, which goes
+ * by the sizes, moves them by at most about 2^-47 of the total, and a draw nearer
+ * than that to the border between two tokens may give either.  draft_probs NULL: the drafts are
  * deterministic (q_i is 1 at x_i and 0 elsewhere).  A draft token outside
  * [0, V) is refused, with q_a = 0 everywhere if draft_probs is NULL.  Weights
  * that are NaN, infinite or not positive count as 0; a row whose weights are all 0 draws
