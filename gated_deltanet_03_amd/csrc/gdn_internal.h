@@ -89,69 +89,9 @@ inline size_t chunk_block_bytes(DType dt) {
   return 2 * 6 * 512 * es + 64 * 4 * 4;
 }
 
-// Linear attention with a decay for each head.  Prefill: segments of
-// seg_tokens tokens (0: one segment per sequence, no workspace).
-struct LinearArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const float* g;
-  int64_t g_stride;      // elements between tokens' log decays: Hv, or 0 (one per head)
-  const float* s0;       // may be null (zeros)
-  int64_t s0_stride;
-  float* s_out;          // may be null
-  void* o;
-  const int32_t* cu;     // null = dense rows
-  int32_t B, T, total;
-  int32_t Hq, Hv, dk, dv;
-  float scale;
-  int32_t first;         // (segment, key head) pair (step: (row, head) pair) of this launch's first workgroup
-  // step only
-  int32_t cap;
-  const int32_t* counts;
-  float* su;             // [B, cap, R]
-  // prefill only
-  int32_t seg_tokens, max_segs;
-  float* seg_state;      // [max_segs + B, Hv, dk, dv]: a segment's own state (the first's with the
-                         // initial one), then the initial states, in the kernels' order
-  float* seg_decay;      // [max_segs, Hv]: its decay
-};
-
-constexpr uint32_t kLaunchThreads = 0xffffffffu;   // threads of one launch, at most
-
-constexpr int32_t kVerifyRowMax = 65536;   // entries of a row that one workgroup verifies (no workspace)
-
-struct VerifyArgs {
-  const void* p;
-  const void* q;         // may be null (deterministic drafts)
-  int64_t p_stride, q_stride;
-  const int32_t* x;
-  const float* u;
-  const int32_t* n;      // may be null
-  int32_t* tokens;
-  int32_t* emit;
-  int32_t B, K, V;
-  int32_t tile, tiles;   // tiles of `tile` vocabulary entries per row
-  double* part;          // [B, tiles] sums of weights
-};
-
-struct NormArgs {
-  const void* y;
-  const void* gate;
-  const void* res;
-  const void* wpost;
-  const void* wnext;
-  void* h;
-  void* normed;
-  int64_t T, row0;       // rows, and the first of this launch
-  int32_t D, group, act;
-  float scale, eps;
-};
-
 // Opt-in per-kernel event timing (gdn_profile_enable / gdn_profile_collect).
 enum KernelId : int {
-  K_PLAN = 0, K_PREP, K_STATE, K_RECURRENT, K_REPLAY, K_COPY,
-  K_LIN_STATE, K_LIN_OUT, K_LIN_WHOLE, K_LIN_STEP, K_VERIFY_SUM, K_VERIFY_DRAW, K_VERIFY_ROW, K_NORM, kNumKernels
+  K_PLAN = 0, K_PREP, K_STATE, K_RECURRENT, K_REPLAY, K_COPY, kNumKernels
 };
 void prof_begin(KernelId id, hipStream_t s);
 void prof_end(KernelId id, hipStream_t s);
@@ -159,12 +99,6 @@ void prof_end(KernelId id, hipStream_t s);
 hipError_t launch_recurrent(DType dt, const DecodeArgs& a, hipStream_t s);
 hipError_t launch_replay(const ReplayArgs& a, hipStream_t s);
 hipError_t launch_copy(const float* src, float* dst, size_t n, hipStream_t s);
-hipError_t launch_linear_prefill_f32(const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_prefill_f16(const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_prefill_bf16(const LinearArgs& a, hipStream_t s);
-hipError_t launch_linear_step(DType dt, const LinearArgs& a, hipStream_t s);
-hipError_t launch_verify(DType dt, const VerifyArgs& a, hipStream_t s);
-hipError_t launch_norm(DType dt, const NormArgs& a, hipStream_t s);
 hipError_t launch_prefill(DType dt, const PrefillArgs& a, hipStream_t s);
 
 }  // namespace gdn

@@ -61,8 +61,9 @@
 #include <algorithm>
 
 #include "gdn_device.h"
-#include "gdn_internal.h"
 #include "gdn_mfma.h"
+#include "gdn_ops_internal.h"
+#include "gdn_scan.h"
 
 namespace gdn {
 namespace linear {

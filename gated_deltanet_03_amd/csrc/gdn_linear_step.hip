@@ -17,7 +17,7 @@
 #include <algorithm>
 
 #include "gdn_device.h"
-#include "gdn_internal.h"
+#include "gdn_ops_internal.h"
 
 namespace gdn {
 

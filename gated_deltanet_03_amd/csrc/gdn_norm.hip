@@ -15,7 +15,7 @@
 // once: 5.5 TB/s, where a 1 GiB copy reaches 5.2.
 #include <algorithm>
 
-#include "gdn_internal.h"
+#include "gdn_ops_internal.h"
 #include "gdn_rows.h"
 
 namespace gdn {

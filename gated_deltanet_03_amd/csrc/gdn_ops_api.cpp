@@ -8,7 +8,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_check.h"
-#include "gdn_internal.h"
+#include "gdn_ops_internal.h"
 
 using namespace gdn;
 

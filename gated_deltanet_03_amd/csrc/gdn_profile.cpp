@@ -10,12 +10,12 @@
 #include <vector>
 
 #include "../../include/gdn.h"
-#include "gdn_internal.h"
+#include "gdn_ops_internal.h"
 
 namespace gdn {
 namespace {
 
-const char* const kNames[kNumKernels] = {"chunk_plan_kernel", "chunk_prep_kernel", "chunk_state_kernel",
+const char* const kNames[kAllKernels] = {"chunk_plan_kernel", "chunk_prep_kernel", "chunk_state_kernel",
                                           "recurrent_step_kernel", "replay_kernel", "copy_kernel",
                                           "linear_chunk_kernel (state)", "linear_chunk_kernel (outputs)",
                                           "linear_chunk_kernel (whole)", "linear_step_kernel", "verify_sum_kernel",
@@ -90,8 +90,8 @@ int32_t gdn_profile_collect(const char** names, double* total_ms, int32_t* launc
     std::lock_guard<std::mutex> lk(g_mu);
     recs.swap(g_pending);
   }
-  double tot[kNumKernels] = {0};
-  int cnt[kNumKernels] = {0};
+  double tot[kAllKernels] = {0};
+  int cnt[kAllKernels] = {0};
   for (const Rec& r : recs) {
     float ms = 0.f;
     if (hipEventSynchronize(r.b) == hipSuccess && hipEventElapsedTime(&ms, r.a, r.b) == hipSuccess) {
@@ -107,7 +107,7 @@ int32_t gdn_profile_collect(const char** names, double* total_ms, int32_t* launc
     }
   }
   int n = 0;
-  for (int k = 0; k < kNumKernels; ++k) {
+  for (int k = 0; k < kAllKernels; ++k) {
     if (cnt[k] == 0) continue;
     if (n < max_kernels) {
       if (names) names[n] = kNames[k];

@@ -22,8 +22,9 @@
 // 12.6 and 12.8, 128 rows of 65536 15.7 and 17.8.  64 rows of 131072 take 18.0 us
 // (64 MB), 18.4 with four tiles a workgroup; 256 rows of them 49.3 and 52.7.  The
 // token is picked by ballots: with atomics on LDS the second kernel took 25 us.
-#include "gdn_internal.h"
+#include "gdn_ops_internal.h"
 #include "gdn_rows.h"
+#include "gdn_scan.h"
 
 namespace gdn {
 
