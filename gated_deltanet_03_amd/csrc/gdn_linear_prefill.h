@@ -47,15 +47,15 @@
 // the key to the tile's start.  A decay below e^-128 is 0 in fp32, so g is clamped
 // there and -infinity needs no special case.
 //
-// What bounds it: 14286 ragged tokens x 32 heads, d = 128, bf16 take 62 us (state)
-// and 97 us (outputs), where a copy of the same bytes would take 40 and 75.  In
-// the output pass a 32-token chunk of a workgroup takes 5.6 k cycles, two
-// workgroups a CU: 0.6 k to issue the loads, 0.9 k scores, 0.6 k S^T Q, 1.3 k
-// update, 0.7 k V^T P^T and stores, 0.5 k staging, 0.8 k barriers.  VALU, MFMA and
-// LDS are busy 28, 20 and 33 % of the time: latencies inside a wave, with two
-// waves a SIMD (232 VGPRs) to hide them.  Chunks re-read from the cache are no
-// faster, bank-conflict-free tiles gained 1 %, a third wave a SIMD spills, and one
-// column tile a wave (twice the waves and LDS reads) takes 122 us, four 119 us.
+// What bounds it: 14286 ragged tokens x 32 heads, d = 128, bf16 take 178 us, 62 of
+// them the state pass; the passes move 245 and 421 MB, 47 and 81 us as a copy.  In the
+// output pass a wave's 32-token chunk is about 610 VALU, 75 MFMA and 50 LDS
+// instructions, and VALU, MFMA and LDS are busy 49, 24 and 23 % of the time (41, 31 and
+// 31 in the state pass): conversions and decays, then latencies, with two waves a
+// SIMD (232 to 250 VGPRs) to hide them.  A third wave a SIMD spills.  Before the
+// operands were in two parts (output pass 97 us) chunks re-read from the cache were
+// no faster, bank-conflict-free tiles gained 1 %, and one column tile a wave (twice
+// the waves and LDS reads) took 122 us, four 119 us.
 #pragma once
 
 #include <algorithm>

@@ -12,8 +12,9 @@
 // once per TB tokens.
 //
 // Measured at 32 heads of d = 128, bf16: 64 rows of one token 40.5 us (270 MB at
-// 6.6 TB/s back to back, part of it from the last-level cache; 5.5 TB/s with other
-// inputs each time), one row 3.9 us, 8 rows of 1 to 7 tokens with records 9.4 us.
+// 6.6 TB/s back to back, part of it from the last-level cache; 49 us, 5.5 TB/s, with
+// other inputs each time), one row 3.9 us (5.2), 8 rows of 1 to 7 tokens with records
+// 9.4 us (11.4): there each token's loads wait inside of the token loop.
 #include <algorithm>
 
 #include "gdn_device.h"
