@@ -347,8 +347,11 @@ __device__ __forceinline__ Frag<T> make_slots(F f) {
 
 // Two waves a SIMD; one for the narrow output pass with few workgroups (at most two of two
 // waves a CU), which keeps a 64-token chunk on its way in 72 registers.
+template <Pass PASS, int C, int NW>
+constexpr int kWaves = PASS == Pass::kOut && C == 64 && NW <= 2 ? 1 : 2;
+
 template <typename T, int C, int DK, int NT, int NW, Pass PASS>
-__global__ __launch_bounds__(64 * NW, (PASS == Pass::kOut && C == 64 && NW <= 2 ? 1 : 2)) void linear_chunk_kernel(LinearArgs p) {
+__global__ __launch_bounds__(64 * NW, (kWaves<PASS, C, NW>)) void linear_chunk_kernel(LinearArgs p) {
   constexpr bool STATE = PASS == Pass::kState;
   using SM = Smem<T, C, DK, NT, NW, STATE>;
   constexpr int CW = SM::CW, THREADS = 64 * NW;
