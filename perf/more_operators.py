@@ -225,7 +225,7 @@ def _run_own(st, case):
             st["logits"], st["scores"], beams=case["K"], finished=st["finished"], eos_token=2, pad_token=0)
         return {"tokens": tokens, "parents": parents, "scores": scores, "finished": finished}
     if case["kind"] == "states":
-        return {"state": gdn.gdn_state_reorder(st["state"], st["parents"], out=st["state"])}
+        return {"state": gdn.gdn_state_reorder(st["state"], st["parents"], axis=1, out=st["state"])}
     gdn.gdn_cache_copy_pages(st["k_cache"], st["v_cache"], st["src"], st["dst"])
     return {"k_cache": st["k_cache"], "v_cache": st["v_cache"]}
 
