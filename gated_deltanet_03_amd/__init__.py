@@ -16,11 +16,17 @@ Entry points (same names as the C ABI):
 ``gdn_linear_step``           the same token by token, with capture
 ``gdn_verify_drafts``         drafted tokens against the target's probabilities
 ``gdn_block_norm``            norms around a block, fused with gate, residual and scale
+``gdn_cache_append``          new keys (rotated) and values into a paged cache
+``gdn_cache_attention``       attention of new tokens over the paged cache
+``gdn_cache_copy_pages``      pages copied inside the cache
+``gdn_beam_select``           the best continuations of a beam search
+``gdn_state_reorder``         states moved from each parent to its beam
 """
 
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -36,7 +42,9 @@ EXPORTED = ("gdn_abi_version", "gdn_prefill_workspace_bytes", "gdn_prefill_chunk
             "gdn_recurrent_step_ex", "gdn_replay_state_updates", "gdn_state_snapshot",
             "gdn_status_string", "gdn_last_error", "gdn_profile_enable", "gdn_profile_collect",
             "gdn_prefill_chunked_noalloc", "gdn_linear_workspace_bytes", "gdn_linear_prefill", "gdn_linear_step",
-            "gdn_verify_workspace_bytes", "gdn_verify_drafts", "gdn_block_norm")
+            "gdn_verify_workspace_bytes", "gdn_verify_drafts", "gdn_block_norm", "gdn_cache_append",
+            "gdn_cache_attention_workspace_bytes", "gdn_cache_attention", "gdn_beam_workspace_bytes",
+            "gdn_beam_select", "gdn_state_reorder")
 GDN_NOALLOC_SCRATCH_BYTES = 128 * 1024 * 1024
 
 
@@ -77,6 +85,30 @@ class gdn_verify_shape(ctypes.Structure):
 class gdn_norm_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("D", ctypes.c_int32), ("group", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("gate_act", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class gdn_cache_shape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class gdn_append_shape(ctypes.Structure):
+    _fields_ = [("q_token_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("rotary", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32)]
+
+
+class gdn_beam_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("W", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eos_token", ctypes.c_int32), ("pad_token", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64)]
+
+
+class gdn_reorder_shape(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int64), ("src_layer_stride", ctypes.c_int64), ("dst_layer_stride", ctypes.c_int64),
+                ("src_rows", ctypes.c_int64), ("dst_rows", ctypes.c_int64), ("row_bytes", ctypes.c_int64),
+                ("src_group", ctypes.c_int64), ("G", ctypes.c_int32), ("W", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -134,6 +166,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn_verify_drafts.argtypes = [vshp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.gdn_block_norm.restype = i32
     lib.gdn_block_norm.argtypes = [nshp, vp, vp, vp, vp, vp, vp, vp, vp]
+    cshp, ashp = ctypes.POINTER(gdn_cache_shape), ctypes.POINTER(gdn_append_shape)
+    bshp, rshp = ctypes.POINTER(gdn_beam_shape), ctypes.POINTER(gdn_reorder_shape)
+    lib.gdn_cache_append.restype = i32
+    lib.gdn_cache_append.argtypes = [cshp, ashp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.gdn_cache_attention_workspace_bytes.restype = sz
+    lib.gdn_cache_attention_workspace_bytes.argtypes = [cshp, i32]
+    lib.gdn_cache_attention.restype = i32
+    lib.gdn_cache_attention.argtypes = [cshp, vp, i64, vp, vp, vp, vp, vp, ctypes.c_float, i32, vp, vp, sz, vp]
+    lib.gdn_beam_workspace_bytes.restype = sz
+    lib.gdn_beam_workspace_bytes.argtypes = [bshp]
+    lib.gdn_beam_select.restype = i32
+    lib.gdn_beam_select.argtypes = [bshp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gdn_state_reorder.restype = i32
+    lib.gdn_state_reorder.argtypes = [rshp, vp, vp, vp, vp, vp]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_status_string.argtypes = [i32]
     lib.gdn_last_error.restype = ctypes.c_char_p
@@ -768,6 +814,308 @@ def gdn_block_norm(y, *, gate=None, gate_act="silu", residual=None, residual_sca
     return out, normed
 
 
+# ---------------------------------------------------------------------------
+# Paged cache, beams
+# ---------------------------------------------------------------------------
+def _tokens(t, name, dtype, dev, ragged, H=None, d=None):
+    """(elements between tokens, tokens, H, d) of a [T, H, d] (ragged; also [1, T, H, d]) or [B, L, H, d] tensor whose
+    tokens are evenly spaced and whole."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    shape = t.shape
+    if ragged and len(shape) == 4 and shape[0] == 1:
+        t = t[0]
+    if t.dim() != (3 if ragged else 4):
+        raise ValueError(f"{name} must be {'[T, H, d] with cu_seqlens' if ragged else '[B, L, H, d]'}, "
+                         f"got shape {tuple(shape)}")
+    h, e = t.shape[-2:]
+    if (H is not None and h != H) or (d is not None and e != d):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected heads {H} of {d}")
+    count = t.shape[0] if ragged else t.shape[0] * t.shape[1]
+    if t.is_contiguous():
+        return h * e, count, h, e
+    s = t.stride()
+    if (e > 1 and s[-1] != 1) or (h > 1 and s[-2] != e):
+        raise ValueError(f"{name}'s heads must be contiguous within a token")
+    if ragged:
+        row = s[0] if count > 1 else h * e
+    else:
+        B, L = t.shape[:2]
+        row = s[1] if L > 1 else (s[0] if B > 1 else h * e)
+        if B > 1 and L > 1 and s[0] != L * row:
+            raise ValueError(f"{name} must have evenly spaced tokens, got strides {tuple(s)}")
+    if row < h * e:
+        raise ValueError(f"{name}'s tokens overlap: strides {tuple(s)}")
+    return row, count, h, e
+
+
+def _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev):
+    """Checks shared by the cache's entry points; (N, Hkv, d, page_size, num_pages, max_pages)."""
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [N, max_pages]")
+    dtype = k_cache.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _need(k_cache, "k_cache", None, dev)
+    _need(v_cache, "v_cache", dtype, dev)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(k_cache.shape)}")
+    _need(block_table, "block_table", torch.int32, dev)
+    _need(cache_lens, "cache_lens", torch.int32, dev)
+    N, max_pages = block_table.shape
+    if cache_lens.shape != (N,):
+        raise ValueError(f"cache_lens has shape {tuple(cache_lens.shape)}, expected {(N,)}")
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.shape != (N + 1,):
+            raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected {(N + 1,)}")
+    pages, Hkv, page_size, d = k_cache.shape
+    if Hkv < 1 or page_size < 1:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}")
+    return N, Hkv, d, page_size, pages, max_pages
+
+
+def gdn_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, *, cu_seqlens=None, q=None, inv_freq=None,
+                     positions=None, pair_axis=None, interleaved=False, q_out=None):
+    """New keys and values into their pages, keys (and queries) rotated by their positions on the way.
+
+    Dense k, v [N, L, Hkv, d], q [N, L, Hq, d]; ragged: [T, H, d] plus cu_seqlens int32 [N+1].  Tokens may be slices
+    of wider rows.  k_cache, v_cache [num_pages, Hkv, page_size, d]; block_table int32 [N, max_pages]; cache_lens
+    int32 [N] counts the new tokens.  inv_freq fp32 [rotary / 2] (None: nothing is rotated); positions int32
+    [tokens] or [axes, tokens] (None: places in the cache); pair_axis int32 [rotary / 2] (which axis turns which
+    pair).  ``interleaved`` pairs elements 2j, 2j + 1 instead of j, j + rotary / 2.  ``q_out`` may be q.
+    Returns q_out (None without q)."""
+    lib = load_library()
+    dev, ragged = k_cache.device, cu_seqlens is not None
+    N, Hkv, d, page_size, pages, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev)
+    dtype = k_cache.dtype
+    ks, tokens, _, _ = _tokens(k, "k", dtype, dev, ragged, Hkv, d)
+    vs, nv, _, _ = _tokens(v, "v", dtype, dev, ragged, Hkv, d)
+    if nv != tokens or (not ragged and (k.shape[0] != N or v.shape != k.shape)):
+        raise ValueError(f"k has shape {tuple(k.shape)}, v {tuple(v.shape)}, for {N} sequences")
+    Hq, qs = Hkv, Hkv * d
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q is given without inv_freq: there is nothing to do with it")
+        qs, nq, Hq, _ = _tokens(q, "q", dtype, dev, ragged, None, d)
+        if nq != tokens or (not ragged and q.shape[:2] != k.shape[:2]):
+            raise ValueError(f"q has shape {tuple(q.shape)}, k {tuple(k.shape)}")
+        if Hq % Hkv != 0:
+            raise ValueError(f"Hq={Hq} must be a multiple of Hkv={Hkv}")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=dev)
+        else:
+            _need(q_out, "q_out", dtype, dev)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
+    rotary, axes = 0, 1
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        rotary = 2 * inv_freq.numel()
+        if inv_freq.dim() != 1 or rotary < 1 or rotary > d:
+            raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [rotary / 2] with rotary <= {d}")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev)
+        if inv_freq is None:
+            raise ValueError("positions are given without inv_freq")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.dim() > 2 or axes < 1 or positions.shape[-1] != tokens:
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{tokens}] or [axes, {tokens}]")
+    if pair_axis is not None:
+        _need(pair_axis, "pair_axis", torch.int32, dev)
+        _expect(pair_axis, "pair_axis", rotary // 2)
+    elif axes > 1:
+        raise ValueError(f"pair_axis is required with {axes} axes")
+    T = tokens if ragged else k.shape[1]
+    _, ref = _descriptor(gdn_cache_shape, (N, T, Hq, Hkv, d, _DTYPES[dtype], page_size, pages, max_pages))
+    _, how = _descriptor(gdn_append_shape, (qs, ks, vs, rotary, int(bool(interleaved)), axes))
+    stream = _on_gpu(dev)
+    st = lib.gdn_cache_append(ref, how, _addr(q), k.data_ptr(), v.data_ptr(), _addr(inv_freq), _addr(positions),
+                              _addr(pair_axis), block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens),
+                              _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), stream)
+    if st:
+        _check(st)
+    return q_out
+
+
+def gdn_cache_attention_workspace_bytes(shape: gdn_cache_shape, ragged: bool) -> int:
+    """Bytes gdn_cache_attention needs for this shape (0: none)."""
+    n = load_library().gdn_cache_attention_workspace_bytes(ctypes.byref(shape), int(bool(ragged)))
+    if n == ctypes.c_size_t(-1).value:
+        _check(GDN_ERR_INVALID_ARG)
+    return int(n)
+
+
+def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seqlens=None, scale=None, window=0, o=None,
+                        workspace=None):
+    """Causal attention of new tokens over the paged cache (their own keys included).
+
+    Dense q [N, L, Hq, d]; ragged: [T, Hq, d] plus cu_seqlens int32 [N+1].  The cache as in gdn_cache_append; new token
+    i of the L of a sequence has the place cache_lens - L + i and sees the keys up to it, with ``window`` only the
+    last ``window`` of them.  ``scale`` is d^-1/2 unless given.  Returns o (q's shape, contiguous)."""
+    lib = load_library()
+    dev, ragged = k_cache.device, cu_seqlens is not None
+    N, Hkv, d, page_size, pages, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev)
+    dtype = k_cache.dtype
+    qs, tokens, Hq, _ = _tokens(q, "q", dtype, dev, ragged, None, d)
+    if Hq < 1 or Hq % Hkv != 0:
+        raise ValueError(f"Hq={Hq} must be a multiple of Hkv={Hkv}")
+    if not ragged and q.shape[0] != N:
+        raise ValueError(f"q has shape {tuple(q.shape)}, for {N} sequences")
+    if o is None:
+        o = torch.empty(q.shape, dtype=dtype, device=dev)
+    else:
+        _need(o, "o", dtype, dev)
+        if o.shape != q.shape:
+            raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(q.shape)}")
+    T = tokens if ragged else q.shape[1]
+    _, ref = _descriptor(gdn_cache_shape, (N, T, Hq, Hkv, d, _DTYPES[dtype], page_size, pages, max_pages))
+    stream = _on_gpu(dev)
+    if workspace is None:   # an invalid shape is named by the call itself
+        workspace = _scratch(lib.gdn_cache_attention_workspace_bytes(ref, ragged), dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.gdn_cache_attention(ref, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                 cache_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else float(scale),
+                                 int(window), o.data_ptr(), _addr(workspace), nbytes, stream)
+    if st:
+        _check(st)
+    return o
+
+
+def gdn_cache_copy_pages(k_cache, v_cache, src_pages, dst_pages):
+    """Copies page src_pages[g, j] to page dst_pages[g, j] in both caches (int32, of one shape, [W] or [G, W] with W
+    up to 64), as when a beam takes over the last, partly filled page of its parent.  Within a row of entries all
+    reads come before all writes; a page that one row writes must not be read or written by another.  Negative
+    numbers copy nothing."""
+    lib = load_library()
+    dev = k_cache.device
+    _need(k_cache, "k_cache", None, dev)
+    _need(v_cache, "v_cache", k_cache.dtype, dev)
+    _need(src_pages, "src_pages", torch.int32, dev)
+    _need(dst_pages, "dst_pages", torch.int32, dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_pages, Hkv, page_size, d] of one shape")
+    if src_pages.dim() not in (1, 2) or dst_pages.shape != src_pages.shape:
+        raise ValueError(f"src_pages has shape {tuple(src_pages.shape)}, dst_pages {tuple(dst_pages.shape)}")
+    G, W = (1, *src_pages.shape) if src_pages.dim() == 1 else src_pages.shape
+    rows, apart = k_cache.shape[0], v_cache.data_ptr() - k_cache.data_ptr()
+    if rows == 0 or src_pages.numel() == 0:
+        return
+    row = k_cache.numel() // rows * k_cache.element_size()
+    _, ref = _descriptor(gdn_reorder_shape, (2, apart, apart, rows, rows, row, 0, G, W))
+    stream = _on_gpu(dev)
+    st = lib.gdn_state_reorder(ref, k_cache.data_ptr(), k_cache.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(),
+                               stream)
+    if st:
+        _check(st)
+
+
+def gdn_beam_workspace_bytes(shape: gdn_beam_shape) -> int:
+    """Bytes gdn_beam_select needs for this shape."""
+    n = load_library().gdn_beam_workspace_bytes(ctypes.byref(shape))
+    if n == ctypes.c_size_t(-1).value:
+        _check(GDN_ERR_INVALID_ARG)
+    return int(n)
+
+
+def gdn_beam_select(logits, scores, *, beams=None, finished=None, eos_token=-1, pad_token=0, tokens=None, parents=None,
+                    new_scores=None, new_finished=None, workspace=None):
+    """The best ``beams`` (None: W) continuations of W beams in each of B searches, by score + log softmax(logits).
+
+    logits [B, W, V] (rows may be padded, evenly spaced), scores fp32 [B, W], finished bool [B, W] or None: a finished
+    beam goes on with pad_token at its score.  Returns (tokens int32, parents int32, scores fp32, finished bool), each
+    [B, beams], best first, ties to the lowest parent, then the lowest token; places that are left hold -1, -1,
+    -infinity, True."""
+    lib = load_library()
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, W, V]")
+    dev, dtype = logits.device, logits.dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    B, W, V = logits.shape
+    K = W if beams is None else int(beams)
+    row = _rows3(logits, "logits", B, W, V, dtype, dev)
+    _need(scores, "scores", torch.float32, dev)
+    if scores.shape != (B, W):
+        raise ValueError(f"scores has shape {tuple(scores.shape)}, expected {(B, W)}")
+    if finished is not None:
+        _need(finished, "finished", torch.bool, dev)
+        if finished.shape != (B, W):
+            raise ValueError(f"finished has shape {tuple(finished.shape)}, expected {(B, W)}")
+    if K < 1:
+        raise ValueError(f"beams={K} < 1")
+    outs = []
+    for t, n, kind in ((tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
+                       (new_scores, "new_scores", torch.float32), (new_finished, "new_finished", torch.bool)):
+        if t is None:
+            t = torch.empty((B, K), dtype=kind, device=dev)
+        else:
+            _need(t, n, kind, dev)
+            if t.shape != (B, K):
+                raise ValueError(f"{n} has shape {tuple(t.shape)}, expected {(B, K)}")
+        outs.append(t)
+    for name, x in (("eos_token", eos_token), ("pad_token", pad_token)):
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError(f"{name}={x} does not fit 32 bits")
+    _, ref = _descriptor(gdn_beam_shape, (B, W, K, V, _DTYPES[dtype], int(eos_token), int(pad_token), row))
+    stream = _on_gpu(dev)
+    if workspace is None:
+        workspace = _scratch(lib.gdn_beam_workspace_bytes(ref), dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib.gdn_beam_select(ref, logits.data_ptr(), scores.data_ptr(), _addr(finished), outs[0].data_ptr(),
+                             outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), _addr(workspace), nbytes,
+                             stream)
+    if st:
+        _check(st)
+    return tuple(outs)
+
+
+def gdn_state_reorder(state, parents, *, axis=0, out=None):
+    """Rows of a state moved after a beam selection: row b * K + j of ``out`` becomes row b * W + parents[b, j] of
+    ``state``, bitwise.  parents int32 [B, K]; the state has B * W rows along ``axis`` (the axes before it are
+    layers) and any dtype, its rows a multiple of 16 bytes.  ``out`` may be the state itself (K = W).  Parents outside
+    of [0, W) leave their row of ``out`` as it is.  Returns out."""
+    lib = load_library()
+    dev = state.device
+    _need(state, "state")
+    _need(parents, "parents", torch.int32, dev)
+    if parents.dim() != 2:
+        raise ValueError(f"parents must be [B, K], got shape {tuple(parents.shape)}")
+    if not 0 <= axis < state.dim():
+        raise ValueError(f"axis={axis} of a state with {state.dim()} axes")
+    shape, (B, K) = state.shape, parents.shape
+    rows = shape[axis]
+    if rows % B != 0 if B else rows != 0:
+        raise ValueError(f"state has {rows} rows for {B} searches")
+    want = (*shape[:axis], B * K, *shape[axis + 1:])
+    if out is None:
+        out = torch.empty(want, dtype=state.dtype, device=dev)
+    else:
+        _need(out, "out", state.dtype, dev)
+        if out.shape != want:
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {want}")
+    if parents.numel() == 0 or state.numel() == 0:
+        return out
+    layers = math.prod(shape[:axis])
+    row = state.numel() // (layers * rows) * state.element_size()
+    if row % 16 != 0:
+        raise ValueError(f"a row of {row} bytes is not a multiple of 16")
+    _, ref = _descriptor(gdn_reorder_shape, (layers, rows * row, B * K * row, rows, B * K, row, rows // B, B, K))
+    stream = _on_gpu(dev)
+    st = lib.gdn_state_reorder(ref, state.data_ptr(), out.data_ptr(), parents.data_ptr(), None, stream)
+    if st:
+        _check(st)
+    return out
+
+
 def gdn_profile_enable(on: bool = True) -> None:
     """Turn per-kernel HIP-event timing inside the library on or off."""
     _check(load_library().gdn_profile_enable(int(bool(on))))
@@ -776,7 +1124,7 @@ def gdn_profile_enable(on: bool = True) -> None:
 def gdn_profile_collect() -> dict:
     """{kernel name: (launches, total ms)} for the kernels timed since the last collect."""
     lib = load_library()
-    n = 16
+    n = 32
     names = (ctypes.c_char_p * n)()
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int32 * n)()
@@ -790,4 +1138,6 @@ __all__ = ["gdn_profile_enable", "gdn_profile_collect", "load_library", "GdnErro
            "gdn_prefill_chunked_ex", "gdn_recurrent_step_ex", "Prologue", "gdn_prologue",
            "gdn_recurrent_step", "gdn_replay_state_updates", "gdn_state_snapshot", "gdn_linear_workspace_bytes",
            "gdn_linear_prefill", "gdn_linear_step", "gdn_verify_drafts", "gdn_verify_shape", "gdn_block_norm",
-           "gdn_norm_shape", "EXPORTED", "LIB_PATH"]
+           "gdn_norm_shape", "gdn_cache_append", "gdn_cache_attention_workspace_bytes", "gdn_cache_attention",
+           "gdn_cache_copy_pages", "gdn_beam_workspace_bytes", "gdn_beam_select", "gdn_state_reorder",
+           "gdn_cache_shape", "gdn_append_shape", "gdn_beam_shape", "gdn_reorder_shape", "EXPORTED", "LIB_PATH"]

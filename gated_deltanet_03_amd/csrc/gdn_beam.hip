@@ -1,0 +1,367 @@
+// The K best continuations of a beam search: log softmax, scores and selection over beams and vocabulary.
+//
+//   c(w, v) = (score_w - log sum_u exp(x_wu - m_w)) + (x_wv - m_w),   m_w = max_u x_wu
+//
+// Bound by reading the logits once.  beam_part_kernel: a workgroup takes a segment of one row into registers, and
+// leaves its maximum, its sum of exponentials against that maximum, and its K largest entries in order: within a beam
+// that is the order of the logits, whatever the sum turns out to be.  beam_join_kernel: a workgroup for each search
+// joins the segments' sums and selects among the K * segments * W entries that are left.
+//
+// Selection: the K-th largest of a wave's 64 lane maxima, found by bisection over the bits with ballots, is a bound
+// that at least K entries reach; the entries that reach the highest wave's bound go to a list in LDS, and an
+// entry's rank is the number of entries before it.  Lists that do not fit (very many equal entries) are taken one
+// maximum at a time.
+//
+// Sums of exponentials: 2^(t log2 e) with the product's own rounding error added back, so that what is left is the
+// rounding of v_exp_f32, which averages out over a row; terms are added in 64 bits.
+#include <algorithm>
+
+#include "gdn_cache_internal.h"
+#include "gdn_rows.h"
+
+namespace gdn {
+
+constexpr int kThreads = 256, kList = 1024;
+
+// Floats as integers of the same order (-0 as 0, NaN above or below everything).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ (~(uint32_t)((int32_t)u >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unordered64(uint64_t u) {
+  return __builtin_bit_cast(double, u ^ (~(uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull));
+}
+
+// The k-th largest of the lanes' values (1 <= k <= 64).
+__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t at = t | (1u << b);
+    if (__popcll(__ballot(v >= at)) >= k) t = at;
+  }
+  return t;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const uint32_t o = __shfl_xor(v, m);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const uint64_t o = __shfl_xor(v, m);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// exp(t), t <= 0, to the rounding of v_exp_f32; 0 from -150 (2^-216) down, -infinity among it
+__device__ __forceinline__ float exp_terms(float t) {
+  t = fmaxf(t, -150.f);
+  const float hi = t * 1.44269504f;
+  const float lo = fmaf(t, 1.44269504f, -hi) + t * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return fmaf(e, 0.693147181f * lo, e);
+}
+
+// Entries of a segment as keys: the logit's order, then the lower index first.
+__device__ __forceinline__ uint64_t entry_key(float x, int v) { return (uint64_t)ordered(x) << 32 | (uint32_t)~v; }
+
+// NV 16-byte vectors a thread: NV * 256 * (16 / sizeof(T)) entries a segment.
+template <typename T, int NV>
+__global__ __launch_bounds__(kThreads) void beam_part_kernel(SelectArgs p, int64_t row0) {
+  constexpr int E = Vec16<T>::N;
+  __shared__ uint64_t list[kList];
+  __shared__ uint32_t wave_top[4], wave_kth[4];
+  __shared__ double wave_sum[4];
+  __shared__ int bad[4], count;
+  __shared__ uint64_t top_key[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = row0 + blockIdx.y;
+  const int seg = blockIdx.x, v0 = seg * p.segment;
+  if (p.finished && p.finished[row]) return;      // the join reads nothing of it
+  const T* x = static_cast<const T*>(p.x) + row * p.row_stride;
+  Vec16<T> q[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int v = v0 + (j * kThreads + tid) * E;
+    if (v + E <= p.V) {
+      __builtin_memcpy(q[j].e, x + v, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) q[j].e[i] = v + i < p.V ? x[v + i] : Elem<T>::from_f(-INFINITY);
+    }
+  }
+  if (tid == 0) count = 0;
+  float top = -INFINITY;
+  bool wrong = false;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float f = q[j].f(i);
+      wrong |= !(f < INFINITY);                  // NaN or +infinity
+      top = fmaxf(top, f);
+    }
+  }
+  const uint32_t mine = ordered(top);
+  const uint32_t kth = kth_of_lanes(mine, p.K), wtop = wave_max(mine);
+  const bool wave_wrong = __ballot(wrong) != 0;
+  if (lane == 0) wave_top[wave] = wtop, wave_kth[wave] = kth, bad[wave] = wave_wrong;
+  __syncthreads();
+  uint32_t m = wave_top[0], bound = wave_kth[0];
+  bool any = bad[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    m = wave_top[w] > m ? wave_top[w] : m;
+    bound = wave_kth[w] > bound ? wave_kth[w] : bound;
+    any |= bad[w] != 0;
+  }
+  const int64_t at = row * p.segments + seg;
+  const float most = unordered(m);
+  if (any || most == -INFINITY) {                // no entries; NaN tells the join that the beam is absent
+    if (tid < p.K) p.best[at * p.K + tid] = 0;
+    if (tid == 0) p.seg_max[at] = any ? NAN : -INFINITY, p.seg_sum[at] = 0.0;
+    return;
+  }
+  const uint32_t void_key = ordered(-INFINITY);
+  if (bound <= void_key) bound = void_key + 1;   // -infinity is no entry
+  double sum = 0.0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float f = q[j].f(i);
+      sum += (double)exp_terms(f - most);
+      if (ordered(f) >= bound) {
+        const int n = atomicAdd(&count, 1);
+        if (n < kList) list[n] = entry_key(f, v0 + (j * kThreads + tid) * E + i);
+      }
+    }
+  }
+  sum = wave_sum64(sum);
+  if (lane == 0) wave_sum[wave] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    p.seg_max[at] = most;
+    p.seg_sum[at] = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+  }
+  const int n = count;
+  uint64_t* best = p.best + at * p.K;
+  if (n <= kList) {
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t k = list[i];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += list[o] > k;
+      if (rank < p.K) best[rank] = k;
+    }
+    if (tid >= n && tid < p.K) best[tid] = 0;
+    return;
+  }
+  uint64_t last = ~0ull;                         // one maximum below the last one at a time
+  for (int r = 0; r < p.K; ++r) {
+    uint64_t k = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const uint64_t e = entry_key(q[j].f(i), v0 + (j * kThreads + tid) * E + i);
+        if (e < last && e > k && (uint32_t)(e >> 32) > void_key) k = e;
+      }
+    }
+    k = wave_max64(k);
+    if (lane == 0) top_key[wave] = k;
+    __syncthreads();
+    k = top_key[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) k = top_key[w] > k ? top_key[w] : k;
+    if (tid == 0) best[r] = k;
+    last = k;
+    __syncthreads();
+  }
+}
+
+// One workgroup a search.
+__global__ __launch_bounds__(kThreads) void beam_join_kernel(SelectArgs p) {
+  __shared__ double start[64];                   // score minus log of the sum; NaN: absent
+  __shared__ double high[64];                    // the maximum, apart: the log would drown in one of -1e38
+  __shared__ uint8_t done[64];
+  __shared__ uint64_t key[kList];
+  __shared__ uint32_t from[kList];
+  __shared__ uint32_t wave_kth[4];
+  __shared__ int count;
+  __shared__ uint64_t top_key[4];
+  __shared__ uint32_t top_from[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t b = blockIdx.x;
+  if (tid == 0) count = 0;
+  // sums: a group of lanes a beam
+  for (int w = wave; w < p.W; w += 4) {
+    const int64_t row = b * p.W + w;
+    const float score = p.scores[row];
+    const bool fin = p.finished && p.finished[row];
+    double log_sum = 0.0;
+    float m = -INFINITY;
+    bool wrong = !(fabsf(score) < INFINITY);
+    if (!fin) {
+      for (int s = lane; s < p.segments; s += 64) {
+        const float f = p.seg_max[row * p.segments + s];
+        wrong |= f != f;
+        m = fmaxf(m, f);
+      }
+      m = unordered(wave_max(ordered(m)));
+      double sum = 0.0;
+      for (int s = lane; s < p.segments; s += 64) {
+        const float f = p.seg_max[row * p.segments + s];
+        if (f > -INFINITY) sum += p.seg_sum[row * p.segments + s] * exp((double)f - (double)m);
+      }
+      sum = wave_sum64(sum);
+      wrong = __ballot(wrong) != 0 || m == -INFINITY;
+      log_sum = log(sum);
+    }
+    if (lane == 0) {
+      start[w] = wrong ? (double)NAN : (double)score - log_sum;
+      high[w] = m;
+      done[w] = fin;
+    }
+  }
+  __syncthreads();
+
+  // candidate i: entry i % K of segment (i / K) % segments of beam i / (K * segments)
+  const int per = p.K * p.segments, all = per * p.W;
+  auto candidate = [&](int i, uint64_t& k, uint32_t& f) {
+    const int w = i / per, r = i - w * per;
+    k = 0;
+    f = 0;
+    const double s = start[w];
+    if (s != s) return;
+    if (done[w]) {
+      if (r != 0) return;
+      k = ordered64(s);
+      f = (uint32_t)~((w << 24) | p.pad);
+      return;
+    }
+    const uint64_t e = p.best[(b * p.W + w) * per + r];
+    if (e == 0) return;
+    k = ordered64(s + ((double)unordered((uint32_t)(e >> 32)) - high[w]));
+    f = (uint32_t)~((w << 24) | (int)~(uint32_t)e);   // token below 2^24, beam below 2^6: lower flat index, larger f
+  };
+  uint32_t mine = 0;                             // upper halves: rounded down, so still in order
+  for (int i = tid; i < all; i += kThreads) {
+    uint64_t k;
+    uint32_t f;
+    candidate(i, k, f);
+    const uint32_t h = (uint32_t)(k >> 32);
+    mine = h > mine ? h : mine;
+  }
+  const uint32_t kth = kth_of_lanes(mine, p.K);
+  if (lane == 0) wave_kth[wave] = kth;
+  __syncthreads();
+  uint32_t bound = wave_kth[0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) bound = wave_kth[w] > bound ? wave_kth[w] : bound;
+  for (int i = tid; i < all; i += kThreads) {
+    uint64_t k;
+    uint32_t f;
+    candidate(i, k, f);
+    if (k != 0 && (uint32_t)(k >> 32) >= bound) {
+      const int n = atomicAdd(&count, 1);
+      if (n < kList) key[n] = k, from[n] = f;
+    }
+  }
+  __syncthreads();
+  const int n = count;
+  auto put = [&](int r, uint64_t k, uint32_t f) {
+    const int64_t o = b * p.K + r;
+    const uint32_t u = ~f;
+    const int w = (int)(u >> 24), v = (int)(u & 0xffffff);
+    p.tokens[o] = k ? v : -1;
+    p.parents[o] = k ? w : -1;
+    p.new_scores[o] = k ? (float)unordered64(k) : -INFINITY;
+    p.new_finished[o] = !k || done[w] || v == p.eos;
+  };
+  if (n <= kList) {
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t k = key[i];
+      const uint32_t f = from[i];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += key[o] > k || (key[o] == k && from[o] > f);
+      if (rank < p.K) put(rank, k, f);
+    }
+    if (tid >= n && tid < p.K) put(tid, 0, ~0u);
+    return;
+  }
+  uint64_t last = ~0ull;
+  uint32_t last_f = ~0u;
+  for (int r = 0; r < p.K; ++r) {
+    uint64_t k = 0;
+    uint32_t f = 0;
+    for (int i = tid; i < all; i += kThreads) {
+      uint64_t ki;
+      uint32_t fi;
+      candidate(i, ki, fi);
+      if ((ki < last || (ki == last && fi < last_f)) && (ki > k || (ki == k && fi > f))) k = ki, f = fi;
+    }
+    const uint64_t wk = wave_max64(k);
+    const uint32_t wf = wave_max(k == wk ? f : 0);
+    if (lane == 0) top_key[wave] = wk, top_from[wave] = wf;
+    __syncthreads();
+    k = top_key[0], f = top_from[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+      if (top_key[w] > k || (top_key[w] == k && top_from[w] > f)) k = top_key[w], f = top_from[w];
+    if (tid == 0) put(r, k, f);
+    last = k, last_f = f;
+    __syncthreads();
+  }
+}
+
+template <typename T>
+static hipError_t launch_select_t(const SelectArgs& a, hipStream_t s) {
+  constexpr int E = Vec16<T>::N;
+  prof_begin(K_SELECT_PART, s);
+  const int64_t rows = (int64_t)a.B * a.W;
+  const int64_t most = std::min<int64_t>(65535, kLaunchThreads / kThreads / a.segments);
+  for (int64_t r = 0; r < rows; r += most) {
+    const dim3 grid((unsigned)a.segments, (unsigned)std::min(most, rows - r));
+    if (a.segment == 2048) hipLaunchKernelGGL((beam_part_kernel<T, 8 / E>), grid, dim3(kThreads), 0, s, a, r);
+    else hipLaunchKernelGGL((beam_part_kernel<T, 32 / E>), grid, dim3(kThreads), 0, s, a, r);
+  }
+  prof_end(K_SELECT_PART, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  prof_begin(K_SELECT_JOIN, s);
+  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+  prof_end(K_SELECT_JOIN, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_select(DType dt, const SelectArgs& a, hipStream_t s) {
+  switch (dt) {
+    case DType::F32: return launch_select_t<float>(a, s);
+    case DType::F16: return launch_select_t<_Float16>(a, s);
+    case DType::BF16: return launch_select_t<__bf16>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gdn

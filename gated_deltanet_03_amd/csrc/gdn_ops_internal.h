@@ -70,8 +70,11 @@ struct NormArgs {
 constexpr KernelId K_LIN_STATE = KernelId(kNumKernels), K_LIN_OUT = KernelId(kNumKernels + 1),
                    K_LIN_WHOLE = KernelId(kNumKernels + 2), K_LIN_STEP = KernelId(kNumKernels + 3),
                    K_VERIFY_SUM = KernelId(kNumKernels + 4), K_VERIFY_DRAW = KernelId(kNumKernels + 5),
-                   K_VERIFY_ROW = KernelId(kNumKernels + 6), K_NORM = KernelId(kNumKernels + 7);
-constexpr int kAllKernels = kNumKernels + 8;
+                   K_VERIFY_ROW = KernelId(kNumKernels + 6), K_NORM = KernelId(kNumKernels + 7),
+                   K_APPEND = KernelId(kNumKernels + 8), K_ATTEND = KernelId(kNumKernels + 9),
+                   K_ATTEND_JOIN = KernelId(kNumKernels + 10), K_SELECT_PART = KernelId(kNumKernels + 11),
+                   K_SELECT_JOIN = KernelId(kNumKernels + 12), K_REORDER = KernelId(kNumKernels + 13);
+constexpr int kAllKernels = kNumKernels + 14;
 
 hipError_t launch_linear_prefill_f32(const LinearArgs& a, hipStream_t s);
 hipError_t launch_linear_prefill_f16(const LinearArgs& a, hipStream_t s);

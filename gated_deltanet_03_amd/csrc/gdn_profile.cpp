@@ -19,7 +19,10 @@ const char* const kNames[kAllKernels] = {"chunk_plan_kernel", "chunk_prep_kernel
                                           "recurrent_step_kernel", "replay_kernel", "copy_kernel",
                                           "linear_chunk_kernel (state)", "linear_chunk_kernel (outputs)",
                                           "linear_chunk_kernel (whole)", "linear_step_kernel", "verify_sum_kernel",
-                                          "verify_draw_kernel", "verify_row_kernel", "block_norm_kernel"};
+                                          "verify_draw_kernel", "verify_row_kernel", "block_norm_kernel",
+                                          "cache_append_kernel", "cache_attention_kernel",
+                                          "cache_attention_join_kernel", "beam_part_kernel", "beam_join_kernel",
+                                          "state_reorder_kernel"};
 
 struct Rec {
   int id;

@@ -442,6 +442,167 @@ gdn_status gdn_block_norm(const gdn_norm_shape* shape, const void* y, const void
                           void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Attention layers between the delta-rule blocks: keys and values in pages
+ * ---------------------------------------------------------------------------
+ *
+ * k_cache, v_cache  [num_pages, Hkv, page_size, d] dtype: the page_size rows of one
+ *                   head in one page are contiguous.
+ * block_table       int32 [N, max_pages]: key j of sequence s is row j % page_size of
+ *                   page block_table[s, j / page_size].  A number outside
+ *                   [0, num_pages) is no page: what is appended there is dropped, and
+ *                   the keys there are absent (masked).
+ * cache_lens        int32 [N]: keys of each sequence, its new tokens included.  New
+ *                   token i of the L_s of sequence s has the place
+ *                   cache_lens[s] - L_s + i.
+ * cu_seqlens        int32 [N+1] as above (packed rows; those behind cu_seqlens[N] are
+ *                   neither read nor written), or NULL: T tokens for each of N rows.
+ * d in {32, 64, 128, 256}; page_size a multiple of 16 up to 1024; max_pages * page_size
+ * up to 2^26; all pointers 16-byte aligned, token strides multiples of 16 bytes
+ * (cu_seqlens, cache_lens, block_table, positions, pair_axis, inv_freq: 4-byte).
+ */
+typedef struct {
+  int32_t N;            /* sequences */
+  int32_t T;            /* tokens per sequence, or with cu_seqlens the number of packed rows */
+  int32_t Hq, Hkv;      /* query heads, a multiple of the key/value heads */
+  int32_t d;            /* head dim of queries, keys and values */
+  int32_t dtype;        /* gdn_dtype of all of them */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;    /* columns of block_table */
+} gdn_cache_shape;
+
+/*
+ * Appends new keys and values to their pages, the keys (and the queries, into
+ * q_out) rotated by their positions on the way:
+ *
+ *   a_j = position * inv_freq[j],  j = 0 .. rotary/2 - 1
+ *   (x1, x2) -> (x1 cos a_j - x2 sin a_j, x1 sin a_j + x2 cos a_j)
+ *   x1, x2 = elements j, j + rotary/2, or with `interleaved` 2j, 2j + 1;
+ *   the elements from `rotary` on stay as they are.
+ *
+ * The angle is reduced in 64 bits, its sine and cosine and the rotation are taken
+ * in 32, rounded once.
+ *
+ *  k, v       [tokens, Hkv, d] at their token strides (elements), as slices of one
+ *             projection's rows have them; q [tokens, Hq, d] or NULL.
+ *  q_out      [tokens, Hq, d] contiguous, required exactly with q; may be q itself
+ *             where q is contiguous.
+ *  inv_freq   fp32 [rotary/2], or NULL (rotary = 0): keys are appended as they are.
+ *  positions  int32 [axes, tokens], or NULL: the token's place in the cache.
+ *  pair_axis  int32 [rotary/2]: the axis (time, height, width, ...) whose position
+ *             turns pair j, clamped to [0, axes); NULL: axis 0.
+ * rotary is even, 0 <= rotary <= d.  Tokens whose place is outside of the table or
+ * on no page are not appended (their q_out is written).  Two tokens on one place:
+ * unspecified which stays.
+ */
+typedef struct {
+  int64_t q_token_stride, k_token_stride, v_token_stride;
+  int32_t rotary;
+  int32_t interleaved;
+  int32_t axes;         /* rows of positions, 1 .. 8 */
+} gdn_append_shape;
+
+gdn_status gdn_cache_append(const gdn_cache_shape* shape, const gdn_append_shape* append, const void* q,
+                            const void* k, const void* v, const float* inv_freq, const int32_t* positions,
+                            const int32_t* pair_axis, const int32_t* block_table, const int32_t* cache_lens,
+                            const int32_t* cu_seqlens, void* q_out, void* k_cache, void* v_cache, void* stream);
+
+/*
+ * Attention of the new tokens over the cache, causal:
+ *
+ *   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale * q_i . k_j)
+ *   over the keys j of the sequence with  p_i - window < j <= p_i  (window > 0) or
+ *   j <= p_i (window = 0), p_i the token's place; query head h reads key head
+ *   h / (Hq/Hkv).
+ *
+ * A token that sees no key, and one whose weights are all 0, gets 0.  What lies in
+ * masked places (infinities, NaN, pages never written) touches nothing.
+ *
+ * Precision: scores, the running maximum and all sums in fp32, o rounded once; for
+ * 16-bit inputs the weights are rounded to the input type (against a running
+ * maximum, at most 2^8) as operands of their product with v.
+ *
+ *  q, o       [tokens, Hq, d]; q at q_token_stride (elements), o contiguous.
+ *  scale      finite and > 0.
+ *  workspace  gdn_cache_attention_workspace_bytes() bytes, 16-byte aligned, contents
+ *             on entry ignored; may be NULL where that is 0.  Long sequences are split
+ *             over their keys; the parts are joined in a fixed order.
+ */
+size_t gdn_cache_attention_workspace_bytes(const gdn_cache_shape* shape, int32_t ragged);   /* (size_t)-1 if invalid */
+
+gdn_status gdn_cache_attention(const gdn_cache_shape* shape, const void* q, int64_t q_token_stride,
+                               const void* k_cache, const void* v_cache, const int32_t* block_table,
+                               const int32_t* cache_lens, const int32_t* cu_seqlens, float scale, int32_t window,
+                               void* o, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Beam search: the K best continuations of W beams for each of B searches.
+ *
+ *   c(w, v) = scores[b,w] + logits[b,w,v] - log sum_u exp(logits[b,w,u])
+ *
+ * of an unfinished beam w and every token v; a finished beam has one continuation,
+ * pad_token, with its score unchanged.  The K largest in descending order, ties to
+ * the lowest w, then the lowest v.
+ *
+ * exp in fp32 (2^-23 of a term), sums, logarithm and scores in 64 bits; new_scores
+ * rounded once to fp32.  Two continuations of different beams nearer than about
+ * 2^-24 may change places.  Logits of -infinity are no continuations.  A beam counts
+ * as absent if its score is not finite, or (unfinished) a logit is NaN or +infinity,
+ * or all are -infinity.  Places that are left have token -1, parent -1, score
+ * -infinity and count as finished.
+ *
+ *  logits        [B, W, V] dtype, row r = b*W+w at row_stride * r (the alignment of
+ *                their type is enough)
+ *  scores        fp32 [B, W]            finished  uint8 [B, W] or NULL (none)
+ *  tokens, parents  int32 [B, K]        new_scores  fp32 [B, K]
+ *  new_finished  uint8 [B, K]: finished[parent], or token == eos_token (-1: none)
+ *  workspace     gdn_beam_workspace_bytes() bytes, 16-byte aligned, contents on entry
+ *                ignored
+ * 1 <= W <= 64, 1 <= K <= 64, V <= 2^24; new_scores and new_finished must not be
+ * scores and finished.
+ */
+typedef struct {
+  int32_t B, W, K, V;
+  int32_t dtype;
+  int32_t eos_token, pad_token;   /* pad_token in [0, V) */
+  int64_t row_stride;             /* >= V */
+} gdn_beam_shape;
+
+size_t gdn_beam_workspace_bytes(const gdn_beam_shape* shape);   /* (size_t)-1 if invalid */
+
+gdn_status gdn_beam_select(const gdn_beam_shape* shape, const void* logits, const float* scores,
+                           const uint8_t* finished, int32_t* tokens, int32_t* parents, float* new_scores,
+                           uint8_t* new_finished, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves rows (states, convolution windows, pages) after a beam selection:
+ *
+ *   dst[l, d] = src[l, s]  for every layer l and every entry (g, j) of G groups of W
+ *   s = src_index[g, j] (+ g * src_group),  d = dst_index[g, j], or g * W + j without
+ *
+ * Bitwise.  Within a group all reads come before all writes, so dst may be src: the
+ * rows of one group may be permuted, repeated and dropped in place.  A row that one
+ * group writes must not be read or written by another, and no row is written twice.
+ * Entries whose index is outside of [0, src_group) (src_group > 0), or whose row is
+ * outside of [0, src_rows) or [0, dst_rows), write nothing.
+ *
+ *  src, dst     layers at their strides in bytes (multiples of 16, also negative), rows of
+ *               row_bytes (a multiple of 16); 16-byte aligned.  dst is src (with equal
+ *               strides) or apart from it.
+ *  src_index, dst_index  int32 [G, W], W <= 64
+ */
+typedef struct {
+  int64_t layers, src_layer_stride, dst_layer_stride;
+  int64_t src_rows, dst_rows, row_bytes;
+  int64_t src_group;    /* rows from one group's index 0 to the next's; 0: indexes count from the first row */
+  int32_t G, W;
+} gdn_reorder_shape;
+
+gdn_status gdn_state_reorder(const gdn_reorder_shape* shape, const void* src, void* dst, const int32_t* src_index,
+                             const int32_t* dst_index, void* stream);
+
+/*
  * Measurement support (not part of the method).  gdn_profile_enable(1) makes
  * every entry point bracket each kernel it launches with a pair of hipEvents
  * recorded on the launch stream; gdn_profile_collect() waits for all pending
