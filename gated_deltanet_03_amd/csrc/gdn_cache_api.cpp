@@ -55,7 +55,8 @@ gdn_status check_cache(const gdn_cache_shape* sh, bool ragged, int64_t* tokens) 
                 (long long)sh->max_pages * sh->page_size);
   if ((int64_t)sh->num_pages * sh->page_size > 0x7fffffffLL / sh->Hkv)
     return fail(GDN_ERR_UNSUPPORTED, "the cache has more than 2^31-1 rows");
-  if (sh->N > (1 << 20) || sh->Hq > 65535) return fail(GDN_ERR_UNSUPPORTED, "N=%d exceeds 2^20 or Hq=%d 65535", sh->N, sh->Hq);
+  if (sh->N > (1 << 20) || sh->Hq > 65535 || sh->Hq / sh->Hkv > 256)
+    return fail(GDN_ERR_UNSUPPORTED, "N=%d exceeds 2^20, Hq=%d 65535 or Hq/Hkv 256", sh->N, sh->Hq);
   *tokens = ragged ? (int64_t)sh->T : (int64_t)sh->N * sh->T;
   if (*tokens > (1LL << 30) || *tokens * sh->Hq > 0x7fffffffLL)
     return fail(GDN_ERR_UNSUPPORTED, "%lld tokens of %d heads exceed 2^30 tokens or 2^31-1 rows", (long long)*tokens, sh->Hq);
@@ -107,34 +108,28 @@ CacheArgs cache_args(const gdn_cache_shape* sh, const int32_t* table, const int3
   return c;
 }
 
-// How the attention of a call is cut: rows of a tile, (tile, slice) pairs of a head.
+// How the attention of a call is cut: rows of a tile, shares of a head's work (0: a tile each).
 struct Plan {
-  int32_t few, slices, rows;
-  int64_t units;
+  int32_t few, shares, rows;
+  int64_t tiles;
 };
 
-// Slices of keys are aimed at when the tiles alone leave workgroups idle: as many as the card holds at once.
+// As many workgroups as the card holds at once share the work evenly; sequences that are sure to be short are not cut.
 Plan attention_plan(const gdn_cache_shape* sh, int64_t tokens, bool ragged) {
   const int64_t G = sh->Hq / sh->Hkv, rows = tokens * G;
   Plan p{};
   p.few = rows <= (int64_t)kFewRows * sh->N;
   p.rows = p.few ? kFewRows : kManyRows;
-  const int64_t tiles = ragged ? rows / p.rows + sh->N : sh->N * (((int64_t)sh->T * G + p.rows - 1) / p.rows);
-  const int64_t rb = (int64_t)sh->d * elem_size(sh->dtype);
-  const int64_t lds = p.few ? (rb >= 1024 ? 2 : 4) * 64 * rb : 4 * (rb >= 1024 ? 32 : 64) * rb;
-  const int64_t at_once = 256 * std::max<int64_t>(1, std::min<int64_t>(4, 163840 / lds));
-  const bool longer = (int64_t)sh->max_pages * sh->page_size > kSliceKeys;
-  if (longer && (p.few || tiles * sh->Hkv < at_once))
-    p.slices = (int32_t)std::max<int64_t>(2, std::min<int64_t>(kMostSlices, at_once / sh->Hkv));
-  p.units = tiles + p.slices;
+  p.tiles = ragged ? rows / p.rows + sh->N : sh->N * (((int64_t)sh->T * G + p.rows - 1) / p.rows);
+  const int rb = sh->d * (int)elem_size(sh->dtype), at_once = 256 * (p.few ? few_waves(rb) : many_waves(rb));
+  if ((int64_t)sh->max_pages * sh->page_size > (p.few ? kFewKeys : kManyKeys))
+    p.shares = std::max(1, std::min(kMostShares, at_once / sh->Hkv));
   return p;
 }
 
-size_t part_o_bytes(const gdn_cache_shape* sh, const Plan& p) {
-  return p.slices ? (size_t)p.units * sh->Hkv * p.rows * sh->d * 4 : 0;
-}
+size_t part_rows(const gdn_cache_shape* sh, const Plan& p) { return (size_t)2 * p.shares * sh->Hkv * p.rows; }
 size_t plan_bytes(const gdn_cache_shape* sh, const Plan& p) {
-  return p.slices ? part_o_bytes(sh, p) + (size_t)p.units * sh->Hkv * p.rows * 8 : 0;
+  return part_rows(sh, p) * (sh->d + 2) * 4 + (size_t)p.shares * sh->Hkv * 16;
 }
 
 }  // namespace
@@ -233,8 +228,8 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
     const Buf wb = {ws, need, "workspace"};
     if ((st = check_apart(wb, ins, 6)) != GDN_OK || (st = check_apart(wb, &ob, 1)) != GDN_OK) return st;
   }
-  if (plan.units * sh->Hkv > (int64_t)(kLaunchThreads / 256))
-    return fail(GDN_ERR_UNSUPPORTED, "too many (tile, head) pairs (%lld)", (long long)plan.units * sh->Hkv);
+  if ((plan.tiles + plan.shares) * sh->Hkv > (int64_t)(kLaunchThreads / 256))
+    return fail(GDN_ERR_UNSUPPORTED, "too many (tile, head) pairs (%lld)", (long long)plan.tiles * sh->Hkv);
   AttendArgs a{};
   a.c = cache_args(sh, table, lens, cu, tokens);
   a.q = q; a.q_stride = q_stride; a.k_cache = kc; a.v_cache = vc; a.o = o;
@@ -242,9 +237,12 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   a.window = std::min(window, 1 << 30);
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;
-  a.few = plan.few; a.slices = plan.slices; a.units = (int32_t)plan.units;
-  a.part_o = static_cast<float*>(ws);
-  a.part_ml = need ? reinterpret_cast<float*>(static_cast<char*>(ws) + part_o_bytes(sh, plan)) : nullptr;
+  a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles;
+  if (need > 0) {
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = a.part_o + part_rows(sh, plan) * sh->d;
+    a.cuts = a.part_ml + part_rows(sh, plan) * 2;
+  }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const hipError_t e = sh->dtype == GDN_F32   ? launch_attend_f32(a, s)
                        : sh->dtype == GDN_F16 ? launch_attend_f16(a, s)

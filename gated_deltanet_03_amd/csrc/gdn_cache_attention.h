@@ -78,82 +78,208 @@ __device__ __forceinline__ int value_swizzle(int r) {
   else return ((r >> 1) & 1) << 1;
 }
 
-// Which tile, slice of keys and sequence a workgroup has.
-struct Unit {
-  int s, tile, slice, slices;
-  int b, L, lens;        // first token, new tokens, keys of the sequence
+__device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// How the work of one head is laid out.
+//
+// The tiles of all sequences lie on one line, a tile as long as the keys it sees (times G, plus what starting one
+// costs): v_i = first + step * i for tile i of a sequence, exact up to the last block of keys.  The first workgroups take
+// whole tiles, one each; what is left of the line is cut into `shares` even pieces, whatever the sequences' lengths are:
+// the rest of one tile, whole tiles, the beginning of one more.  Pieces that are not whole tiles go to the workspace and
+// are joined.
+//
+// Few rows: everything is cut (each key is read by one workgroup anyway).  Many rows: workgroups that walk one head's
+// keys side by side read them from the cache they share, and pieces that begin anywhere do not (16384 keys of 8 heads,
+// 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole rounds of `shares` tiles stay whole, the last ones
+// of a sequence, which see the most keys, first; with three rounds or more nothing is cut.  Tiles longer than 5/4 of an even
+// share are always cut, so that one long sequence does not outlast all others.
+struct Piece {
+  int s, b, L, lens, tile;
+  int64_t at, length;      // the tile's start and length on the line
 };
 
-// Tiles and keys of sequence s (0 tiles: nothing to do).
-template <int ROWS>
-__device__ __forceinline__ void sequence_size(const AttendArgs& a, int G, int s, int& b, int& L, int& lens, int& tiles,
-                                              int& span) {
-  b = L = lens = tiles = span = 0;
-  if (s < a.c.N) {
-    int e;
-    seq_range(a.c.cu, a.c.T, a.c.total, s, b, e);
-    L = e - b;
-    lens = min(max(a.c.lens[s], -(1 << 30)), 1 << 30);
-    tiles = (int)(((int64_t)L * G + ROWS - 1) / ROWS);
-    const int room = a.c.max_pages * a.c.page_size;
-    span = lens < 0 ? 0 : (lens < room ? lens : room);
-    if (a.window > 0) {   // one tile sees no more than this
-      const int64_t most = (int64_t)a.window + ROWS / G + 1;
-      if (span > most) span = (int)most;
+template <bool FEW>
+struct Line {
+  static constexpr int ROWS = FEW ? kFewRows : kManyRows;
+  const AttendArgs& a;
+  int G;
+  // the 64 sequences from s0 on, one a lane
+  int b, L, lens, tiles;
+  int64_t first, step;
+
+  // i tiles of a sequence.
+  static __device__ __forceinline__ int64_t tiles_length(int64_t first, int64_t step, int64_t i) {
+    return first * i + step * (i * (i - 1) / 2);
+  }
+
+  __device__ __forceinline__ Line(const AttendArgs& args, int G_) : a(args), G(G_) {}
+
+  __device__ __forceinline__ void load(int s) {
+    b = L = lens = tiles = 0;
+    first = step = 0;
+    if (s < a.c.N) {
+      int e;
+      seq_range(a.c.cu, a.c.T, a.c.total, s, b, e);
+      L = e - b;
+      lens = min(max(a.c.lens[s], -(1 << 30)), 1 << 30);
+      tiles = (int)(((int64_t)L * G + ROWS - 1) / ROWS);
+      const int room = a.c.max_pages * a.c.page_size, old = min(max(lens - L, 0), room);
+      first = (int64_t)G * (old + 64) + ROWS;
+      step = ROWS;
+      if (a.window > 0 && a.window < old) first = (int64_t)G * (a.window + 64) + ROWS, step = 0;
     }
   }
-}
 
-// Keys of a slice: the work of all tiles over the slices aimed at, at least kSliceKeys.
-template <int ROWS>
-__device__ __forceinline__ int slice_keys(const AttendArgs& a, int G) {
-  const int lane = threadIdx.x & 63;
-  int64_t all = 0;
-  for (int s = lane; s < a.c.N; s += 64) {
-    int b, L, lens, tiles, span;
-    sequence_size<ROWS>(a, G, s, b, L, lens, tiles, span);
-    all += (int64_t)tiles * span;
+  // Whether the loaded sequence's tiles may stay whole.
+  __device__ __forceinline__ bool may_be_whole(int64_t longest) const {
+    return !FEW && first + step * (tiles - 1) <= longest;
   }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m);
-  const int64_t k = (all + a.slices - 1) / a.slices;
-  return (int)(k < kSliceKeys ? kSliceKeys : (k + 127) / 128 * 128);
-}
 
-// The u-th (sequence, tile, slice) of a head; false past the last one.  The whole wave calls it.
-template <int ROWS>
-__device__ __forceinline__ bool find_unit(const AttendArgs& a, int G, int u, Unit& r) {
-  const int lane = threadIdx.x & 63;
-  const int keys = a.slices ? slice_keys<ROWS>(a, G) : 0x7fffff00;
-  int before = 0;
-  for (int s0 = 0; s0 < a.c.N; s0 += 64) {
-    int b, L, lens, tiles, span;
-    sequence_size<ROWS>(a, G, s0 + lane, b, L, lens, tiles, span);
-    const int slices = span > keys ? (span + keys - 1) / keys : 1, mine = tiles * slices;
-    int upto = mine;
+  static __device__ __forceinline__ int64_t sum(int64_t x) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+    return lane_value(x, 0);
+  }
+  static __device__ __forceinline__ int64_t scan(int64_t x) {
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-      const int o = __shfl_up(upto, m);
-      if (lane >= m) upto += o;
+      const int64_t o = __shfl_up(x, m);
+      if ((int)(threadIdx.x & 63) >= m) x += o;
     }
-    const int total = __builtin_amdgcn_readlane(upto, 63);
-    if (u < before + total) {
-      const int j = __ffsll((unsigned long long)__ballot(u < before + upto)) - 1;
-      const int rest = u - before - (__builtin_amdgcn_readlane(upto, j) - __builtin_amdgcn_readlane(mine, j));
-      r.s = s0 + j;
-      r.b = __builtin_amdgcn_readlane(b, j);
-      r.L = __builtin_amdgcn_readlane(L, j);
-      r.lens = __builtin_amdgcn_readlane(lens, j);
-      r.slices = __builtin_amdgcn_readlane(slices, j);
-      // a sequence's last tiles see the most keys: first
-      r.tile = __builtin_amdgcn_readlane(tiles, j) - 1 - rest / r.slices;
-      r.slice = rest % r.slices;
+    return x;
+  }
+};
+
+// What all workgroups of a call agree on.
+struct Shares {
+  int64_t longest;         // of the tiles that may stay whole
+  int64_t whole;           // tiles that stay whole
+  int64_t rest, share;     // length of the line that is left, and of a share of it
+};
+
+template <bool FEW>
+__device__ __forceinline__ Shares share_out(const AttendArgs& a, int G) {
+  Line<FEW> line(a, G);
+  const int lane = threadIdx.x & 63;
+  Shares r{0, 0, 0, 1};
+  int64_t all = 0;
+  for (int s = 0; s < a.c.N; s += 64) {
+    line.load(s + lane);
+    all += Line<FEW>::sum(line.tiles_length(line.first, line.step, line.tiles));
+  }
+  const int64_t even = (all + a.shares - 1) / a.shares, least = (int64_t)G * (FEW ? kFewKeys : kManyKeys);
+  r.rest = all;
+  if constexpr (!FEW) {
+    r.longest = even + even / 4 > 2 * least ? even + even / 4 : 2 * least;
+    int64_t may = 0, sure = 0;
+    for (int s = 0; s < a.c.N; s += 64) {
+      if (a.c.N > 64) line.load(s + lane);
+      const bool w = line.tiles > 0 && line.may_be_whole(r.longest);
+      may += Line<FEW>::sum(w ? line.tiles : 0);
+      sure += Line<FEW>::sum(w ? 0 : line.tiles);
+    }
+    const int64_t rounds = may / a.shares;
+    r.whole = sure == 0 && (rounds >= 3 || r.longest == 2 * least) ? may : rounds * a.shares;
+    r.whole = min(r.whole, (int64_t)a.tiles);    // (malformed offsets may count more tiles than there is room for)
+    // what is left after them
+    int64_t before = 0;
+    r.rest = 0;
+    for (int s = 0; s < a.c.N; s += 64) {
+      if (a.c.N > 64) line.load(s + lane);
+      const int mine = line.tiles > 0 && line.may_be_whole(r.longest) ? line.tiles : 0;
+      const int64_t upto = before + Line<FEW>::scan(mine);
+      const int64_t kept = min(max(r.whole - (upto - mine), (int64_t)0), (int64_t)mine);
+      r.rest += Line<FEW>::sum(line.tiles_length(line.first, line.step, line.tiles - kept));
+      before = lane_value(upto, 63);
+    }
+  }
+  const int64_t s = (r.rest + a.shares - 1) / a.shares;
+  r.share = s < least ? least : s;
+  return r;
+}
+
+// The whole tile number `pos` (WHOLE), or the sequence and tile at `pos` of what is left.
+template <bool FEW, bool WHOLE>
+__device__ __forceinline__ bool find_piece(const AttendArgs& a, int G, const Shares& sh, int64_t pos, Piece& p) {
+  Line<FEW> line(a, G);
+  int64_t tiles_before = 0, before = 0;
+  for (int s0 = 0; s0 < a.c.N; s0 += 64) {
+    line.load(s0 + (int)(threadIdx.x & 63));
+    int64_t kept = 0;
+    if constexpr (!FEW) {
+      const int mine = line.tiles > 0 && line.may_be_whole(sh.longest) ? line.tiles : 0;
+      const int64_t upto = tiles_before + Line<FEW>::scan(mine);
+      kept = min(max(sh.whole - (upto - mine), (int64_t)0), (int64_t)mine);
+      tiles_before = lane_value(upto, 63);
+    }
+    const int64_t mine = WHOLE ? kept : line.tiles_length(line.first, line.step, line.tiles - kept);
+    const int64_t upto = before + Line<FEW>::scan(mine), total = lane_value(upto, 63);
+    if (pos < total) {
+      const int j = __ffsll((unsigned long long)__ballot(pos < upto)) - 1;
+      const int64_t f = lane_value(line.first, j), st = lane_value(line.step, j);
+      const int64_t start = lane_value(upto - mine, j), rest = pos - start;
+      const int n = __builtin_amdgcn_readlane(line.tiles, j) - (int)lane_value(kept, j);
+      int64_t i;
+      if constexpr (WHOLE) {
+        i = n + lane_value(kept, j) - 1 - rest;
+      } else {
+        if (st == 0) {
+          i = rest / f;
+        } else {        // f i + st i (i - 1) / 2 <= rest, by the quadratic's root
+          const double u = (double)f / (double)st - 0.5;
+          i = (int64_t)(sqrt(u * u + 2.0 * (double)rest / (double)st) - u);
+          i = min(max(i, (int64_t)0), (int64_t)n - 1);
+          while (i > 0 && line.tiles_length(f, st, i) > rest) --i;
+          while (i + 1 < n && line.tiles_length(f, st, i + 1) <= rest) ++i;
+        }
+        i = min(i, (int64_t)n - 1);
+      }
+      p.s = s0 + j;
+      p.b = __builtin_amdgcn_readlane(line.b, j);
+      p.L = __builtin_amdgcn_readlane(line.L, j);
+      p.lens = __builtin_amdgcn_readlane(line.lens, j);
+      p.tile = __builtin_amdgcn_readfirstlane((int)i);
+      p.at = WHOLE ? pos : lane_value(start + line.tiles_length(f, st, i), 0);
+      p.length = WHOLE ? 1 : lane_value(f + st * i, 0);
       return true;
     }
-    before += total;
+    before = total;
   }
   return false;
 }
+
+// The j-th tile, where nothing is cut.
+template <bool FEW>
+__device__ __forceinline__ bool find_tile(const AttendArgs& a, int G, int64_t j, Piece& p) {
+  Line<FEW> line(a, G);
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.c.N; s0 += 64) {
+    line.load(s0 + (int)(threadIdx.x & 63));
+    const int64_t upto = before + Line<FEW>::scan(line.tiles), total = lane_value(upto, 63);
+    if (j < total) {
+      const int k = __ffsll((unsigned long long)__ballot(j < upto)) - 1;
+      p.s = s0 + k;
+      p.b = __builtin_amdgcn_readlane(line.b, k);
+      p.L = __builtin_amdgcn_readlane(line.L, k);
+      p.lens = __builtin_amdgcn_readlane(line.lens, k);
+      p.tile = (int)(lane_value(upto, k) - 1 - j);      // a sequence's last tiles see the most keys: first
+      p.at = j;
+      p.length = 1;
+      return true;
+    }
+    before = total;
+  }
+  return false;
+}
+
+// What the join of a tile cut between workgroups j - 1 and j needs (pieces = 0: no tile that begins in j - 1).
+struct Cut {
+  int b, L, tile, pieces;
+};
 
 template <typename T> struct Op;
 template <> struct Op<__bf16> {
@@ -273,12 +399,12 @@ struct Wave {
                                            ((col & 3) << 2));
   }
 
-  // Two weights of the lane's keys 8 s .. 8 s + 7, rounded to T.
+  // The weights of the lane's keys 8 s .. 8 s + 7, rounded to T.
   static __device__ __forceinline__ uint4 weight_operand(const f32x16& p, int s) {
-    union { T e[8]; uint4 u; } w;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w.e[j] = Elem<T>::from_f(p[8 * s + j]);
-    return w.u;
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    const f32x8 x = {p[8 * s], p[8 * s + 1], p[8 * s + 2], p[8 * s + 3],
+                     p[8 * s + 4], p[8 * s + 5], p[8 * s + 6], p[8 * s + 7]};
+    return __builtin_bit_cast(uint4, __builtin_convertvector(x, typename Op<T>::V));
   }
 
   // o += V^T P^T over 32 keys.
@@ -326,38 +452,17 @@ struct Wave {
     return rows;
   }
 
-  // The same for tiles of which a query may see a part, with infinities or NaN in rows `bad`: those rows enter the
-  // products as zeros and are added key by key to the queries that see them.
-  __device__ __forceinline__ void add_values_apart(const unsigned char* V, int r0, const f32x16& p, uint32_t bad,
-                                                   int key0, int gone) {
+  // Rows of values with infinities or NaN, in a tile of which a query may see a part: a weight of 0 would not keep them
+  // out of the product.  They are added key by key to the queries that see them; clear_rows() then takes them out.
+  __device__ __forceinline__ void add_rows(const unsigned char* V, int r0, const f32x16& p, uint32_t bad, int key0,
+                                           int gone) {
     const int lane = threadIdx.x & 63, h = lane >> 5;
-#pragma unroll
-    for (int t = 0; t < DT; ++t) {
-      if constexpr (F32) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = value_at(V, r0, t, i);
-          o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(((bad >> key_of(i)) & 1) ? 0.f : v, p[i], o[t], 0, 0, 0);
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          union { uint16_t e[8]; uint4 u; } v;
-          v.u = value_operand(V, r0 + 16 * s, t);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((bad >> key_of(8 * s + j)) & 1) v.e[j] = 0;
-          o[t] = Op<T>::mma(__builtin_bit_cast(typename Op<T>::V, v.u),
-                            __builtin_bit_cast(typename Op<T>::V, weight_operand(p, s)), o[t]);
-        }
-      }
-    }
     for (uint32_t left = bad; left != 0; left &= left - 1) {
       const int k = __ffs(left) - 1, key = key0 + k;
       float w = 0.f;      // its weight, in the lanes of half (k / 4) % 2
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i == (k >> 3) * 4 + (k & 3)) w = F32 ? p[i] : Elem<T>::to_f(Elem<T>::from_f(p[i]));
+        if (i == (k >> 3) * 4 + (k & 3)) w = p[i];
       w = __shfl(w, (lane & 31) + 32 * ((k >> 2) & 1));
       const bool sees = key >= lo && key <= hi && !((gone >> (k >> 4)) & 1);
       const int r = r0 + k;
@@ -371,6 +476,13 @@ struct Wave {
           if (sees) o[t][i] += w * Elem<T>::to_f(v);
         }
       }
+    }
+  }
+  static __device__ __forceinline__ void clear_rows(unsigned char* V, int r0, uint32_t bad) {
+    const int lane = threadIdx.x & 63;
+    for (uint32_t left = bad; left != 0; left &= left - 1) {
+      const int r = r0 + __ffs(left) - 1;
+      for (int x = lane; x < PPR; x += 64) *reinterpret_cast<uint4*>(V + r * RB + x * 16) = make_uint4(0, 0, 0, 0);
     }
   }
 };
@@ -433,7 +545,7 @@ __device__ __forceinline__ void stage_rows(const void* cache, const Pages& pg, i
 template <int ROWS>
 struct Tile {
   int R, row0, room, pmin, pmax, beg, end, b, lens, L;
-  __device__ __forceinline__ Tile(const AttendArgs& a, int G, const Unit& u) {
+  __device__ __forceinline__ Tile(const AttendArgs& a, int G, const Piece& u) {
     R = u.L * G;
     row0 = u.tile * ROWS;
     b = u.b, lens = u.lens, L = u.L;
@@ -464,293 +576,311 @@ __device__ __forceinline__ void store_final(T* dst, float x, float y, float z, f
   else store4<T>(dst, x * f, y * f, z * f, u * f);
 }
 
+// A workgroup's tile, or its share's pieces one after another: body(piece, from, to, whole, slot) for the part
+// [from, to) of a tile's length; pieces that are not whole tiles have a slot of the workspace.  Without shares every
+// workgroup has a tile.
+template <bool FEW, typename B>
+__device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j, B&& body) {
+  Shares sh{0, 0, 0, 1};
+  int64_t pos = 0, end = 0;
+  bool tile = a.shares == 0;
+  if (!tile) {
+    sh = share_out<FEW>(a, G);
+    if (j >= sh.whole + a.shares) return;        // the grid has room for more whole tiles
+    tile = j < sh.whole;
+    if (!tile) {
+      j -= (int)sh.whole;
+      pos = j * sh.share;
+      end = lane_value(min(sh.rest, pos + sh.share), 0);
+    }
+  }
+  Cut cut{0, 0, 0, 0};
+  for (bool first = true; tile || pos < end; first = false) {
+    Piece u;
+    int64_t from = 0, to = 1;
+    if (tile) {
+      if (!(a.shares ? find_piece<FEW, true>(a, G, sh, j, u) : find_tile<FEW>(a, G, j, u))) return;
+    } else {
+      if (!find_piece<FEW, false>(a, G, sh, pos, u)) break;
+      from = pos - u.at, to = min(u.length, end - u.at);
+      if (to <= from) break;
+      if (first && from > 0 && u.at / sh.share == j - 1)
+        cut = Cut{u.b, u.L, u.tile, (int)((u.at + u.length - 1) / sh.share) - j + 2};
+    }
+    body(u, from, to, from == 0 && to == u.length, 2 * j + (from == 0));
+    if (tile) return;
+    pos = lane_value(u.at + to, 0);
+  }
+  if (threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)j * a.c.Hkv + head] = cut;
+}
+
+// The blocks of `n` that the part [from, to) of a tile's length is.
+__device__ __forceinline__ void part_blocks(int n, const Piece& u, int64_t from, int64_t to, int& b, int& e) {
+  b = from == 0 ? 0 : (int)(from * n / u.length);
+  e = to == u.length ? n : (int)(to * n / u.length);
+}
+
 // Many rows: four waves of 32 rows, the same keys.  Tiles of KT keys are double buffered; a tile's loads are issued one
 // tile ahead, and the one barrier a tile also says that nobody reads the other buffer any more.
 template <typename T, int D>
 struct ManyShape {
-  static constexpr int RB = D * (int)sizeof(T);
-  static constexpr int KT = RB >= 1024 ? 32 : 64;
-  static constexpr int NS = KT / 32, BYTES = 4 * KT * RB;
-  static constexpr int WAVES = BYTES <= 81920 ? 2 : 1;   // a SIMD
+  static constexpr int RB = D * (int)sizeof(T), KT = many_keys(RB), NS = KT / 32;
 };
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, (ManyShape<T, D>::WAVES)) void cache_attention_many_kernel(AttendArgs a) {
+__global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_attention_many_kernel(AttendArgs a) {
   using S = ManyShape<T, D>;
   constexpr int KT = S::KT, RB = S::RB, ES = (int)sizeof(T), NR = KT / 4;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), unit = (int)(blockIdx.x / a.c.Hkv);
-  Unit u;
-  if (!find_unit<kManyRows>(a, G, unit, u)) return;
-  const Tile<kManyRows> t(a, G, u);
-  Wave<T, D> w;
-  w.init();
-  const int mine = wave * 32 + (lane & 31);
-  const int64_t out = set_row(a, G, head, t, mine, w);
-  const int key_first = t.beg & ~(KT - 1);
-  const int tiles = t.end > t.beg ? (t.end - key_first + KT - 1) / KT : 0, per = (tiles + u.slices - 1) / u.slices;
-  const int tb = u.slice * per, te = min(tiles, tb + per);
+  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), h = lane >> 5;
   const float c = a.scale_log2, slack = 8.f / c;
-  const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  Pages pg;
-  pg.first = -0x40000000;
-  auto stage = [&](int i, int buf) {
-    const int key = key_first + i * KT;
-    if ((key >> 4) - pg.first >= 64) load_pages(a, table, head, key >> 4, pg);
-    const uint32_t at = lds + (uint32_t)(buf * 2 * KT * RB + wave * NR * RB);
-    stage_rows<ES, D, NR, false>(a.k_cache, pg, key + wave * NR, t.beg, t.end, at);
-    stage_rows<ES, D, NR, true>(a.v_cache, pg, key + wave * NR, t.beg, t.end, at + KT * RB);
-    return (int)((pg.none >> ((key >> 4) - pg.first)) & ((1 << (KT / 16)) - 1));
-  };
-  int gone = 0;
-  if (tb < te) gone = stage(tb, 0);
-  for (int i = tb; i < te; ++i) {
-    const int buf = (i - tb) & 1, key = key_first + i * KT, absent = gone;
-    wait_loads<0>();
-    lds_barrier();
-    if (i + 1 < te) gone = stage(i + 1, buf ^ 1);
-    const unsigned char* K = smem + buf * 2 * KT * RB;
-    const unsigned char* V = K + KT * RB;
-    f32x16 s[S::NS];
+  walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int64_t from, int64_t to, bool whole, int slot) {
+    const Tile<kManyRows> t(a, G, u);
+    Wave<T, D> w;
+    w.init();
+    const int mine = wave * 32 + (lane & 31);
+    const int64_t out = set_row(a, G, head, t, mine, w);
+    const int key_first = t.beg & ~(KT - 1);
+    int tb, te;
+    part_blocks(t.end > t.beg ? (t.end - key_first + KT - 1) / KT : 0, u, from, to, tb, te);
+    const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
+    Pages pg;
+    pg.first = -0x40000000;
+    auto stage = [&](int i, int buf) {
+      const int key = key_first + i * KT;
+      if ((key >> 4) - pg.first >= 64) load_pages(a, table, head, key >> 4, pg);
+      const uint32_t at = lds + (uint32_t)(buf * 2 * KT * RB + wave * NR * RB);
+      stage_rows<ES, D, NR, false>(a.k_cache, pg, key + wave * NR, t.beg, t.end, at);
+      stage_rows<ES, D, NR, true>(a.v_cache, pg, key + wave * NR, t.beg, t.end, at + KT * RB);
+      return (int)((pg.none >> ((key >> 4) - pg.first)) & ((1 << (KT / 16)) - 1));
+    };
+    lds_barrier();                                 // nobody reads the last piece's tiles any more
+    int gone = 0;
+    if (tb < te) gone = stage(tb, 0);
+    for (int i = tb; i < te; ++i) {
+      const int buf = (i - tb) & 1, key = key_first + i * KT, absent = gone;
+      wait_loads<0>();
+      lds_barrier();
+      if (i + 1 < te) gone = stage(i + 1, buf ^ 1);
+      unsigned char* K = smem + buf * 2 * KT * RB;
+      unsigned char* V = K + KT * RB;
+      f32x16 s[S::NS];
 #pragma unroll
-    for (int n = 0; n < S::NS; ++n) s[n] = w.scores(K, 32 * n);
-    const bool part = key + KT - 1 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
-    if (part) {
+      for (int n = 0; n < S::NS; ++n) s[n] = w.scores(K, 32 * n);
+      const bool part = key + KT - 1 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
+      if (part) {
 #pragma unroll
-      for (int n = 0; n < S::NS; ++n) w.mask(s[n], key + 32 * n, absent >> (2 * n));
+        for (int n = 0; n < S::NS; ++n) w.mask(s[n], key + 32 * n, absent >> (2 * n));
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < S::NS; ++n)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, s[n][j]);
+      w.raise(top, c, slack);
+#pragma unroll
+      for (int n = 0; n < S::NS; ++n) w.weigh(s[n], c);
+      if (part) {
+#pragma unroll
+        for (int n = 0; n < S::NS; ++n) {
+          const uint32_t bad = w.not_finite(V, 32 * n);          // the same for all four waves
+          if (__builtin_expect(bad != 0, 0)) {
+            w.add_rows(V, 32 * n, s[n], bad, key + 32 * n, absent >> (2 * n));
+            lds_barrier();
+            w.clear_rows(V, 32 * n, bad);                        // all waves write the same zeros
+            lds_barrier();
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < S::NS; ++n) w.add_values(V, 32 * n, s[n]);
     }
-    float top = -INFINITY;
+    const float l = other_half_sum(w.l);
+    if (t.row0 + mine >= t.R) return;
+    if (whole) {
+      T* o = static_cast<T*>(a.o) + out;
 #pragma unroll
-    for (int n = 0; n < S::NS; ++n)
+      for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[n][j]);
-    w.raise(top, c, slack);
+        for (int j = 0; j < 4; ++j)
+          store_final(o + 32 * k + 8 * j + 4 * h, w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3], l);
+    } else {
+      const int64_t at = ((int64_t)slot * a.c.Hkv + head) * kManyRows + mine;
+      float* o = a.part_o + at * D;
 #pragma unroll
-    for (int n = 0; n < S::NS; ++n) w.weigh(s[n], c);
+      for (int k = 0; k < D / 32; ++k)
 #pragma unroll
-    for (int n = 0; n < S::NS; ++n) {
-      const uint32_t bad = part ? w.not_finite(V, 32 * n) : 0;
-      if (__builtin_expect(bad != 0, 0)) w.add_values_apart(V, 32 * n, s[n], bad, key + 32 * n, absent >> (2 * n));
-      else w.add_values(V, 32 * n, s[n]);
+        for (int j = 0; j < 4; ++j)
+          store4<float>(o + 32 * k + 8 * j + 4 * h, w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3]);
+      if (h == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(w.m, l);
     }
-  }
-  const float l = other_half_sum(w.l);
-  if (t.row0 + mine >= t.R) return;
-  const int h = lane >> 5;
-  if (u.slices == 1) {
-    T* o = static_cast<T*>(a.o) + out;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        store_final(o + 32 * k + 8 * j + 4 * h, w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3], l);
-  } else {
-    const int64_t slot = ((int64_t)unit * a.c.Hkv + head) * kManyRows + mine;
-    float* o = a.part_o + slot * D;
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        store4<float>(o + 32 * k + 8 * j + 4 * h, w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3]);
-    if (h == 0) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(w.m, l);
-  }
+  });
 }
 
 // Few rows: one tile of 32 rows, each wave on its own 32 keys at a time with its own piece of LDS and no barrier: once
 // a tile's keys have been read the next ones are on their way, once its values have been read the next values.
 template <typename T, int D>
-struct FewShape {
-  static constexpr int RB = D * (int)sizeof(T), NW = RB >= 1024 ? 2 : 4;
-  static constexpr int BYTES = NW * 64 * RB, WAVES = BYTES <= 81920 ? 2 : 1;
-};
-
-template <typename T, int D>
-__global__ __launch_bounds__((64 * FewShape<T, D>::NW), (FewShape<T, D>::WAVES))
+__global__ __launch_bounds__((64 * few_group(D * (int)sizeof(T))), (few_waves(D * (int)sizeof(T))))
 void cache_attention_few_kernel(AttendArgs a) {
-  using S = FewShape<T, D>;
-  constexpr int RB = S::RB, ES = (int)sizeof(T), NW = S::NW, NI = 32 * RB / 1024;
+  constexpr int RB = D * (int)sizeof(T), ES = (int)sizeof(T), NW = few_group(RB), NI = 32 * RB / 1024;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float2 ml[NW][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), unit = (int)(blockIdx.x / a.c.Hkv);
-  Unit u;
-  if (!find_unit<kFewRows>(a, G, unit, u)) return;
-  const Tile<kFewRows> t(a, G, u);
-  Wave<T, D> w;
-  w.init();
-  set_row(a, G, head, t, lane & 31, w);
-  const int key_first = t.beg & ~31;
-  const int tiles = t.end > t.beg ? (t.end - key_first + 31) / 32 : 0, per = (tiles + u.slices - 1) / u.slices;
-  const int tb = u.slice * per, te = min(tiles, tb + per);
+  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
   const float c = a.scale_log2, slack = 8.f / c;
-  const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
-  const unsigned char* K = smem + wave * 64 * RB;
-  const unsigned char* V = K + 32 * RB;
+  unsigned char* K = smem + wave * 64 * RB;
+  unsigned char* V = K + 32 * RB;
   const uint32_t ldsK = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * 64 * RB;
-  Pages pg;
-  pg.first = -0x40000000;
-  auto pages_for = [&](int i) {
-    const int g = (key_first >> 4) + 2 * i;
-    if (g - pg.first >= 64) load_pages(a, table, head, g, pg);
-    return (int)((pg.none >> (g - pg.first)) & 3);
-  };
-  int i = tb + wave, gone = 0;
-  if (i < te) {
-    gone = pages_for(i);
-    stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK);
-    stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK + 32 * RB);
-  }
-  for (; i < te; i += NW) {
-    const int key = key_first + 32 * i, absent = gone, next = i + NW;
-    wait_loads<NI>();                              // the keys: the values were issued after them
-    f32x16 s = w.scores(K, 0);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (next < te) {
-      gone = pages_for(next);
-      stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK);
+  walk<true>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int64_t from, int64_t to, bool whole, int slot) {
+    const Tile<kFewRows> t(a, G, u);
+    Wave<T, D> w;
+    w.init();
+    const int key_first = t.beg & ~31;
+    int tb, te;
+    part_blocks(t.end > t.beg ? (t.end - key_first + 31) / 32 : 0, u, from, to, tb, te);
+    const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
+    Pages pg;
+    pg.first = -0x40000000;
+    auto pages_for = [&](int i) {
+      const int g = (key_first >> 4) + 2 * i;
+      if (g - pg.first >= 64) load_pages(a, table, head, g, pg);
+      return (int)((pg.none >> (g - pg.first)) & 3);
+    };
+    int i = tb + wave, gone = 0;
+    if (i < te) {
+      gone = pages_for(i);
+      stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK);
+      stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK + 32 * RB);
     }
-    const bool part = key + 31 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
-    if (part) w.mask(s, key, absent);
-    float top = -INFINITY;
+    set_row(a, G, head, t, lane & 31, w);
+    for (; i < te; i += NW) {
+      const int key = key_first + 32 * i, absent = gone, next = i + NW;
+      wait_loads<NI>();                              // the keys: the values were issued after them
+      f32x16 s = w.scores(K, 0);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (next < te) {
+        gone = pages_for(next);
+        stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK);
+      }
+      const bool part = key + 31 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
+      if (part) w.mask(s, key, absent);
+      float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
-    w.raise(top, c, slack);
-    w.weigh(s, c);
-    if (next < te) wait_loads<NI>();               // the values: the next keys were issued after them
-    else wait_loads<0>();
-    const uint32_t bad = part ? w.not_finite(V, 0) : 0;
-    if (__builtin_expect(bad != 0, 0)) w.add_values_apart(V, 0, s, bad, key, absent);
-    else w.add_values(V, 0, s);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (next < te) stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK + 32 * RB);
-  }
-  // join the waves: everyone's accumulators in LDS (pieces of 16 bytes at piece ^ row % 8)
-  const float l = other_half_sum(w.l);
-  const int h = lane >> 5, row = lane & 31;
-  if (h == 0) ml[wave][row] = make_float2(w.m, l);
-  __syncthreads();                                 // and nobody reads keys or values any more
-  float4* O = reinterpret_cast<float4*>(smem);
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      O[(wave * 32 + row) * (D / 4) + ((8 * k + 2 * j + h) ^ (row & 7))] =
-          make_float4(w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3]);
-  __syncthreads();
-  const int rows = min(kFewRows, t.R - t.row0);
-  const int64_t slot = ((int64_t)unit * a.c.Hkv + head) * kFewRows;
-  for (int k = threadIdx.x; k < rows * (D / 4); k += 64 * NW) {
-    const int r = k / (D / 4), piece = k % (D / 4);
-    float m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) m = fmaxf(m, ml[v][r].x);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float tot = 0.f;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) {
-      const float2 x = ml[v][r];
-      const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * c);
-      const float4 p = O[(v * 32 + r) * (D / 4) + (piece ^ (r & 7))];
-      sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
-      tot += f * x.y;
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
+      w.raise(top, c, slack);
+      w.weigh(s, c);
+      if (next < te) wait_loads<NI>();               // the values: the next keys were issued after them
+      else wait_loads<0>();
+      if (part) {
+        const uint32_t bad = w.not_finite(V, 0);
+        if (__builtin_expect(bad != 0, 0)) {
+          w.add_rows(V, 0, s, bad, key, absent);
+          w.clear_rows(V, 0, bad);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+      }
+      w.add_values(V, 0, s);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (next < te) stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK + 32 * RB);
     }
-    if (u.slices == 1) {
-      const int token = (t.row0 + r) / G, g = t.row0 + r - token * G;
-      T* o = static_cast<T*>(a.o) + ((int64_t)(t.b + token) * a.c.Hq + head * G + g) * D + 4 * piece;
-      store_final(o, sum.x, sum.y, sum.z, sum.w, tot);
-    } else {
-      *reinterpret_cast<float4*>(a.part_o + (slot + r) * D + 4 * piece) = sum;
-      if (piece == 0) *reinterpret_cast<float2*>(a.part_ml + (slot + r) * 2) = make_float2(m, tot);
+    // join the waves: everyone's accumulators in LDS (pieces of 16 bytes at piece ^ row % 8)
+    const float l = other_half_sum(w.l);
+    const int h = lane >> 5, row = lane & 31;
+    if (h == 0) ml[wave][row] = make_float2(w.m, l);
+    __syncthreads();                                 // and nobody reads keys or values any more
+    float4* O = reinterpret_cast<float4*>(smem);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        O[(wave * 32 + row) * (D / 4) + ((8 * k + 2 * j + h) ^ (row & 7))] =
+            make_float4(w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3]);
+    __syncthreads();
+    const int rows = min(kFewRows, t.R - t.row0);
+    const int64_t at = ((int64_t)slot * a.c.Hkv + head) * kFewRows;
+    for (int k = threadIdx.x; k < rows * (D / 4); k += 64 * NW) {
+      const int r = k / (D / 4), piece = k % (D / 4);
+      float m = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < NW; ++v) m = fmaxf(m, ml[v][r].x);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float tot = 0.f;
+#pragma unroll
+      for (int v = 0; v < NW; ++v) {
+        const float2 x = ml[v][r];
+        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * c);
+        const float4 p = O[(v * 32 + r) * (D / 4) + (piece ^ (r & 7))];
+        sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
+        tot += f * x.y;
+      }
+      if (whole) {
+        const int token = (t.row0 + r) / G, g = t.row0 + r - token * G;
+        T* o = static_cast<T*>(a.o) + ((int64_t)(t.b + token) * a.c.Hq + head * G + g) * D + 4 * piece;
+        store_final(o, sum.x, sum.y, sum.z, sum.w, tot);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (at + r) * D + 4 * piece) = sum;
+        if (piece == 0) *reinterpret_cast<float2*>(a.part_ml + (at + r) * 2) = make_float2(m, tot);
+      }
     }
-  }
+    __syncthreads();                                 // the next piece may overwrite all of it
+  });
 }
 
-// Joins the slices of a row: a workgroup a row, groups of D / 4 threads on every few slices.
+// Joins the pieces of tiles that lie in several shares, in their order.  A wave takes 64 columns (or D = 32) of a row,
+// its groups of lanes every few pieces.
 template <typename T, int D, int ROWS>
-__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttendArgs a, int64_t row0) {
-  constexpr int PIECES = D / 4, GROUPS = 256 / PIECES;
-  __shared__ float weight[kMostSlices];
-  __shared__ float4 sums[GROUPS][PIECES];
-  __shared__ float red[8];
-  const int lane = threadIdx.x & 63, G = a.c.Hq / a.c.Hkv;
-  const int64_t at = row0 + blockIdx.x;             // (tile, head, row of the tile)
-  const int n = (int)(at % ROWS), head = (int)(at / ROWS % a.c.Hkv), want = (int)(at / ROWS / a.c.Hkv);
-  // the want-th tile, and how many (tile, slice) pairs come before it
-  const int keys = slice_keys<ROWS>(a, G);
-  int before = 0, units = 0, slices = 0, first = 0, tile = 0, b = 0, L = 0;
-  bool found = false;
-  for (int s0 = 0; s0 < a.c.N && !found; s0 += 64) {
-    int bb, LL, lens, tiles, span;
-    sequence_size<ROWS>(a, G, s0 + lane, bb, LL, lens, tiles, span);
-    const int sl = span > keys ? (span + keys - 1) / keys : 1;
-    int upto = tiles, upto_units = tiles * sl;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int o = __shfl_up(upto, m), o2 = __shfl_up(upto_units, m);
-      if (lane >= m) upto += o, upto_units += o2;
+__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttendArgs a) {
+  constexpr int COLS = D < 64 ? D : 64, LANES = COLS / 4, GROUPS = 64 / LANES, PARTS = D / COLS;
+  __shared__ float weights[4][kMostShares];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
+  if (cut.pieces < 2 || cut.pieces > a.shares) return;
+  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), j = (int)(blockIdx.x / a.c.Hkv);
+  const int row0 = cut.tile * ROWS, items = min(ROWS, cut.L * G - row0) * PARTS;
+  float* weight = weights[wave];
+  for (int i = (int)blockIdx.y * 4 + wave; i < items; i += 4 * (int)gridDim.y) {
+    const int n = i / PARTS, col = i % PARTS * COLS + lane % LANES * 4, group = lane / LANES;
+    // piece k: the end of share j - 1, then the beginnings of the next ones
+    auto at = [&](int k) {
+      return ((int64_t)(k == 0 ? 2 * (j - 1) + 1 : 2 * (j - 1 + k)) * a.c.Hkv + head) * ROWS + n;
+    };
+    float m = -INFINITY;
+    for (int k = lane; k < cut.pieces; k += 64) {
+      const float x = a.part_ml[at(k) * 2];
+      weight[k] = x;
+      m = fmaxf(m, x);
     }
-    const int total = __builtin_amdgcn_readlane(upto, 63);
-    if (want < before + total) {
-      const int j = __ffsll((unsigned long long)__ballot(want < before + upto)) - 1;
-      const int tl = __builtin_amdgcn_readlane(tiles, j);
-      slices = __builtin_amdgcn_readlane(sl, j);
-      const int rest = want - before - (__builtin_amdgcn_readlane(upto, j) - tl);
-      first = units + __builtin_amdgcn_readlane(upto_units, j) - tl * slices + rest * slices;
-      tile = tl - 1 - rest;
-      b = __builtin_amdgcn_readlane(bb, j);
-      L = __builtin_amdgcn_readlane(LL, j);
-      found = true;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+    float l = 0.f;
+    for (int k = lane; k < cut.pieces; k += 64) {
+      const float x = weight[k], f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x - m) * a.scale_log2);
+      weight[k] = f;
+      l += f * a.part_ml[at(k) * 2 + 1];
     }
-    before += total;
-    units += __builtin_amdgcn_readlane(upto_units, 63);
-  }
-  const int r = tile * ROWS + n;
-  // (malformed offsets may count more pairs than there is room for)
-  if (!found || slices < 2 || r >= L * G || first + slices > a.units) return;
-  auto slot = [&](int s) { return ((int64_t)(first + s) * a.c.Hkv + head) * ROWS + n; };
-  float m = -INFINITY;
-  for (int s = threadIdx.x; s < slices; s += 256) {
-    const float x = a.part_ml[slot(s) * 2];
-    weight[s] = x;
-    m = fmaxf(m, x);
-  }
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
-  if (lane == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float l = 0.f;
-  for (int s = threadIdx.x; s < slices; s += 256) {
-    const float x = weight[s], f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x - m) * a.scale_log2);
-    weight[s] = f;
-    l += f * a.part_ml[slot(s) * 2 + 1];
-  }
+    for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the weights, which only this wave reads
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = group; k < cut.pieces; k += GROUPS) {
+      const float4 p = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col);
+      const float f = weight[k];
+      sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
+    }
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
-  if (lane == 0) red[4 + (threadIdx.x >> 6)] = l;
-  __syncthreads();
-  l = (red[4] + red[5]) + (red[6] + red[7]);
-  const int piece = threadIdx.x % PIECES, group = threadIdx.x / PIECES;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = group; s < slices; s += GROUPS) {
-    const float4 p = *reinterpret_cast<const float4*>(a.part_o + slot(s) * D + 4 * piece);
-    const float f = weight[s];
-    sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
+    for (int k = LANES; k < 64; k <<= 1) {
+      sum.x += __shfl_xor(sum.x, k), sum.y += __shfl_xor(sum.y, k);
+      sum.z += __shfl_xor(sum.z, k), sum.w += __shfl_xor(sum.w, k);
+    }
+    if (group == 0) {
+      const int token = (row0 + n) / G, g = row0 + n - token * G;
+      store_final(static_cast<T*>(a.o) + ((int64_t)(cut.b + token) * a.c.Hq + head * G + g) * D + col, sum.x, sum.y,
+                  sum.z, sum.w, l);
+    }
   }
-  sums[group][piece] = sum;
-  __syncthreads();
-  if (group != 0) return;
-#pragma unroll
-  for (int k = 1; k < GROUPS; ++k) {
-    const float4 p = sums[k][piece];
-    sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
-  }
-  const int token = r / G, g = r - token * G;
-  store_final(static_cast<T*>(a.o) + ((int64_t)(b + token) * a.c.Hq + head * G + g) * D + 4 * piece, sum.x, sum.y,
-              sum.z, sum.w, l);
 }
 
 template <typename K>
@@ -761,42 +891,38 @@ static hipError_t allow_lds(K kernel, int bytes) {
 }
 
 template <typename T, int D>
-static hipError_t launch_attend_d(const AttendArgs& a, int64_t tiles, hipStream_t s) {
-  const unsigned wgs = (unsigned)((int64_t)a.units * a.c.Hkv);
+static hipError_t launch_attend_d(const AttendArgs& a, hipStream_t s) {
+  constexpr int RB = D * (int)sizeof(T);
+  // few rows: shares alone; many rows: some tiles are taken whole before them
+  const unsigned shares = (unsigned)((int64_t)a.shares * a.c.Hkv), tiles = (unsigned)((int64_t)a.tiles * a.c.Hkv);
+  const unsigned wgs = a.shares && a.few ? shares : tiles + shares;
   prof_begin(K_ATTEND, s);
   hipError_t e;
   if (a.few) {
-    using S = FewShape<T, D>;
-    e = allow_lds(cache_attention_few_kernel<T, D>, S::BYTES);
+    e = allow_lds(cache_attention_few_kernel<T, D>, few_lds(RB));
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((cache_attention_few_kernel<T, D>), dim3(wgs), dim3(64 * S::NW), S::BYTES, s, a);
+    hipLaunchKernelGGL((cache_attention_few_kernel<T, D>), dim3(wgs), dim3(64 * few_group(RB)), few_lds(RB), s, a);
   } else {
-    using S = ManyShape<T, D>;
-    e = allow_lds(cache_attention_many_kernel<T, D>, S::BYTES);
+    e = allow_lds(cache_attention_many_kernel<T, D>, many_lds(RB));
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((cache_attention_many_kernel<T, D>), dim3(wgs), dim3(256), S::BYTES, s, a);
+    hipLaunchKernelGGL((cache_attention_many_kernel<T, D>), dim3(wgs), dim3(256), many_lds(RB), s, a);
   }
   prof_end(K_ATTEND, s);
-  if ((e = hipGetLastError()) != hipSuccess || a.slices == 0) return e;
+  if ((e = hipGetLastError()) != hipSuccess || a.shares < 2) return e;
   prof_begin(K_ATTEND_JOIN, s);
-  const int64_t rows = tiles * a.c.Hkv * (a.few ? kFewRows : kManyRows), most = kLaunchThreads / 256;
-  for (int64_t r = 0; r < rows; r += most) {
-    const dim3 grid((unsigned)std::min(most, rows - r));
-    if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), grid, dim3(256), 0, s, a, r);
-    else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), grid, dim3(256), 0, s, a, r);
-  }
+  if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), dim3(shares, 16), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), dim3(shares, 32), dim3(256), 0, s, a);
   prof_end(K_ATTEND_JOIN, s);
   return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t launch_attend_t(const AttendArgs& a, hipStream_t s) {
-  const int64_t tiles = a.units - a.slices;
   switch (a.c.d) {
-    case 32: return launch_attend_d<T, 32>(a, tiles, s);
-    case 64: return launch_attend_d<T, 64>(a, tiles, s);
-    case 128: return launch_attend_d<T, 128>(a, tiles, s);
-    case 256: return launch_attend_d<T, 256>(a, tiles, s);
+    case 32: return launch_attend_d<T, 32>(a, s);
+    case 64: return launch_attend_d<T, 64>(a, s);
+    case 128: return launch_attend_d<T, 128>(a, s);
+    case 256: return launch_attend_d<T, 256>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -42,10 +42,11 @@ struct AttendArgs {
   int32_t granules;      // 16-row granules of a page
   uint64_t granule_magic;   // ceil(2^32 / granules)
   int32_t few;           // one 32-row tile a workgroup, its waves on different keys
-  int32_t slices;        // key slices a head to aim at, 0: tiles are not split
-  int32_t units;         // upper bound on (tile, slice) pairs of a head
-  float* part_o;         // [units, Hkv, rows of a tile, d]
-  float* part_ml;        // [units, Hkv, rows of a tile, 2]
+  int32_t shares;        // even shares of a head's work, 0: a tile for each workgroup
+  int32_t tiles;         // upper bound on a head's tiles
+  float* part_o;         // [2 shares, Hkv, rows of a tile, d]
+  float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
+  void* cuts;            // [shares, Hkv] of 16 bytes
 };
 
 struct SelectArgs {
@@ -75,9 +76,17 @@ struct ReorderArgs {
   const int32_t* dst_index;   // may be null
 };
 
-// Rows of a tile and the smallest slice of keys: shared by the host's sizes and the kernels.
+// Sizes that the host's plan and the attention's kernels share: rows of a tile, the fewest keys of a share of few and of
+// many rows, and by the
+// bytes of one key (rb) the keys of a tile, waves of a workgroup, LDS and waves a SIMD (one workgroup each).
 constexpr int32_t kFewRows = 32, kManyRows = 128;
-constexpr int32_t kSliceKeys = 256, kMostSlices = 1024;
+constexpr int32_t kFewKeys = 256, kManyKeys = 256, kMostShares = 1024;
+constexpr int many_keys(int rb) { return rb >= 1024 ? 32 : 64; }
+constexpr int many_lds(int rb) { return 4 * many_keys(rb) * rb; }
+constexpr int many_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : rb >= 128 ? 3 : 4; }
+constexpr int few_group(int rb) { return rb >= 1024 ? 2 : 4; }
+constexpr int few_lds(int rb) { return few_group(rb) * 64 * rb; }
+constexpr int few_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : rb >= 128 ? 3 : 4; }
 
 hipError_t launch_append(DType dt, const AppendArgs& a, hipStream_t s);
 hipError_t launch_attend_f32(const AttendArgs& a, hipStream_t s);
