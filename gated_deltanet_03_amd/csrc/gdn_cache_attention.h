@@ -23,6 +23,7 @@
 
 #include "gdn_cache_device.h"
 #include "gdn_rows.h"
+#include "gdn_scan.h"
 
 namespace gdn {
 namespace attend {
@@ -78,10 +79,11 @@ __device__ __forceinline__ int value_swizzle(int r) {
   else return ((r >> 1) & 1) << 1;
 }
 
-__device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)((uint64_t)x >> 32), lane);
-  return (int64_t)((uint64_t)hi << 32 | lo);
+__device__ __forceinline__ double lane_value(double x, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // How the work of one head is laid out.
@@ -97,184 +99,154 @@ __device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
 // 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole rounds of `shares` tiles stay whole, the last ones
 // of a sequence, which see the most keys, first; with three rounds or more nothing is cut.  Tiles longer than 5/4 of an even
 // share are always cut, so that one long sequence does not outlast all others.
+//
+// Lengths are doubles, whole numbers below 2^53 for anything that runs in a day; beyond, they are rounded the same in
+// every workgroup, so that pieces still meet.
 struct Piece {
   int s, b, L, lens, tile;
-  int64_t at, length;      // the tile's start and length on the line
+  double at, length;       // the tile's start and length on the line
+};
+
+// What all workgroups of a call agree on.
+struct Shares {
+  double longest;          // of the tiles that may stay whole
+  double whole;            // tiles that stay whole
+  double rest, share;      // length of the line that is left, and of a share of it
+};
+
+// What the work is laid out from.
+struct Work {
+  const int32_t* cu;
+  const int32_t* lens;
+  int N, T, total, G, room, window, tiles, shares;
 };
 
 template <bool FEW>
 struct Line {
   static constexpr int ROWS = FEW ? kFewRows : kManyRows;
-  const AttendArgs& a;
-  int G;
-  // the 64 sequences from s0 on, one a lane
+  const Work& a;
+  int base;                // sequences base .. base + 63 are loaded, one a lane
   int b, L, lens, tiles;
-  int64_t first, step;
+  double first, step;
 
   // i tiles of a sequence.
-  static __device__ __forceinline__ int64_t tiles_length(int64_t first, int64_t step, int64_t i) {
-    return first * i + step * (i * (i - 1) / 2);
+  static __device__ __forceinline__ double tiles_length(double first, double step, double i) {
+    return first * i + step * (i * (i - 1.0) * 0.5);
   }
 
-  __device__ __forceinline__ Line(const AttendArgs& args, int G_) : a(args), G(G_) {}
+  __device__ __forceinline__ explicit Line(const Work& work) : a(work), base(-1) {}
 
-  __device__ __forceinline__ void load(int s) {
+  __device__ __forceinline__ void load(int s0) {
+    if (s0 == base) return;
+    base = s0;
+    const int s = s0 + (int)(threadIdx.x & 63);
     b = L = lens = tiles = 0;
-    first = step = 0;
-    if (s < a.c.N) {
+    first = step = 0.0;
+    if (s < a.N) {
       int e;
-      seq_range(a.c.cu, a.c.T, a.c.total, s, b, e);
+      seq_range(a.cu, a.T, a.total, s, b, e);
       L = e - b;
-      lens = min(max(a.c.lens[s], -(1 << 30)), 1 << 30);
-      tiles = (int)(((int64_t)L * G + ROWS - 1) / ROWS);
-      const int room = a.c.max_pages * a.c.page_size, old = min(max(lens - L, 0), room);
-      first = (int64_t)G * (old + 64) + ROWS;
-      step = ROWS;
-      if (a.window > 0 && a.window < old) first = (int64_t)G * (a.window + 64) + ROWS, step = 0;
+      lens = min(max(a.lens[s], -(1 << 30)), 1 << 30);
+      tiles = (int)(((int64_t)L * a.G + ROWS - 1) / ROWS);
+      const int old = min(max(lens - L, 0), a.room);
+      const bool inside = a.window > 0 && a.window < old;
+      first = (double)a.G * (double)((inside ? a.window : old) + 64) + ROWS;
+      step = inside ? 0.0 : ROWS;
     }
   }
 
-  // Whether the loaded sequence's tiles may stay whole.
-  __device__ __forceinline__ bool may_be_whole(int64_t longest) const {
-    return !FEW && first + step * (tiles - 1) <= longest;
+  // How many of the lane's tiles may stay whole, however many others do.
+  __device__ __forceinline__ double may_be_whole(double longest) const {
+    return !FEW && first + step * (double)(tiles - 1) <= longest ? (double)tiles : 0.0;
   }
 
-  static __device__ __forceinline__ int64_t sum(int64_t x) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
-    return lane_value(x, 0);
-  }
-  static __device__ __forceinline__ int64_t scan(int64_t x) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int64_t o = __shfl_up(x, m);
-      if ((int)(threadIdx.x & 63) >= m) x += o;
+  static __device__ __forceinline__ double sum(double x) { return lane_value(wave_scan64(x), 63); }
+
+  __device__ __forceinline__ Shares share_out() {
+    Shares r{0.0, 0.0, 0.0, 0.0};
+    double all = 0.0;
+    for (int s = 0; s < a.N; s += 64) {
+      load(s);
+      all += sum(tiles_length(first, step, tiles));
     }
-    return x;
-  }
-};
-
-// What all workgroups of a call agree on.
-struct Shares {
-  int64_t longest;         // of the tiles that may stay whole
-  int64_t whole;           // tiles that stay whole
-  int64_t rest, share;     // length of the line that is left, and of a share of it
-};
-
-template <bool FEW>
-__device__ __forceinline__ Shares share_out(const AttendArgs& a, int G) {
-  Line<FEW> line(a, G);
-  const int lane = threadIdx.x & 63;
-  Shares r{0, 0, 0, 1};
-  int64_t all = 0;
-  for (int s = 0; s < a.c.N; s += 64) {
-    line.load(s + lane);
-    all += Line<FEW>::sum(line.tiles_length(line.first, line.step, line.tiles));
-  }
-  const int64_t even = (all + a.shares - 1) / a.shares, least = (int64_t)G * (FEW ? kFewKeys : kManyKeys);
-  r.rest = all;
-  if constexpr (!FEW) {
-    r.longest = even + even / 4 > 2 * least ? even + even / 4 : 2 * least;
-    int64_t may = 0, sure = 0;
-    for (int s = 0; s < a.c.N; s += 64) {
-      if (a.c.N > 64) line.load(s + lane);
-      const bool w = line.tiles > 0 && line.may_be_whole(r.longest);
-      may += Line<FEW>::sum(w ? line.tiles : 0);
-      sure += Line<FEW>::sum(w ? 0 : line.tiles);
-    }
-    const int64_t rounds = may / a.shares;
-    r.whole = sure == 0 && (rounds >= 3 || r.longest == 2 * least) ? may : rounds * a.shares;
-    r.whole = min(r.whole, (int64_t)a.tiles);    // (malformed offsets may count more tiles than there is room for)
-    // what is left after them
-    int64_t before = 0;
-    r.rest = 0;
-    for (int s = 0; s < a.c.N; s += 64) {
-      if (a.c.N > 64) line.load(s + lane);
-      const int mine = line.tiles > 0 && line.may_be_whole(r.longest) ? line.tiles : 0;
-      const int64_t upto = before + Line<FEW>::scan(mine);
-      const int64_t kept = min(max(r.whole - (upto - mine), (int64_t)0), (int64_t)mine);
-      r.rest += Line<FEW>::sum(line.tiles_length(line.first, line.step, line.tiles - kept));
-      before = lane_value(upto, 63);
-    }
-  }
-  const int64_t s = (r.rest + a.shares - 1) / a.shares;
-  r.share = s < least ? least : s;
-  return r;
-}
-
-// The whole tile number `pos` (WHOLE), or the sequence and tile at `pos` of what is left.
-template <bool FEW, bool WHOLE>
-__device__ __forceinline__ bool find_piece(const AttendArgs& a, int G, const Shares& sh, int64_t pos, Piece& p) {
-  Line<FEW> line(a, G);
-  int64_t tiles_before = 0, before = 0;
-  for (int s0 = 0; s0 < a.c.N; s0 += 64) {
-    line.load(s0 + (int)(threadIdx.x & 63));
-    int64_t kept = 0;
+    const double even = ceil(all / a.shares), least = (double)a.G * (FEW ? kFewKeys : kManyKeys);
+    r.rest = all;
     if constexpr (!FEW) {
-      const int mine = line.tiles > 0 && line.may_be_whole(sh.longest) ? line.tiles : 0;
-      const int64_t upto = tiles_before + Line<FEW>::scan(mine);
-      kept = min(max(sh.whole - (upto - mine), (int64_t)0), (int64_t)mine);
-      tiles_before = lane_value(upto, 63);
-    }
-    const int64_t mine = WHOLE ? kept : line.tiles_length(line.first, line.step, line.tiles - kept);
-    const int64_t upto = before + Line<FEW>::scan(mine), total = lane_value(upto, 63);
-    if (pos < total) {
-      const int j = __ffsll((unsigned long long)__ballot(pos < upto)) - 1;
-      const int64_t f = lane_value(line.first, j), st = lane_value(line.step, j);
-      const int64_t start = lane_value(upto - mine, j), rest = pos - start;
-      const int n = __builtin_amdgcn_readlane(line.tiles, j) - (int)lane_value(kept, j);
-      int64_t i;
-      if constexpr (WHOLE) {
-        i = n + lane_value(kept, j) - 1 - rest;
-      } else {
-        if (st == 0) {
-          i = rest / f;
-        } else {        // f i + st i (i - 1) / 2 <= rest, by the quadratic's root
-          const double u = (double)f / (double)st - 0.5;
-          i = (int64_t)(sqrt(u * u + 2.0 * (double)rest / (double)st) - u);
-          i = min(max(i, (int64_t)0), (int64_t)n - 1);
-          while (i > 0 && line.tiles_length(f, st, i) > rest) --i;
-          while (i + 1 < n && line.tiles_length(f, st, i + 1) <= rest) ++i;
-        }
-        i = min(i, (int64_t)n - 1);
+      r.longest = fmax(even * 1.25, 2.0 * least);
+      double may = 0.0, sure = 0.0;
+      for (int s = 0; s < a.N; s += 64) {
+        load(s);
+        const double w = may_be_whole(r.longest);
+        may += sum(w);
+        sure += sum((double)tiles - w);
       }
-      p.s = s0 + j;
-      p.b = __builtin_amdgcn_readlane(line.b, j);
-      p.L = __builtin_amdgcn_readlane(line.L, j);
-      p.lens = __builtin_amdgcn_readlane(line.lens, j);
-      p.tile = __builtin_amdgcn_readfirstlane((int)i);
-      p.at = WHOLE ? pos : lane_value(start + line.tiles_length(f, st, i), 0);
-      p.length = WHOLE ? 1 : lane_value(f + st * i, 0);
-      return true;
+      const double rounds = floor(may / a.shares);
+      r.whole = sure == 0.0 && (rounds >= 3.0 || r.longest == 2.0 * least) ? may : rounds * a.shares;
+      r.whole = fmin(r.whole, (double)a.tiles);  // (malformed offsets may count more tiles than there is room for)
+      // what is left after them
+      double before = 0.0;
+      r.rest = 0.0;
+      for (int s = 0; s < a.N; s += 64) {
+        load(s);
+        const double mine = may_be_whole(r.longest), upto = before + wave_scan64(mine);
+        const double kept = fmin(fmax(r.whole - (upto - mine), 0.0), mine);
+        r.rest += sum(tiles_length(first, step, (double)tiles - kept));
+        before = lane_value(upto, 63);
+      }
     }
-    before = total;
+    r.share = fmax(ceil(r.rest / a.shares), least);
+    return r;
   }
-  return false;
-}
 
-// The j-th tile, where nothing is cut.
-template <bool FEW>
-__device__ __forceinline__ bool find_tile(const AttendArgs& a, int G, int64_t j, Piece& p) {
-  Line<FEW> line(a, G);
-  int64_t before = 0;
-  for (int s0 = 0; s0 < a.c.N; s0 += 64) {
-    line.load(s0 + (int)(threadIdx.x & 63));
-    const int64_t upto = before + Line<FEW>::scan(line.tiles), total = lane_value(upto, 63);
-    if (j < total) {
-      const int k = __ffsll((unsigned long long)__ballot(j < upto)) - 1;
-      p.s = s0 + k;
-      p.b = __builtin_amdgcn_readlane(line.b, k);
-      p.L = __builtin_amdgcn_readlane(line.L, k);
-      p.lens = __builtin_amdgcn_readlane(line.lens, k);
-      p.tile = (int)(lane_value(upto, k) - 1 - j);      // a sequence's last tiles see the most keys: first
-      p.at = j;
-      p.length = 1;
-      return true;
+  // The tile number `pos` of those that are whole (WHOLE; of all tiles if nothing is shared), or the sequence and tile
+  // at `pos` of what is left.
+  template <bool WHOLE>
+  __device__ __forceinline__ bool find(const Shares& sh, double pos, Piece& p) {
+    double tiles_before = 0.0, before = 0.0;
+    for (int s0 = 0; s0 < a.N; s0 += 64) {
+      load(s0);
+      double kept = 0.0;
+      if (a.shares == 0) {
+        kept = tiles;
+      } else if constexpr (!FEW) {
+        const double may = may_be_whole(sh.longest), upto = tiles_before + wave_scan64(may);
+        kept = fmin(fmax(sh.whole - (upto - may), 0.0), may);
+        tiles_before = lane_value(upto, 63);
+      }
+      const double mine = WHOLE ? kept : tiles_length(first, step, (double)tiles - kept);
+      const double upto = before + wave_scan64(mine), total = lane_value(upto, 63);
+      if (pos < total) {
+        const int j = __ffsll((unsigned long long)__ballot(pos < upto)) - 1;
+        const double f = lane_value(first, j), st = lane_value(step, j), start = lane_value(upto - mine, j);
+        const double rest = pos - start;
+        const int cut = __builtin_amdgcn_readlane(tiles, j) - (int)lane_value(kept, j);   // tiles that are not whole
+        int i;
+        if constexpr (WHOLE) {
+          i = cut + (int)(lane_value(kept, j) - 1.0 - rest);   // a sequence's last tiles see the most keys: first
+        } else {
+          double x = rest / f;
+          if (st != 0.0) {      // f i + st i (i - 1) / 2 <= rest, by the quadratic's root
+            const double u = f / st - 0.5;
+            x = sqrt(u * u + 2.0 * rest / st) - u;
+          }
+          i = min(max((int)x, 0), cut - 1);
+          while (i > 0 && tiles_length(f, st, i) > rest) --i;
+          while (i + 1 < cut && tiles_length(f, st, i + 1) <= rest) ++i;
+        }
+        p.s = s0 + j;
+        p.b = __builtin_amdgcn_readlane(b, j);
+        p.L = __builtin_amdgcn_readlane(L, j);
+        p.lens = __builtin_amdgcn_readlane(lens, j);
+        p.tile = __builtin_amdgcn_readfirstlane(i);
+        p.at = WHOLE ? pos : lane_value(start + tiles_length(f, st, i), 0);
+        p.length = WHOLE ? 1.0 : lane_value(f + st * i, 0);
+        return true;
+      }
+      before = total;
     }
-    before = total;
+    return false;
   }
-  return false;
-}
+};
 
 // What the join of a tile cut between workgroups j - 1 and j needs (pieces = 0: no tile that begins in j - 1).
 struct Cut {
@@ -306,8 +278,10 @@ struct Wave {
   f32x16 o[DT];
   float m, mc, l;      // m in score units, mc = m * scale (0 while m = -infinity), l of this lane's keys
   int lo, hi;          // the keys this lane's query sees: lo <= key <= hi
+  int lane;
 
-  __device__ __forceinline__ void init() {
+  __device__ __forceinline__ void init(int lane_) {
+    lane = lane_;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -318,14 +292,14 @@ struct Wave {
 
   // Query row `src` (all lanes of a pair read theirs); pieces 2 s + l / 32.
   __device__ __forceinline__ void load_query(const T* src) {
-    const int h = (threadIdx.x >> 5) & 1;
+    const int h = lane >> 5;
 #pragma unroll
     for (int s = 0; s < QN; ++s) q[s] = *reinterpret_cast<const uint4*>(src + (2 * s + h) * E);
   }
 
   // Scores of 32 keys, rows r0 .. r0 + 31 of the LDS tile.
   __device__ __forceinline__ f32x16 scores(const unsigned char* K, int r0) const {
-    const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+    const int h = lane >> 5, r = lane & 31;
     const int f = key_swizzle<PPR>(r);
     f32x16 s;
 #pragma unroll
@@ -345,8 +319,8 @@ struct Wave {
   }
 
   // -infinity where the query does not see the key; key0: key of row 0, gone: bit g set where 16 rows have no page.
-  static __device__ __forceinline__ int key_of(int i) {
-    return 8 * (i >> 2) + (i & 3) + 4 * (((int)threadIdx.x >> 5) & 1);
+  __device__ __forceinline__ int key_of(int i) const {
+    return 8 * (i >> 2) + (i & 3) + 4 * (lane >> 5);
   }
   __device__ __forceinline__ void mask(f32x16& s, int key0, int gone) const {
 #pragma unroll
@@ -383,8 +357,8 @@ struct Wave {
   }
 
   // V's operand for 16 keys (rows r0 .. r0 + 15) and 32 columns, in the weights' order.
-  static __device__ __forceinline__ uint4 value_operand(const unsigned char* V, int r0, int t) {
-    const int lane = threadIdx.x & 63, h = lane >> 5, g = (lane >> 4) & 1;
+  __device__ __forceinline__ uint4 value_operand(const unsigned char* V, int r0, int t) const {
+    const int h = lane >> 5, g = (lane >> 4) & 1;
     const int r = 4 * h + ((lane & 15) >> 2);
     const int piece = (4 * t + 2 * g + ((lane & 3) >> 1)) ^ value_swizzle<ES, PPR>(r);
     const unsigned char* at = V + (r0 + r) * RB + (piece << 4) + ((lane & 1) << 3);
@@ -392,8 +366,7 @@ struct Wave {
     return make_uint4(a.x, a.y, b.x, b.y);
   }
   // One fp32 value: column 32 t + l % 32 of the lane's i-th key.
-  static __device__ __forceinline__ float value_at(const unsigned char* V, int r0, int t, int i) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ float value_at(const unsigned char* V, int r0, int t, int i) const {
     const int r = r0 + key_of(i), col = 32 * t + (lane & 31);
     return *reinterpret_cast<const float*>(V + r * RB + (((col >> 2) ^ value_swizzle<ES, PPR>(r)) << 4) +
                                            ((col & 3) << 2));
@@ -427,9 +400,8 @@ struct Wave {
   }
 
   // Which of 32 rows of values hold an infinity or NaN.
-  static __device__ __forceinline__ uint32_t not_finite(const unsigned char* V, int r0) {
+  __device__ __forceinline__ uint32_t not_finite(const unsigned char* V, int r0) const {
     constexpr int LANES = PPR < 64 ? PPR : 64, PER = 64 / LANES;   // lanes of a row, rows at once
-    const int lane = threadIdx.x & 63;
     uint32_t rows = 0;
     for (int r = 0; r < 32; r += PER) {
       const uint4 x = *reinterpret_cast<const uint4*>(V + (r0 + r) * RB + lane * 16);
@@ -456,7 +428,7 @@ struct Wave {
   // out of the product.  They are added key by key to the queries that see them; clear_rows() then takes them out.
   __device__ __forceinline__ void add_rows(const unsigned char* V, int r0, const f32x16& p, uint32_t bad, int key0,
                                            int gone) {
-    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int h = lane >> 5;
     for (uint32_t left = bad; left != 0; left &= left - 1) {
       const int k = __ffs(left) - 1, key = key0 + k;
       float w = 0.f;      // its weight, in the lanes of half (k / 4) % 2
@@ -478,8 +450,7 @@ struct Wave {
       }
     }
   }
-  static __device__ __forceinline__ void clear_rows(unsigned char* V, int r0, uint32_t bad) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ void clear_rows(unsigned char* V, int r0, uint32_t bad) const {
     for (uint32_t left = bad; left != 0; left &= left - 1) {
       const int r = r0 + __ffs(left) - 1;
       for (int x = lane; x < PPR; x += 64) *reinterpret_cast<uint4*>(V + r * RB + x * 16) = make_uint4(0, 0, 0, 0);
@@ -495,8 +466,8 @@ struct Pages {
 };
 
 template <typename A>
-__device__ __forceinline__ void load_pages(const A& a, const int32_t* __restrict__ table, int head, int g0, Pages& p) {
-  const int g = g0 + (int)(threadIdx.x & 63);
+__device__ __forceinline__ void load_pages(const A& a, const int32_t* __restrict__ table, int head, int g0, int lane, Pages& p) {
+  const int g = g0 + lane;
   // g * (ceil(2^32 / n)) >> 32 = g / n: the error g (n - 1) / (n 2^32) is below 1 / n for g < 2^32 / n
   const int page = (int)(((uint64_t)(uint32_t)g * a.granule_magic) >> 32), sub = g - page * a.granules;
   int row = -1;
@@ -512,10 +483,9 @@ __device__ __forceinline__ void load_pages(const A& a, const int32_t* __restrict
 // Copies NR rows of keys (or values) from key `key` on (a multiple of NR, inside of one granule or NR a multiple of
 // 16) to LDS; rows outside of [beg, end) and without a page as zeros.
 template <int ES, int D, int NR, bool VALUES>
-__device__ __forceinline__ void stage_rows(const void* cache, const Pages& pg, int key, int beg, int end, uint32_t lds) {
+__device__ __forceinline__ void stage_rows(const void* cache, const Pages& pg, int key, int beg, int end, int lane, uint32_t lds) {
   constexpr int RB = D * ES, PPR = RB / 16, RPI = 64 / PPR > 0 ? 64 / PPR : 1;   // rows an instruction
   static_assert(PPR <= 64, "a row is at most one instruction");
-  const int lane = threadIdx.x & 63;
   constexpr int GR = NR < 16 ? NR : 16;      // rows of one granule
 #pragma unroll
   for (int g = 0; g < NR / GR; ++g) {
@@ -576,48 +546,100 @@ __device__ __forceinline__ void store_final(T* dst, float x, float y, float z, f
   else store4<T>(dst, x * f, y * f, z * f, u * f);
 }
 
+// The lane, hidden from the compiler: what a piece computes from it is not kept in registers for the next piece.
+__device__ __forceinline__ int fresh_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane & 63;
+}
+
+// A workgroup's next piece: the part [from, to) of a tile's length.
+struct Next {
+  Piece u;
+  double from, to;
+  Shares sh;
+  double end;
+  Cut cut;
+  int j, state;          // share; kTile, kPart, or kNone: nothing left
+};
+enum { kNone, kTile, kPart };
+
+// Finds workgroup j's first piece (first), or the one after the last.  Not inlined: the kernels' registers are full, and
+// what this computes would be kept in them over the pieces.  Every wave has a Next of its own.
+template <bool FEW>
+__device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
+                                                     __attribute__((address_space(3))) Next* k) {
+  Line<FEW> line(a);
+  Shares sh{0.0, 0.0, 0.0, 0.0};
+  double pos = 0.0, end = 0.0;
+  bool tile = a.shares == 0;
+  if (!first) {
+    sh.longest = k->sh.longest, sh.whole = k->sh.whole, sh.rest = k->sh.rest, sh.share = k->sh.share;
+    pos = k->u.at + k->to;
+    end = k->end;
+    j = k->j;
+  } else if (!tile) {
+    sh = line.share_out();
+    const int whole = (int)sh.whole;
+    if (j >= whole + a.shares) {                     // the grid has room for more whole tiles
+      k->state = kNone;
+      k->j = -1;
+      return;
+    }
+    tile = j < whole;
+    if (!tile) j -= whole;
+    pos = j * sh.share;
+    end = fmin(sh.rest, (j + 1) * sh.share);
+  }
+  Piece u{0, 0, 0, 0, 0, 0.0, 0.0};
+  double from = 0.0, to = 1.0;
+  Cut cut{0, 0, 0, 0};
+  int state = kNone;
+  if (tile) {
+    if (line.template find<true>(sh, j, u)) state = kTile;
+    j = -1;
+  } else if (pos < end && line.template find<false>(sh, pos, u)) {
+    from = pos - u.at;
+    to = fmin(u.length, end - u.at);
+    if (to > from) state = kPart;
+    if (first && from > 0.0 && (int)floor(u.at / sh.share) == j - 1)
+      cut = Cut{u.b, u.L, u.tile, (int)ceil((u.at + u.length) / sh.share) - j + 1};
+  }
+  k->u.s = u.s, k->u.b = u.b, k->u.L = u.L, k->u.lens = u.lens, k->u.tile = u.tile;
+  k->u.at = u.at, k->u.length = u.length, k->from = from, k->to = to, k->end = end;
+  k->sh.longest = sh.longest, k->sh.whole = sh.whole, k->sh.rest = sh.rest, k->sh.share = sh.share;
+  k->cut.b = cut.b, k->cut.L = cut.L, k->cut.tile = cut.tile, k->cut.pieces = cut.pieces;
+  k->j = j, k->state = state;
+}
+
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // A workgroup's tile, or its share's pieces one after another: body(piece, from, to, whole, slot) for the part
 // [from, to) of a tile's length; pieces that are not whole tiles have a slot of the workspace.  Without shares every
 // workgroup has a tile.
 template <bool FEW, typename B>
 __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j, B&& body) {
-  Shares sh{0, 0, 0, 1};
-  int64_t pos = 0, end = 0;
-  bool tile = a.shares == 0;
-  if (!tile) {
-    sh = share_out<FEW>(a, G);
-    if (j >= sh.whole + a.shares) return;        // the grid has room for more whole tiles
-    tile = j < sh.whole;
-    if (!tile) {
-      j -= (int)sh.whole;
-      pos = j * sh.share;
-      end = lane_value(min(sh.rest, pos + sh.share), 0);
-    }
+  __shared__ Next next[4];
+  Next& k = next[threadIdx.x >> 6];
+  const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares};
+  for (bool first = true;; first = false) {
+    plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
+    const int state = scalar(k.state), share = scalar(k.j);
+    if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)share * a.c.Hkv + head] = k.cut;
+    if (state == kNone) return;
+    const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), k.u.at, k.u.length};
+    const bool begins = k.from == 0.0;
+    body(u, k.from, k.to, state == kTile || (begins && k.to == u.length), 2 * share + begins);
+    if (state == kTile) return;
   }
-  Cut cut{0, 0, 0, 0};
-  for (bool first = true; tile || pos < end; first = false) {
-    Piece u;
-    int64_t from = 0, to = 1;
-    if (tile) {
-      if (!(a.shares ? find_piece<FEW, true>(a, G, sh, j, u) : find_tile<FEW>(a, G, j, u))) return;
-    } else {
-      if (!find_piece<FEW, false>(a, G, sh, pos, u)) break;
-      from = pos - u.at, to = min(u.length, end - u.at);
-      if (to <= from) break;
-      if (first && from > 0 && u.at / sh.share == j - 1)
-        cut = Cut{u.b, u.L, u.tile, (int)((u.at + u.length - 1) / sh.share) - j + 2};
-    }
-    body(u, from, to, from == 0 && to == u.length, 2 * j + (from == 0));
-    if (tile) return;
-    pos = lane_value(u.at + to, 0);
-  }
-  if (threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)j * a.c.Hkv + head] = cut;
 }
 
 // The blocks of `n` that the part [from, to) of a tile's length is.
-__device__ __forceinline__ void part_blocks(int n, const Piece& u, int64_t from, int64_t to, int& b, int& e) {
-  b = from == 0 ? 0 : (int)(from * n / u.length);
-  e = to == u.length ? n : (int)(to * n / u.length);
+__device__ __forceinline__ void part_blocks(int n, const Piece& u, double from, double to, int& b, int& e) {
+  b = from == 0.0 ? 0 : (int)floor(from * n / u.length);
+  e = to == u.length ? n : (int)floor(to * n / u.length);
+  b = __builtin_amdgcn_readfirstlane(min(b, n));
+  e = __builtin_amdgcn_readfirstlane(min(e, n));
 }
 
 // Many rows: four waves of 32 rows, the same keys.  Tiles of KT keys are double buffered; a tile's loads are issued one
@@ -632,14 +654,15 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
   using S = ManyShape<T, D>;
   constexpr int KT = S::KT, RB = S::RB, ES = (int)sizeof(T), NR = KT / 4;
   extern __shared__ __align__(16) unsigned char smem[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
   const float c = a.scale_log2, slack = 8.f / c;
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int64_t from, int64_t to, bool whole, int slot) {
+  walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, double from, double to, bool whole, int slot) {
+    const int lane = fresh_lane(), h = lane >> 5;
     const Tile<kManyRows> t(a, G, u);
     Wave<T, D> w;
-    w.init();
+    w.init(lane);
     const int mine = wave * 32 + (lane & 31);
     const int64_t out = set_row(a, G, head, t, mine, w);
     const int key_first = t.beg & ~(KT - 1);
@@ -650,10 +673,10 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
     pg.first = -0x40000000;
     auto stage = [&](int i, int buf) {
       const int key = key_first + i * KT;
-      if ((key >> 4) - pg.first >= 64) load_pages(a, table, head, key >> 4, pg);
+      if ((key >> 4) - pg.first >= 64) load_pages(a, table, head, key >> 4, lane, pg);
       const uint32_t at = lds + (uint32_t)(buf * 2 * KT * RB + wave * NR * RB);
-      stage_rows<ES, D, NR, false>(a.k_cache, pg, key + wave * NR, t.beg, t.end, at);
-      stage_rows<ES, D, NR, true>(a.v_cache, pg, key + wave * NR, t.beg, t.end, at + KT * RB);
+      stage_rows<ES, D, NR, false>(a.k_cache, pg, key + wave * NR, t.beg, t.end, lane, at);
+      stage_rows<ES, D, NR, true>(a.v_cache, pg, key + wave * NR, t.beg, t.end, lane, at + KT * RB);
       return (int)((pg.none >> ((key >> 4) - pg.first)) & ((1 << (KT / 16)) - 1));
     };
     lds_barrier();                                 // nobody reads the last piece's tiles any more
@@ -727,16 +750,17 @@ void cache_attention_few_kernel(AttendArgs a) {
   constexpr int RB = D * (int)sizeof(T), ES = (int)sizeof(T), NW = few_group(RB), NI = 32 * RB / 1024;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ float2 ml[NW][32];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
   const float c = a.scale_log2, slack = 8.f / c;
   unsigned char* K = smem + wave * 64 * RB;
   unsigned char* V = K + 32 * RB;
   const uint32_t ldsK = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * 64 * RB;
-  walk<true>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int64_t from, int64_t to, bool whole, int slot) {
+  walk<true>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, double from, double to, bool whole, int slot) {
+    const int lane = fresh_lane();
     const Tile<kFewRows> t(a, G, u);
     Wave<T, D> w;
-    w.init();
+    w.init(lane);
     const int key_first = t.beg & ~31;
     int tb, te;
     part_blocks(t.end > t.beg ? (t.end - key_first + 31) / 32 : 0, u, from, to, tb, te);
@@ -745,14 +769,14 @@ void cache_attention_few_kernel(AttendArgs a) {
     pg.first = -0x40000000;
     auto pages_for = [&](int i) {
       const int g = (key_first >> 4) + 2 * i;
-      if (g - pg.first >= 64) load_pages(a, table, head, g, pg);
+      if (g - pg.first >= 64) load_pages(a, table, head, g, lane, pg);
       return (int)((pg.none >> (g - pg.first)) & 3);
     };
     int i = tb + wave, gone = 0;
     if (i < te) {
       gone = pages_for(i);
-      stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK);
-      stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK + 32 * RB);
+      stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, lane, ldsK);
+      stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, lane, ldsK + 32 * RB);
     }
     set_row(a, G, head, t, lane & 31, w);
     for (; i < te; i += NW) {
@@ -762,7 +786,7 @@ void cache_attention_few_kernel(AttendArgs a) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (next < te) {
         gone = pages_for(next);
-        stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK);
+        stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, lane, ldsK);
       }
       const bool part = key + 31 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
       if (part) w.mask(s, key, absent);
@@ -783,7 +807,7 @@ void cache_attention_few_kernel(AttendArgs a) {
       }
       w.add_values(V, 0, s);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (next < te) stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK + 32 * RB);
+      if (next < te) stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, lane, ldsK + 32 * RB);
     }
     // join the waves: everyone's accumulators in LDS (pieces of 16 bytes at piece ^ row % 8)
     const float l = other_half_sum(w.l);
@@ -828,54 +852,78 @@ void cache_attention_few_kernel(AttendArgs a) {
   });
 }
 
-// Joins the pieces of tiles that lie in several shares, in their order.  A wave takes 64 columns (or D = 32) of a row,
-// its groups of lanes every few pieces.
+// Joins the pieces of tiles that lie in several shares.  Its rows go round among gridDim.y workgroups; a thread has 4
+// columns of a row and every few pieces of it (a running maximum and sum over them), the groups of pieces are joined in
+// LDS, in their order.
+constexpr int kJoinThreads = 1024;
+
 template <typename T, int D, int ROWS>
-__global__ __launch_bounds__(256) void cache_attention_join_kernel(AttendArgs a) {
-  constexpr int COLS = D < 64 ? D : 64, LANES = COLS / 4, GROUPS = 64 / LANES, PARTS = D / COLS;
-  __shared__ float weights[4][kMostShares];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(AttendArgs a) {
+  constexpr int COLS = D / 4;
+  __shared__ float2 ml[kJoinThreads];
+  __shared__ float4 sums[kJoinThreads];
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
   if (cut.pieces < 2 || cut.pieces > a.shares) return;
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), j = (int)(blockIdx.x / a.c.Hkv);
-  const int row0 = cut.tile * ROWS, items = min(ROWS, cut.L * G - row0) * PARTS;
-  float* weight = weights[wave];
-  for (int i = (int)blockIdx.y * 4 + wave; i < items; i += 4 * (int)gridDim.y) {
-    const int n = i / PARTS, col = i % PARTS * COLS + lane % LANES * 4, group = lane / LANES;
-    // piece k: the end of share j - 1, then the beginnings of the next ones
-    auto at = [&](int k) {
-      return ((int64_t)(k == 0 ? 2 * (j - 1) + 1 : 2 * (j - 1 + k)) * a.c.Hkv + head) * ROWS + n;
-    };
-    float m = -INFINITY;
-    for (int k = lane; k < cut.pieces; k += 64) {
-      const float x = a.part_ml[at(k) * 2];
-      weight[k] = x;
-      m = fmaxf(m, x);
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
-    float l = 0.f;
-    for (int k = lane; k < cut.pieces; k += 64) {
-      const float x = weight[k], f = x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x - m) * a.scale_log2);
-      weight[k] = f;
-      l += f * a.part_ml[at(k) * 2 + 1];
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) l += __shfl_xor(l, k);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the weights, which only this wave reads
+  const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
+  const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
+  if (items <= 0) return;
+  const int groups = max(1, min(kJoinThreads / items, (cut.pieces + 3) / 4)), group = threadIdx.x / items;
+  for (int base = 0; base < items; base += kJoinThreads) {      // more than once only with one group
+    const int item = base + (groups > 1 ? (int)threadIdx.x - group * items : (int)threadIdx.x);
+    const bool on = groups > 1 ? group < groups : item < items;
+    const int n = (int)blockIdx.y + item / COLS * turn, col = item % COLS * 4;
+    float m = -INFINITY, l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = group; k < cut.pieces; k += GROUPS) {
-      const float4 p = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col);
-      const float f = weight[k];
-      sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
-    }
+    if (on) {
+      // piece k: the end of share j - 1, then the beginnings of the next ones
+      auto at = [&](int k) {
+        return ((int64_t)(k == 0 ? 2 * (j - 1) + 1 : 2 * (j - 1 + k)) * a.c.Hkv + head) * ROWS + n;
+      };
+      const int first = groups > 1 ? group : 0;
+      for (int k0 = first; k0 < cut.pieces; k0 += 4 * groups) {
+        float2 x[4];
+        float4 p[4];
 #pragma unroll
-    for (int k = LANES; k < 64; k <<= 1) {
-      sum.x += __shfl_xor(sum.x, k), sum.y += __shfl_xor(sum.y, k);
-      sum.z += __shfl_xor(sum.z, k), sum.w += __shfl_xor(sum.w, k);
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + i * groups;
+          x[i] = make_float2(-INFINITY, 0.f);
+          p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < cut.pieces) {
+            x[i] = *reinterpret_cast<const float2*>(a.part_ml + at(k) * 2);
+            p[i] = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col);
+          }
+        }
+        const float top = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(fmaxf(x[2].x, x[3].x), m));
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale_log2);
+        sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
+        l *= f;
+        m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = x[i].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x[i].x - m) * a.scale_log2);
+          sum.x += w * p[i].x, sum.y += w * p[i].y, sum.z += w * p[i].z, sum.w += w * p[i].w;
+          l += w * x[i].y;
+        }
+      }
     }
-    if (group == 0) {
+    if (groups > 1) {
+      ml[threadIdx.x] = make_float2(m, l);
+      sums[threadIdx.x] = sum;
+      __syncthreads();
+      if (group != 0) return;
+      for (int g = 1; g < groups; ++g) m = fmaxf(m, ml[g * items + item].x);
+      l = 0.f;
+      sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = 0; g < groups; ++g) {
+        const float2 x = ml[g * items + item];
+        const float4 p = sums[g * items + item];
+        const float w = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * a.scale_log2);
+        sum.x += w * p.x, sum.y += w * p.y, sum.z += w * p.z, sum.w += w * p.w;
+        l += w * x.y;
+      }
+    }
+    if (on) {
       const int token = (row0 + n) / G, g = row0 + n - token * G;
       store_final(static_cast<T*>(a.o) + ((int64_t)(cut.b + token) * a.c.Hq + head * G + g) * D + col, sum.x, sum.y,
                   sum.z, sum.w, l);
@@ -910,8 +958,8 @@ static hipError_t launch_attend_d(const AttendArgs& a, hipStream_t s) {
   prof_end(K_ATTEND, s);
   if ((e = hipGetLastError()) != hipSuccess || a.shares < 2) return e;
   prof_begin(K_ATTEND_JOIN, s);
-  if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), dim3(shares, 16), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), dim3(shares, 32), dim3(256), 0, s, a);
+  if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), dim3(shares, 4), dim3(kJoinThreads), 0, s, a);
+  else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), dim3(shares, 4), dim3(kJoinThreads), 0, s, a);
   prof_end(K_ATTEND_JOIN, s);
   return hipGetLastError();
 }
