@@ -110,7 +110,7 @@ CacheArgs cache_args(const gdn_cache_shape* sh, const int32_t* table, const int3
 
 // How the attention of a call is cut: rows of a tile, shares of a head's work (0: a tile each).
 struct Plan {
-  int32_t few, shares, rows;
+  int32_t few, shares, rows, unit;
   int64_t tiles;
 };
 
@@ -124,6 +124,9 @@ Plan attention_plan(const gdn_cache_shape* sh, int64_t tokens, bool ragged) {
   const int rb = sh->d * (int)elem_size(sh->dtype), at_once = 256 * (p.few ? few_waves(rb) : many_waves(rb));
   if ((int64_t)sh->max_pages * sh->page_size > (p.few ? kFewKeys : kManyKeys))
     p.shares = std::max(1, std::min(kMostShares, at_once / sh->Hkv));
+  // all tiles with all keys, twice that where they are drawn out, stay below 2^30 units
+  const int64_t keys = (int64_t)sh->max_pages * sh->page_size + 64 + p.rows;
+  while (((p.tiles + sh->N) * ((keys >> p.unit) + 2)) > (1LL << 28)) ++p.unit;
   return p;
 }
 
@@ -237,7 +240,7 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   a.window = std::min(window, 1 << 30);
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;
-  a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles;
+  a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles; a.unit = plan.unit;
   if (need > 0) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + part_rows(sh, plan) * sh->d;

@@ -23,7 +23,6 @@
 
 #include "gdn_cache_device.h"
 #include "gdn_rows.h"
-#include "gdn_scan.h"
 
 namespace gdn {
 namespace attend {
@@ -79,20 +78,28 @@ __device__ __forceinline__ int value_swizzle(int r) {
   else return ((r >> 1) & 1) << 1;
 }
 
-__device__ __forceinline__ double lane_value(double x, int lane) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
+
+// Inclusive prefix sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+  return x;
 }
+__device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x), 63); }
 
 // How the work of one head is laid out.
 //
-// The tiles of all sequences lie on one line, a tile as long as the keys it sees (times G, plus what starting one
-// costs): v_i = first + step * i for tile i of a sequence, exact up to the last block of keys.  The first workgroups take
-// whole tiles, one each; what is left of the line is cut into `shares` even pieces, whatever the sequences' lengths are:
-// the rest of one tile, whole tiles, the beginning of one more.  Pieces that are not whole tiles go to the workspace and
-// are joined.
+// The tiles of all sequences lie on one line, a tile about as long as the keys it sees and what starting one costs, in
+// units of 2^unit keys that the host chooses so that the line is shorter than 2^30: v_i = first + step * i for tile i
+// of a sequence.  The first workgroups take whole tiles, one each; what is left of the line is cut into `shares` even
+// pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one more.  Pieces that
+// are not whole tiles go to the workspace and are joined.
 //
 // Few rows: everything is cut (each key is read by one workgroup anyway).  Many rows: workgroups that walk one head's
 // keys side by side read them from the cache they share, and pieces that begin anywhere do not (16384 keys of 8 heads,
@@ -100,25 +107,26 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
 // of a sequence, which see the most keys, first; with three rounds or more nothing is cut.  Tiles longer than 5/4 of an even
 // share are always cut, so that one long sequence does not outlast all others.
 //
-// Lengths are doubles, whole numbers below 2^53 for anything that runs in a day; beyond, they are rounded the same in
-// every workgroup, so that pieces still meet.
+// Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one piece, and a
+// second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.
 struct Piece {
   int s, b, L, lens, tile;
-  double at, length;       // the tile's start and length on the line
+  int at, length;          // the tile's start and length on the line
 };
 
 // What all workgroups of a call agree on.
 struct Shares {
-  double longest;          // of the tiles that may stay whole
-  double whole;            // tiles that stay whole
-  double rest, share;      // length of the line that is left, and of a share of it
+  int longest;             // of the tiles that may stay whole
+  int whole;               // tiles that stay whole
+  int rest, share;         // length of the line that is left, and of a share of it
+  int drawn;               // tiles are whole numbers of shares
 };
 
 // What the work is laid out from.
 struct Work {
   const int32_t* cu;
   const int32_t* lens;
-  int N, T, total, G, room, window, tiles, shares;
+  int N, T, total, G, room, window, tiles, shares, unit;
 };
 
 template <bool FEW>
@@ -127,12 +135,7 @@ struct Line {
   const Work& a;
   int base;                // sequences base .. base + 63 are loaded, one a lane
   int b, L, lens, tiles;
-  double first, step;
-
-  // i tiles of a sequence.
-  static __device__ __forceinline__ double tiles_length(double first, double step, double i) {
-    return first * i + step * (i * (i - 1.0) * 0.5);
-  }
+  int first, step;
 
   __device__ __forceinline__ explicit Line(const Work& work) : a(work), base(-1) {}
 
@@ -140,106 +143,128 @@ struct Line {
     if (s0 == base) return;
     base = s0;
     const int s = s0 + (int)(threadIdx.x & 63);
-    b = L = lens = tiles = 0;
-    first = step = 0.0;
+    b = L = lens = tiles = first = step = 0;
     if (s < a.N) {
       int e;
       seq_range(a.cu, a.T, a.total, s, b, e);
       L = e - b;
       lens = min(max(a.lens[s], -(1 << 30)), 1 << 30);
       tiles = (int)(((int64_t)L * a.G + ROWS - 1) / ROWS);
-      const int old = min(max(lens - L, 0), a.room);
+      const int old = min(max(lens - L, 0), a.room), more = ROWS / a.G + 1;
       const bool inside = a.window > 0 && a.window < old;
-      first = (double)a.G * (double)((inside ? a.window : old) + 64) + ROWS;
-      step = inside ? 0.0 : ROWS;
+      first = (((inside ? a.window : old) + 64 + more) >> a.unit) + 1;
+      step = inside ? 0 : more >> a.unit;
     }
+  }
+
+  // i tiles of a sequence.
+  static __device__ __forceinline__ int tiles_length(int first, int step, int i) {
+    return first * i + (int)((int64_t)step * (((int64_t)i * (i - 1)) >> 1));
+  }
+  // The lane's sequence without its last `kept` tiles.
+  __device__ __forceinline__ int length(int kept, const Shares& sh) const {
+    if (FEW && sh.drawn) return tiles * drawn_tile(first, step, tiles, sh);
+    return tiles_length(first, step, tiles - kept);
+  }
+  static __device__ __forceinline__ int drawn_tile(int first, int step, int tiles, const Shares& sh) {
+    return tiles > 0 ? (int)((float)(first + step * (tiles - 1)) / (float)sh.share + 0.999f) * sh.share : 0;
   }
 
   // How many of the lane's tiles may stay whole, however many others do.
-  __device__ __forceinline__ double may_be_whole(double longest) const {
-    return !FEW && first + step * (double)(tiles - 1) <= longest ? (double)tiles : 0.0;
+  __device__ __forceinline__ int may_be_whole(int longest) const {
+    return !FEW && first + step * (tiles - 1) <= longest ? tiles : 0;
   }
 
-  static __device__ __forceinline__ double sum(double x) { return lane_value(wave_scan64(x), 63); }
-
   __device__ __forceinline__ Shares share_out() {
-    Shares r{0.0, 0.0, 0.0, 0.0};
-    double all = 0.0;
+    Shares r{0, 0, 0, 1, 0};
+    int all = 0, count = 0;
     for (int s = 0; s < a.N; s += 64) {
       load(s);
-      all += sum(tiles_length(first, step, tiles));
+      all += wave_sum(tiles_length(first, step, tiles));
+      if constexpr (FEW) count += wave_sum(tiles);
     }
-    const double even = ceil(all / a.shares), least = (double)a.G * (FEW ? kFewKeys : kManyKeys);
+    // (a little more than an even share does no harm)
+    auto parts = [](int x, int n) { return (int)((float)x / (float)n * 1.000001f) + 1; };
+    const int even = parts(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
     r.rest = all;
-    if constexpr (!FEW) {
-      r.longest = fmax(even * 1.25, 2.0 * least);
-      double may = 0.0, sure = 0.0;
-      for (int s = 0; s < a.N; s += 64) {
-        load(s);
-        const double w = may_be_whole(r.longest);
-        may += sum(w);
-        sure += sum((double)tiles - w);
+    if constexpr (FEW) {
+      r.drawn = count * 4 <= a.shares;
+      r.share = max(least, r.drawn ? parts(all, a.shares - count) : even);
+      if (r.drawn) {
+        r.rest = 0;
+        for (int s = 0; s < a.N; s += 64) {
+          load(s);
+          r.rest += wave_sum(length(0, r));
+        }
       }
-      const double rounds = floor(may / a.shares);
-      r.whole = sure == 0.0 && (rounds >= 3.0 || r.longest == 2.0 * least) ? may : rounds * a.shares;
-      r.whole = fmin(r.whole, (double)a.tiles);  // (malformed offsets may count more tiles than there is room for)
-      // what is left after them
-      double before = 0.0;
-      r.rest = 0.0;
+    } else {
+      r.longest = max(even + even / 4, 2 * least);
+      int may = 0, sure = 0;
       for (int s = 0; s < a.N; s += 64) {
         load(s);
-        const double mine = may_be_whole(r.longest), upto = before + wave_scan64(mine);
-        const double kept = fmin(fmax(r.whole - (upto - mine), 0.0), mine);
-        r.rest += sum(tiles_length(first, step, (double)tiles - kept));
+        const int w = may_be_whole(r.longest);
+        may += wave_sum(w);
+        sure += wave_sum(tiles - w);
+      }
+      const int rounds = (int)((float)may / (float)a.shares);      // (counts below 2^24 are exact)
+      r.whole = sure == 0 && (rounds >= 3 || r.longest == 2 * least) ? may : rounds * a.shares;
+      r.whole = max(min(r.whole, a.tiles), 0);     // (malformed offsets may count more tiles than there is room for)
+      int before = 0;
+      r.rest = 0;
+      for (int s = 0; s < a.N; s += 64) {
+        load(s);
+        const int mine = may_be_whole(r.longest), upto = before + wave_scan(mine);
+        r.rest += wave_sum(length(min(max(r.whole - (upto - mine), 0), mine), r));
         before = lane_value(upto, 63);
       }
+      r.share = max(least, parts(r.rest, a.shares));
     }
-    r.share = fmax(ceil(r.rest / a.shares), least);
     return r;
   }
 
   // The tile number `pos` of those that are whole (WHOLE; of all tiles if nothing is shared), or the sequence and tile
   // at `pos` of what is left.
   template <bool WHOLE>
-  __device__ __forceinline__ bool find(const Shares& sh, double pos, Piece& p) {
-    double tiles_before = 0.0, before = 0.0;
+  __device__ __forceinline__ bool find(const Shares& sh, int pos, Piece& p) {
+    int tiles_before = 0, before = 0;
     for (int s0 = 0; s0 < a.N; s0 += 64) {
       load(s0);
-      double kept = 0.0;
+      int kept = 0;
       if (a.shares == 0) {
         kept = tiles;
       } else if constexpr (!FEW) {
-        const double may = may_be_whole(sh.longest), upto = tiles_before + wave_scan64(may);
-        kept = fmin(fmax(sh.whole - (upto - may), 0.0), may);
+        const int may = may_be_whole(sh.longest), upto = tiles_before + wave_scan(may);
+        kept = min(max(sh.whole - (upto - may), 0), may);
         tiles_before = lane_value(upto, 63);
       }
-      const double mine = WHOLE ? kept : tiles_length(first, step, (double)tiles - kept);
-      const double upto = before + wave_scan64(mine), total = lane_value(upto, 63);
+      const int mine = WHOLE ? kept : length(kept, sh), upto = before + wave_scan(mine), total = lane_value(upto, 63);
       if (pos < total) {
         const int j = __ffsll((unsigned long long)__ballot(pos < upto)) - 1;
-        const double f = lane_value(first, j), st = lane_value(step, j), start = lane_value(upto - mine, j);
-        const double rest = pos - start;
-        const int cut = __builtin_amdgcn_readlane(tiles, j) - (int)lane_value(kept, j);   // tiles that are not whole
-        int i;
+        const int rest = pos - lane_value(upto - mine, j), n = lane_value(tiles, j);
+        const int cut = n - lane_value(kept, j);     // tiles that are not whole
+        int f = lane_value(first, j), st = lane_value(step, j), i = 0;
         if constexpr (WHOLE) {
-          i = cut + (int)(lane_value(kept, j) - 1.0 - rest);   // a sequence's last tiles see the most keys: first
+          i = n - 1 - rest;                          // a sequence's last tiles see the most keys: first
         } else {
-          double x = rest / f;
-          if (st != 0.0) {      // f i + st i (i - 1) / 2 <= rest, by the quadratic's root
-            const double u = f / st - 0.5;
-            x = sqrt(u * u + 2.0 * rest / st) - u;
+          if (FEW && sh.drawn) f = drawn_tile(f, st, n, sh), st = 0;
+          if (cut > 1) {          // f i + st i (i - 1) / 2 <= rest, nearly by the quadratic's root, then exactly
+            float x = (float)rest / (float)f;
+            if (st != 0) {
+              const float v = (float)f / (float)st - 0.5f;
+              x = sqrtf(v * v + 2.f * (float)rest / (float)st) - v;
+            }
+            i = min(max((int)x, 0), cut - 1);
+            while (i > 0 && tiles_length(f, st, i) > rest) --i;
+            while (i + 1 < cut && tiles_length(f, st, i + 1) <= rest) ++i;
           }
-          i = min(max((int)x, 0), cut - 1);
-          while (i > 0 && tiles_length(f, st, i) > rest) --i;
-          while (i + 1 < cut && tiles_length(f, st, i + 1) <= rest) ++i;
         }
         p.s = s0 + j;
-        p.b = __builtin_amdgcn_readlane(b, j);
-        p.L = __builtin_amdgcn_readlane(L, j);
-        p.lens = __builtin_amdgcn_readlane(lens, j);
-        p.tile = __builtin_amdgcn_readfirstlane(i);
-        p.at = WHOLE ? pos : lane_value(start + tiles_length(f, st, i), 0);
-        p.length = WHOLE ? 1.0 : lane_value(f + st * i, 0);
+        p.b = lane_value(b, j);
+        p.L = lane_value(L, j);
+        p.lens = lane_value(lens, j);
+        p.tile = i;
+        p.at = WHOLE ? pos : pos - rest + tiles_length(f, st, i);
+        p.length = WHOLE ? 1 : f + st * i;
         return true;
       }
       before = total;
@@ -556,9 +581,9 @@ __device__ __forceinline__ int fresh_lane() {
 // A workgroup's next piece: the part [from, to) of a tile's length.
 struct Next {
   Piece u;
-  double from, to;
+  int from, to;
   Shares sh;
-  double end;
+  int end;
   Cut cut;
   int j, state;          // share; kTile, kPart, or kNone: nothing left
 };
@@ -570,29 +595,30 @@ template <bool FEW>
 __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
                                                      __attribute__((address_space(3))) Next* k) {
   Line<FEW> line(a);
-  Shares sh{0.0, 0.0, 0.0, 0.0};
-  double pos = 0.0, end = 0.0;
+  Shares sh{0, 0, 0, 1, 0};
+  int pos = 0, end = 0;
   bool tile = a.shares == 0;
   if (!first) {
     sh.longest = k->sh.longest, sh.whole = k->sh.whole, sh.rest = k->sh.rest, sh.share = k->sh.share;
+    sh.drawn = k->sh.drawn;
     pos = k->u.at + k->to;
     end = k->end;
     j = k->j;
   } else if (!tile) {
     sh = line.share_out();
-    const int whole = (int)sh.whole;
-    if (j >= whole + a.shares) {                     // the grid has room for more whole tiles
+    if (j >= sh.whole + a.shares) {                  // the grid has room for more whole tiles
       k->state = kNone;
       k->j = -1;
       return;
     }
-    tile = j < whole;
-    if (!tile) j -= whole;
-    pos = j * sh.share;
-    end = fmin(sh.rest, (j + 1) * sh.share);
+    tile = j < sh.whole;
+    if (!tile) j -= sh.whole;
+    const int64_t at = (int64_t)j * sh.share;
+    pos = (int)min(at, (int64_t)sh.rest);
+    end = (int)min(at + sh.share, (int64_t)sh.rest);
   }
-  Piece u{0, 0, 0, 0, 0, 0.0, 0.0};
-  double from = 0.0, to = 1.0;
+  Piece u{0, 0, 0, 0, 0, 0, 0};
+  int from = 0, to = 1;
   Cut cut{0, 0, 0, 0};
   int state = kNone;
   if (tile) {
@@ -600,19 +626,23 @@ __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
     j = -1;
   } else if (pos < end && line.template find<false>(sh, pos, u)) {
     from = pos - u.at;
-    to = fmin(u.length, end - u.at);
+    to = min(u.length, end - u.at);
     if (to > from) state = kPart;
-    if (first && from > 0.0 && (int)floor(u.at / sh.share) == j - 1)
-      cut = Cut{u.b, u.L, u.tile, (int)ceil((u.at + u.length) / sh.share) - j + 1};
+    if (first && from > 0 && u.at >= pos - sh.share) {
+      const int last = u.at + u.length;
+      int n = max((int)((float)last / (float)sh.share), j);      // the share that ends the tile
+      while (n > j && (int64_t)n * sh.share >= last) --n;
+      while ((int64_t)(n + 1) * sh.share < last) ++n;
+      cut = Cut{u.b, u.L, u.tile, n - j + 2};
+    }
   }
   k->u.s = u.s, k->u.b = u.b, k->u.L = u.L, k->u.lens = u.lens, k->u.tile = u.tile;
   k->u.at = u.at, k->u.length = u.length, k->from = from, k->to = to, k->end = end;
   k->sh.longest = sh.longest, k->sh.whole = sh.whole, k->sh.rest = sh.rest, k->sh.share = sh.share;
+  k->sh.drawn = sh.drawn;
   k->cut.b = cut.b, k->cut.L = cut.L, k->cut.tile = cut.tile, k->cut.pieces = cut.pieces;
   k->j = j, k->state = state;
 }
-
-__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // A workgroup's tile, or its share's pieces one after another: body(piece, from, to, whole, slot) for the part
 // [from, to) of a tile's length; pieces that are not whole tiles have a slot of the workspace.  Without shares every
@@ -621,25 +651,26 @@ template <bool FEW, typename B>
 __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j, B&& body) {
   __shared__ Next next[4];
   Next& k = next[threadIdx.x >> 6];
-  const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares};
+  const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares,
+                  a.unit};
   for (bool first = true;; first = false) {
     plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
     const int state = scalar(k.state), share = scalar(k.j);
     if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)share * a.c.Hkv + head] = k.cut;
     if (state == kNone) return;
-    const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), k.u.at, k.u.length};
-    const bool begins = k.from == 0.0;
-    body(u, k.from, k.to, state == kTile || (begins && k.to == u.length), 2 * share + begins);
+    const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), scalar(k.u.at),
+                  scalar(k.u.length)};
+    const int from = scalar(k.from), to = scalar(k.to);
+    body(u, from, to, state == kTile || (from == 0 && to == u.length), 2 * share + (from == 0));
     if (state == kTile) return;
   }
 }
 
-// The blocks of `n` that the part [from, to) of a tile's length is.
-__device__ __forceinline__ void part_blocks(int n, const Piece& u, double from, double to, int& b, int& e) {
-  b = from == 0.0 ? 0 : (int)floor(from * n / u.length);
-  e = to == u.length ? n : (int)floor(to * n / u.length);
-  b = __builtin_amdgcn_readfirstlane(min(b, n));
-  e = __builtin_amdgcn_readfirstlane(min(e, n));
+// The blocks of `n` that the part [from, to) of a tile's length is: the same function of a border on both its sides.
+__device__ __forceinline__ void part_blocks(int n, const Piece& u, int from, int to, int& b, int& e) {
+  const float blocks = (float)n / (float)u.length;
+  b = scalar(min((int)((float)from * blocks), n));
+  e = to == u.length ? n : scalar(min((int)((float)to * blocks), n));
 }
 
 // Many rows: four waves of 32 rows, the same keys.  Tiles of KT keys are double buffered; a tile's loads are issued one
@@ -658,7 +689,7 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
   const float c = a.scale_log2, slack = 8.f / c;
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
-  walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, double from, double to, bool whole, int slot) {
+  walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int from, int to, bool whole, int slot) {
     const int lane = fresh_lane(), h = lane >> 5;
     const Tile<kManyRows> t(a, G, u);
     Wave<T, D> w;
@@ -756,7 +787,7 @@ void cache_attention_few_kernel(AttendArgs a) {
   unsigned char* K = smem + wave * 64 * RB;
   unsigned char* V = K + 32 * RB;
   const uint32_t ldsK = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * 64 * RB;
-  walk<true>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, double from, double to, bool whole, int slot) {
+  walk<true>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int from, int to, bool whole, int slot) {
     const int lane = fresh_lane();
     const Tile<kFewRows> t(a, G, u);
     Wave<T, D> w;
@@ -859,7 +890,7 @@ constexpr int kJoinThreads = 1024;
 
 template <typename T, int D, int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(AttendArgs a) {
-  constexpr int COLS = D / 4;
+  constexpr int COLS = D / 4, AT_ONCE = 8;
   __shared__ float2 ml[kJoinThreads];
   __shared__ float4 sums[kJoinThreads];
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
@@ -868,7 +899,7 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
   const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
   const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
   if (items <= 0) return;
-  const int groups = max(1, min(kJoinThreads / items, (cut.pieces + 3) / 4)), group = threadIdx.x / items;
+  const int groups = max(1, min(kJoinThreads / items, (cut.pieces + AT_ONCE - 1) / AT_ONCE)), group = threadIdx.x / items;
   for (int base = 0; base < items; base += kJoinThreads) {      // more than once only with one group
     const int item = base + (groups > 1 ? (int)threadIdx.x - group * items : (int)threadIdx.x);
     const bool on = groups > 1 ? group < groups : item < items;
@@ -881,11 +912,12 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
         return ((int64_t)(k == 0 ? 2 * (j - 1) + 1 : 2 * (j - 1 + k)) * a.c.Hkv + head) * ROWS + n;
       };
       const int first = groups > 1 ? group : 0;
-      for (int k0 = first; k0 < cut.pieces; k0 += 4 * groups) {
-        float2 x[4];
-        float4 p[4];
+      for (int k0 = first; k0 < cut.pieces; k0 += AT_ONCE * groups) {
+        float2 x[AT_ONCE];
+        float4 p[AT_ONCE];
+        float top = m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < AT_ONCE; ++i) {
           const int k = k0 + i * groups;
           x[i] = make_float2(-INFINITY, 0.f);
           p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -894,13 +926,14 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
             p[i] = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col);
           }
         }
-        const float top = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(fmaxf(x[2].x, x[3].x), m));
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, x[i].x);
         const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale_log2);
         sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
         l *= f;
         m = top;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < AT_ONCE; ++i) {
           const float w = x[i].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x[i].x - m) * a.scale_log2);
           sum.x += w * p[i].x, sum.y += w * p[i].y, sum.z += w * p[i].z, sum.w += w * p[i].w;
           l += w * x[i].y;

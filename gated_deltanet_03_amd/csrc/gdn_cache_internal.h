@@ -44,6 +44,7 @@ struct AttendArgs {
   int32_t few;           // one 32-row tile a workgroup, its waves on different keys
   int32_t shares;        // even shares of a head's work, 0: a tile for each workgroup
   int32_t tiles;         // upper bound on a head's tiles
+  int32_t unit;          // log2 of the keys of a unit of work
   float* part_o;         // [2 shares, Hkv, rows of a tile, d]
   float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
   void* cuts;            // [shares, Hkv] of 16 bytes
