@@ -241,6 +241,9 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;
   a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles; a.unit = plan.unit;
+  // 16 us of many rows' keys, or 5 us of few rows' (a workgroup's rates beside the others')
+  const int32_t keys = (plan.few ? 1 : 2) * (sh->dtype == GDN_F32 ? 8192 : 40960) / sh->d;
+  a.extra = keys >> plan.unit;
   if (need > 0) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + part_rows(sh, plan) * sh->d;

@@ -91,6 +91,11 @@ __device__ __forceinline__ int wave_scan(int x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
   return x;
 }
+__device__ __forceinline__ int wave_max(int x) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) x = max(x, __shfl_xor(x, m));
+  return scalar(x);
+}
 __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x), 63); }
 
 // How the work of one head is laid out.
@@ -101,14 +106,20 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 // pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one more.  Pieces that
 // are not whole tiles go to the workspace and are joined.
 //
-// Few rows: everything is cut (each key is read by one workgroup anyway).  Many rows: workgroups that walk one head's
-// keys side by side read them from the cache they share, and pieces that begin anywhere do not (16384 keys of 8 heads,
-// 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole rounds of `shares` tiles stay whole, the last ones
-// of a sequence, which see the most keys, first; with three rounds or more nothing is cut.  Tiles longer than 5/4 of an even
-// share are always cut, so that one long sequence does not outlast all others.
+// Nothing is cut where that would end no later: the longest tile, and with more tiles than shares half of it above an even
+// share, against an even share and `extra`, what the pieces and their join cost (measured with 512 tiles of 128 rows or
+// fewer: about 16 us with many rows, 5 us with few).
 //
-// Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one piece, and a
-// second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.
+// Many rows: workgroups that walk one head's keys side by side read them from the cache they share, and pieces that
+// begin anywhere do not (16384 keys of 8 heads, 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole
+// rounds of `shares` tiles stay whole, the last ones of a sequence, which see the most keys, first; with three rounds or
+// more nothing is cut.  Tiles longer than 5/4 of an even share are always cut, so that one long sequence does not
+// outlast all others.
+//
+// Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one
+// piece, and a second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.
+//
+// Borders between shares that come within a 16th of a share of a tile's end are moved there.
 struct Piece {
   int s, b, L, lens, tile;
   int at, length;          // the tile's start and length on the line
@@ -126,7 +137,7 @@ struct Shares {
 struct Work {
   const int32_t* cu;
   const int32_t* lens;
-  int N, T, total, G, room, window, tiles, shares, unit;
+  int N, T, total, G, room, window, tiles, shares, unit, extra;
 };
 
 template <bool FEW>
@@ -163,7 +174,7 @@ struct Line {
   }
   // The lane's sequence without its last `kept` tiles.
   __device__ __forceinline__ int length(int kept, const Shares& sh) const {
-    if (FEW && sh.drawn) return tiles * drawn_tile(first, step, tiles, sh);
+    if (sh.drawn) return tiles * drawn_tile(first, step, tiles, sh);
     return tiles_length(first, step, tiles - kept);
   }
   static __device__ __forceinline__ int drawn_tile(int first, int step, int tiles, const Shares& sh) {
@@ -172,33 +183,40 @@ struct Line {
 
   // How many of the lane's tiles may stay whole, however many others do.
   __device__ __forceinline__ int may_be_whole(int longest) const {
-    return !FEW && first + step * (tiles - 1) <= longest ? tiles : 0;
+    return first + step * (tiles - 1) <= longest ? tiles : 0;
   }
 
   __device__ __forceinline__ Shares share_out() {
     Shares r{0, 0, 0, 1, 0};
-    int all = 0, count = 0;
+    int all = 0, count = 0, longest = 0;
     for (int s = 0; s < a.N; s += 64) {
       load(s);
       all += wave_sum(tiles_length(first, step, tiles));
-      if constexpr (FEW) count += wave_sum(tiles);
+      count += wave_sum(tiles);
+      longest = max(longest, wave_max(tiles > 0 ? first + step * (tiles - 1) : 0));
     }
-    // (a little more than an even share does no harm)
-    auto parts = [](int x, int n) { return (int)((float)x / (float)n * 1.000001f) + 1; };
+    auto parts = [](int x, int n) { return (int)(((uint32_t)x + (uint32_t)n - 1) / (uint32_t)n); };
     const int even = parts(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
     r.rest = all;
+    r.share = max(least, even);
+    const bool none = count <= a.shares ? longest <= r.share + a.extra : !FEW && longest / 2 <= a.extra;
     if constexpr (FEW) {
-      r.drawn = count * 4 <= a.shares;
-      r.share = max(least, r.drawn ? parts(all, a.shares - count) : even);
-      if (r.drawn) {
+      if (none) {
+        r.longest = longest;
+        r.whole = count;
         r.rest = 0;
-        for (int s = 0; s < a.N; s += 64) {
-          load(s);
-          r.rest += wave_sum(length(0, r));
-        }
       }
-    } else {
-      r.longest = max(even + even / 4, 2 * least);
+    }
+    if (!none && count * 4 <= a.shares) {
+      r.drawn = 1;
+      r.share = max(least, parts(all, a.shares - count));
+      r.rest = 0;
+      for (int s = 0; s < a.N; s += 64) {
+        load(s);
+        r.rest += wave_sum(length(0, r));
+      }
+    } else if constexpr (!FEW) {
+      r.longest = none ? longest : even + even / 4;
       int may = 0, sure = 0;
       for (int s = 0; s < a.N; s += 64) {
         load(s);
@@ -206,8 +224,8 @@ struct Line {
         may += wave_sum(w);
         sure += wave_sum(tiles - w);
       }
-      const int rounds = (int)((float)may / (float)a.shares);      // (counts below 2^24 are exact)
-      r.whole = sure == 0 && (rounds >= 3 || r.longest == 2 * least) ? may : rounds * a.shares;
+      const int rounds = may / a.shares;
+      r.whole = none || (sure == 0 && rounds >= 3) ? may : rounds * a.shares;
       r.whole = max(min(r.whole, a.tiles), 0);     // (malformed offsets may count more tiles than there is room for)
       int before = 0;
       r.rest = 0;
@@ -232,7 +250,7 @@ struct Line {
       int kept = 0;
       if (a.shares == 0) {
         kept = tiles;
-      } else if constexpr (!FEW) {
+      } else if (!FEW || WHOLE) {     // (of few rows all are whole, or none)
         const int may = may_be_whole(sh.longest), upto = tiles_before + wave_scan(may);
         kept = min(max(sh.whole - (upto - may), 0), may);
         tiles_before = lane_value(upto, 63);
@@ -246,7 +264,7 @@ struct Line {
         if constexpr (WHOLE) {
           i = n - 1 - rest;                          // a sequence's last tiles see the most keys: first
         } else {
-          if (FEW && sh.drawn) f = drawn_tile(f, st, n, sh), st = 0;
+          if (sh.drawn) f = drawn_tile(f, st, n, sh), st = 0;
           if (cut > 1) {          // f i + st i (i - 1) / 2 <= rest, nearly by the quadratic's root, then exactly
             float x = (float)rest / (float)f;
             if (st != 0) {
@@ -273,10 +291,18 @@ struct Line {
   }
 };
 
-// What the join of a tile cut between workgroups j - 1 and j needs (pieces = 0: no tile that begins in j - 1).
+// What the join of a tile cut between workgroups j - 1 and j needs: its rows, and its pieces begin .. end - 1 (of them
+// the one numbered 0 is the end of share j - 1, k that of share j - 1 + k).  Nothing to join: end - begin < 2.
 struct Cut {
-  int b, L, tile, pieces;
+  int b, L, tile;
+  short begin, end;
 };
+
+// Borders near a tile's end lie there.
+__device__ __forceinline__ int border(int x, int length, int share) {
+  const int near = share >> 4;
+  return x < near ? 0 : (length - x < near ? length : x);
+}
 
 template <typename T> struct Op;
 template <> struct Op<__bf16> {
@@ -583,7 +609,7 @@ struct Next {
   Piece u;
   int from, to;
   Shares sh;
-  int end;
+  int pos, end, slot;    // the share's next place and its end; the piece's slot of the workspace
   Cut cut;
   int j, state;          // share; kTile, kPart, or kNone: nothing left
 };
@@ -601,7 +627,7 @@ __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
   if (!first) {
     sh.longest = k->sh.longest, sh.whole = k->sh.whole, sh.rest = k->sh.rest, sh.share = k->sh.share;
     sh.drawn = k->sh.drawn;
-    pos = k->u.at + k->to;
+    pos = k->pos;
     end = k->end;
     j = k->j;
   } else if (!tile) {
@@ -618,29 +644,41 @@ __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
     end = (int)min(at + sh.share, (int64_t)sh.rest);
   }
   Piece u{0, 0, 0, 0, 0, 0, 0};
-  int from = 0, to = 1;
-  Cut cut{0, 0, 0, 0};
-  int state = kNone;
+  int from = 0, to = 1, state = kNone, slot = 0;
+  Cut cut{0, 0, 0, 0, 0};
   if (tile) {
     if (line.template find<true>(sh, j, u)) state = kTile;
-    j = -1;
-  } else if (pos < end && line.template find<false>(sh, pos, u)) {
-    from = pos - u.at;
-    to = min(u.length, end - u.at);
-    if (to > from) state = kPart;
-    if (first && from > 0 && u.at >= pos - sh.share) {
-      const int last = u.at + u.length;
-      int n = max((int)((float)last / (float)sh.share), j);      // the share that ends the tile
-      while (n > j && (int64_t)n * sh.share >= last) --n;
-      while ((int64_t)(n + 1) * sh.share < last) ++n;
-      cut = Cut{u.b, u.L, u.tile, n - j + 2};
+    // of few rows there are no workgroups behind the shares: the cuts of the last ones, none, are written here
+    j = FEW && a.shares ? a.shares - sh.whole + j : -1;
+  } else {
+    while (pos < end && line.template find<false>(sh, pos, u)) {
+      from = pos - u.at;
+      to = min(u.length, end - u.at);
+      slot = 2 * j + (from == 0);
+      if (first && from > 0 && u.at >= pos - sh.share) {
+        const int last = u.at + u.length;
+        int n = max((int)((float)last / (float)sh.share), j);      // the share that ends the tile
+        while (n > j && (int64_t)n * sh.share >= last) --n;
+        while ((int64_t)(n + 1) * sh.share < last) ++n;
+        const int begin = border(from, u.length, sh.share) == 0;
+        const int over = border((int)((int64_t)n * sh.share - u.at), u.length, sh.share) == u.length;
+        cut = Cut{u.b, u.L, u.tile, (short)begin, (short)(n - j + 2 - over)};
+      }
+      first = false;
+      pos = u.at + to;
+      from = border(from, u.length, sh.share);
+      to = border(to, u.length, sh.share);
+      if (to > from) {
+        state = kPart;
+        break;
+      }
     }
   }
   k->u.s = u.s, k->u.b = u.b, k->u.L = u.L, k->u.lens = u.lens, k->u.tile = u.tile;
-  k->u.at = u.at, k->u.length = u.length, k->from = from, k->to = to, k->end = end;
+  k->u.length = u.length, k->from = from, k->to = to, k->pos = pos, k->end = end, k->slot = slot;
   k->sh.longest = sh.longest, k->sh.whole = sh.whole, k->sh.rest = sh.rest, k->sh.share = sh.share;
   k->sh.drawn = sh.drawn;
-  k->cut.b = cut.b, k->cut.L = cut.L, k->cut.tile = cut.tile, k->cut.pieces = cut.pieces;
+  k->cut.b = cut.b, k->cut.L = cut.L, k->cut.tile = cut.tile, k->cut.begin = cut.begin, k->cut.end = cut.end;
   k->j = j, k->state = state;
 }
 
@@ -652,16 +690,15 @@ __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j
   __shared__ Next next[4];
   Next& k = next[threadIdx.x >> 6];
   const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares,
-                  a.unit};
+                  a.unit, a.extra};
   for (bool first = true;; first = false) {
     plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
     const int state = scalar(k.state), share = scalar(k.j);
     if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)share * a.c.Hkv + head] = k.cut;
     if (state == kNone) return;
-    const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), scalar(k.u.at),
-                  scalar(k.u.length)};
+    const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), 0, scalar(k.u.length)};
     const int from = scalar(k.from), to = scalar(k.to);
-    body(u, from, to, state == kTile || (from == 0 && to == u.length), 2 * share + (from == 0));
+    body(u, from, to, state == kTile || (from == 0 && to == u.length), scalar(k.slot));
     if (state == kTile) return;
   }
 }
@@ -894,12 +931,12 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
   __shared__ float2 ml[kJoinThreads];
   __shared__ float4 sums[kJoinThreads];
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  if (cut.pieces < 2 || cut.pieces > a.shares) return;
+  if (cut.end - cut.begin < 2 || cut.end > a.shares + 1) return;
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), j = (int)(blockIdx.x / a.c.Hkv);
   const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
   const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
   if (items <= 0) return;
-  const int groups = max(1, min(kJoinThreads / items, (cut.pieces + AT_ONCE - 1) / AT_ONCE)), group = threadIdx.x / items;
+  const int groups = max(1, min(kJoinThreads / items, (cut.end - cut.begin + AT_ONCE - 1) / AT_ONCE)), group = threadIdx.x / items;
   for (int base = 0; base < items; base += kJoinThreads) {      // more than once only with one group
     const int item = base + (groups > 1 ? (int)threadIdx.x - group * items : (int)threadIdx.x);
     const bool on = groups > 1 ? group < groups : item < items;
@@ -907,12 +944,11 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
     float m = -INFINITY, l = 0.f;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (on) {
-      // piece k: the end of share j - 1, then the beginnings of the next ones
       auto at = [&](int k) {
         return ((int64_t)(k == 0 ? 2 * (j - 1) + 1 : 2 * (j - 1 + k)) * a.c.Hkv + head) * ROWS + n;
       };
-      const int first = groups > 1 ? group : 0;
-      for (int k0 = first; k0 < cut.pieces; k0 += AT_ONCE * groups) {
+      const int first = cut.begin + (groups > 1 ? group : 0);
+      for (int k0 = first; k0 < cut.end; k0 += AT_ONCE * groups) {
         float2 x[AT_ONCE];
         float4 p[AT_ONCE];
         float top = m;
@@ -921,7 +957,7 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
           const int k = k0 + i * groups;
           x[i] = make_float2(-INFINITY, 0.f);
           p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k < cut.pieces) {
+          if (k < cut.end) {
             x[i] = *reinterpret_cast<const float2*>(a.part_ml + at(k) * 2);
             p[i] = *reinterpret_cast<const float4*>(a.part_o + at(k) * D + col);
           }

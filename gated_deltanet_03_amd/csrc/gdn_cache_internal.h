@@ -45,6 +45,7 @@ struct AttendArgs {
   int32_t shares;        // even shares of a head's work, 0: a tile for each workgroup
   int32_t tiles;         // upper bound on a head's tiles
   int32_t unit;          // log2 of the keys of a unit of work
+  int32_t extra;         // what cutting tiles costs, in units of work
   float* part_o;         // [2 shares, Hkv, rows of a tile, d]
   float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
   void* cuts;            // [shares, Hkv] of 16 bytes
@@ -81,7 +82,7 @@ struct ReorderArgs {
 // many rows, and by the
 // bytes of one key (rb) the keys of a tile, waves of a workgroup, LDS and waves a SIMD (one workgroup each).
 constexpr int32_t kFewRows = 32, kManyRows = 128;
-constexpr int32_t kFewKeys = 256, kManyKeys = 256, kMostShares = 1024;
+constexpr int32_t kFewKeys = 128, kManyKeys = 128, kMostShares = 1024;
 constexpr int many_keys(int rb) { return rb >= 1024 ? 32 : 64; }
 constexpr int many_lds(int rb) { return 4 * many_keys(rb) * rb; }
 constexpr int many_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : rb >= 128 ? 3 : 4; }
