@@ -20,6 +20,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_cache_device.h"
 #include "gdn_rows.h"
@@ -63,7 +64,7 @@ __device__ __forceinline__ float other_half_sum(float x) {
 // Keys: 16-byte reads of one piece in 32 rows; 8 rows on each other's heels meet distinct eighths of 128 bytes, 16 rows
 // distinct sixteenths of 256.
 template <int PPR>
-__device__ __forceinline__ int key_swizzle(int r) {
+__device__ __forceinline__ constexpr int key_swizzle(int r) {
   if constexpr (PPR >= 16) return r & 15;
   else if constexpr (PPR == 8) return ((r >> 1) & 3) | (((r ^ (r >> 3)) & 1) << 2);
   else return (r >> 1) & 3;
@@ -71,7 +72,7 @@ __device__ __forceinline__ int key_swizzle(int r) {
 // Values, 16-bit: transposed reads of 4 rows x 32 bytes by 16 lanes, x 64 bytes by 32.
 // Values, fp32: 4-byte reads of 128 bytes of rows r and r + 4.
 template <int ES, int PPR>
-__device__ __forceinline__ int value_swizzle(int r) {
+__device__ __forceinline__ constexpr int value_swizzle(int r) {
   if constexpr (ES == 4) return PPR >= 16 ? ((r >> 2) & 1) << 3 : 0;
   else if constexpr (PPR >= 16) return (0xca60 >> ((r & 3) << 2)) & 15;   // 0, 6, 10, 12
   else if constexpr (PPR == 8) return (r & 3) << 1;
@@ -348,24 +349,32 @@ struct Wave {
     for (int s = 0; s < QN; ++s) q[s] = *reinterpret_cast<const uint4*>(src + (2 * s + h) * E);
   }
 
-  // Scores of 32 keys, rows r0 .. r0 + 31 of the LDS tile.
-  __device__ __forceinline__ f32x16 scores(const unsigned char* K, int r0) const {
+  // Piece t of 32 keys' operand: rows r0 .. r0 + 31 of the LDS tile; and its products, added to their scores.
+  __device__ __forceinline__ uint4 key_piece(const unsigned char* K, int r0, int t) const {
     const int h = lane >> 5, r = lane & 31;
-    const int f = key_swizzle<PPR>(r);
+    return *reinterpret_cast<const uint4*>(K + (r0 + r) * RB + (((2 * t + h) ^ key_swizzle<PPR>(r)) << 4));
+  }
+  __device__ __forceinline__ void add_product(f32x16& s, const uint4& k, int t) const {
+    if constexpr (F32) {
+      const f32x4 a = __builtin_bit_cast(f32x4, k), b = __builtin_bit_cast(f32x4, q[t]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], s, 0, 0, 0);
+    } else {
+      s = Op<T>::mma(__builtin_bit_cast(typename Op<T>::V, k), __builtin_bit_cast(typename Op<T>::V, q[t]), s);
+    }
+  }
+  static __device__ __forceinline__ f32x16 zeros() {
     f32x16 s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
+    return s;
+  }
+
+  // Scores of 32 keys.
+  __device__ __forceinline__ f32x16 scores(const unsigned char* K, int r0) const {
+    f32x16 s = zeros();
 #pragma unroll
-    for (int t = 0; t < QN; ++t) {
-      const uint4 k = *reinterpret_cast<const uint4*>(K + (r0 + r) * RB + (((2 * t + h) ^ f) << 4));
-      if constexpr (F32) {
-        const f32x4 a = __builtin_bit_cast(f32x4, k), b = __builtin_bit_cast(f32x4, q[t]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], s, 0, 0, 0);
-      } else {
-        s = Op<T>::mma(__builtin_bit_cast(typename Op<T>::V, k), __builtin_bit_cast(typename Op<T>::V, q[t]), s);
-      }
-    }
+    for (int t = 0; t < QN; ++t) add_product(s, key_piece(K, r0, t), t);
     return s;
   }
 
@@ -396,15 +405,59 @@ struct Wave {
       for (int i = 0; i < 16; ++i) o[t][i] *= f;
   }
 
-  // Scores to weights.
-  __device__ __forceinline__ void weigh(f32x16& s, float c) {
-    float part = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
-      part += s[i];
+  // Weights of 32 keys as operands: fp32, or rounded to T.
+  struct Weights {
+    uint4 u[F32 ? 4 : 2];
+    __device__ __forceinline__ float at(int i) const {
+      if constexpr (F32) return __builtin_bit_cast(f32x4, u[i >> 2])[i & 3];
+      else return Elem<T>::to_f(__builtin_bit_cast(typename Op<T>::V, u[i >> 3])[i & 7]);
     }
-    l += part;
+    // Weights i, i + 1 are made here: the compiler would else move them behind the branches that follow.
+    __device__ __forceinline__ void pin(int i) {
+      uint32_t* x = &u[0].x;
+      if constexpr (F32) asm volatile("" : "+v"(x[i]), "+v"(x[i + 1]));
+      else asm volatile("" : "+v"(x[i >> 1]));
+    }
+  };
+  // Two scores to weights.
+  __device__ __forceinline__ void weigh_two(Weights& w, const f32x16& s, int i, float c) const {
+    const float a = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc)), b = __builtin_amdgcn_exp2f(fmaf(s[i + 1], c, -mc));
+    uint32_t* u = &w.u[0].x;
+    if constexpr (F32) {
+      u[i] = __float_as_uint(a);
+      u[i + 1] = __float_as_uint(b);
+    } else {
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      typedef T two __attribute__((ext_vector_type(2)));
+      u[i >> 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, two));
+    }
+  }
+  __device__ __forceinline__ Weights weigh(const f32x16& s, float c) const {
+    Weights w;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) weigh_two(w, s, i, c);
+    return w;
+  }
+  // Adds weights i, i + 1 to x, as they enter the product: what rounding does to a weight acts above and below the line.
+  // For 16-bit types in one instruction, which may cut bits off: sums of 32 keys are made apart and then added to l.
+  static __device__ __forceinline__ float add_two(float x, const Weights& w, int i) {
+    const uint32_t* u = &w.u[0].x;
+    if constexpr (F32) {
+      return x + __uint_as_float(u[i]) + __uint_as_float(u[i + 1]);
+    } else {
+      typedef T two __attribute__((ext_vector_type(2)));
+      const two ones = {(T)1.f, (T)1.f};
+      if constexpr (__is_same(T, __bf16))
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(two, u[i >> 1]), ones, x, false);
+      else
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(two, u[i >> 1]), ones, x, false);
+    }
+  }
+  static __device__ __forceinline__ float sum(const Weights& w) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) x = add_two(x, w, i);
+    return x;
   }
 
   // V's operand for 16 keys (rows r0 .. r0 + 15) and 32 columns, in the weights' order.
@@ -423,31 +476,23 @@ struct Wave {
                                            ((col & 3) << 2));
   }
 
-  // The weights of the lane's keys 8 s .. 8 s + 7, rounded to T.
-  static __device__ __forceinline__ uint4 weight_operand(const f32x16& p, int s) {
-    typedef float f32x8 __attribute__((ext_vector_type(8)));
-    const f32x8 x = {p[8 * s], p[8 * s + 1], p[8 * s + 2], p[8 * s + 3],
-                     p[8 * s + 4], p[8 * s + 5], p[8 * s + 6], p[8 * s + 7]};
-    return __builtin_bit_cast(uint4, __builtin_convertvector(x, typename Op<T>::V));
+  // o += V^T P^T over 32 keys in PARTS parts: part k = (keys, columns) of 16 x 32, or one key's 32 columns a lane.
+  static constexpr int PARTS = (F32 ? 16 : 2) * DT;
+  using Value = typename std::conditional<F32, float, uint4>::type;
+  __device__ __forceinline__ Value value_part(const unsigned char* V, int r0, int k) const {
+    if constexpr (F32) return value_at(V, r0, k % DT, k / DT);
+    else return value_operand(V, r0 + 16 * (k / DT), k % DT);
   }
-
-  // o += V^T P^T over 32 keys.
-  __device__ __forceinline__ void add_values(const unsigned char* V, int r0, const f32x16& p) {
-    if constexpr (F32) {
+  __device__ __forceinline__ void add_part(const Value& v, const Weights& p, int k) {
+    if constexpr (F32)
+      o[k % DT] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, p.at(k / DT), o[k % DT], 0, 0, 0);
+    else
+      o[k % DT] = Op<T>::mma(__builtin_bit_cast(typename Op<T>::V, v), __builtin_bit_cast(typename Op<T>::V, p.u[k / DT]),
+                             o[k % DT]);
+  }
+  __device__ __forceinline__ void add_values(const unsigned char* V, int r0, const Weights& p) {
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(value_at(V, r0, t, i), p[i], o[t], 0, 0, 0);
-    } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const auto w = __builtin_bit_cast(typename Op<T>::V, weight_operand(p, s));
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-          o[t] = Op<T>::mma(__builtin_bit_cast(typename Op<T>::V, value_operand(V, r0 + 16 * s, t)), w, o[t]);
-      }
-    }
+    for (int k = 0; k < PARTS; ++k) add_part(value_part(V, r0, k), p, k);
   }
 
   // Which of 32 rows of values hold an infinity or NaN.
@@ -477,7 +522,7 @@ struct Wave {
 
   // Rows of values with infinities or NaN, in a tile of which a query may see a part: a weight of 0 would not keep them
   // out of the product.  They are added key by key to the queries that see them; clear_rows() then takes them out.
-  __device__ __forceinline__ void add_rows(const unsigned char* V, int r0, const f32x16& p, uint32_t bad, int key0,
+  __device__ __forceinline__ void add_rows(const unsigned char* V, int r0, const Weights& p, uint32_t bad, int key0,
                                            int gone) {
     const int h = lane >> 5;
     for (uint32_t left = bad; left != 0; left &= left - 1) {
@@ -485,7 +530,7 @@ struct Wave {
       float w = 0.f;      // its weight, in the lanes of half (k / 4) % 2
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i == (k >> 3) * 4 + (k & 3)) w = p[i];
+        if (i == (k >> 3) * 4 + (k & 3)) w = p.at(i);
       w = __shfl(w, (lane & 31) + 32 * ((k >> 2) & 1));
       const bool sees = key >= lo && key <= hi && !((gone >> (k >> 4)) & 1);
       const int r = r0 + k;
@@ -531,36 +576,51 @@ __device__ __forceinline__ void load_pages(const A& a, const int32_t* __restrict
   p.none = __ballot(row < 0);
 }
 
-// Copies NR rows of keys (or values) from key `key` on (a multiple of NR, inside of one granule or NR a multiple of
-// 16) to LDS; rows outside of [beg, end) and without a page as zeros.
+// Copies NR rows of keys (or values) from key `key` on to LDS, rows outside of [beg, end) and without a page as zeros.
+// Either NR and key are multiples of 16, or all NR rows from key on lie in one granule, at the same rows of it each time.
+//
+// An instruction copies 1024 bytes of LDS in order, so which piece of which row a lane fetches is a matter of its own
+// address.  The swizzles are linear over exclusive or: instruction n's place is the first one's, with a constant.
 template <int ES, int D, int NR, bool VALUES>
-__device__ __forceinline__ void stage_rows(const void* cache, const Pages& pg, int key, int beg, int end, int lane, uint32_t lds) {
-  constexpr int RB = D * ES, PPR = RB / 16, RPI = 64 / PPR > 0 ? 64 / PPR : 1;   // rows an instruction
-  static_assert(PPR <= 64, "a row is at most one instruction");
-  constexpr int GR = NR < 16 ? NR : 16;      // rows of one granule
+struct Stage {
+  static constexpr int RB = D * ES, PPR = RB / 16, RPI = 64 / PPR;     // rows an instruction
+  static constexpr int GR = NR < 16 ? NR : 16;                         // rows of one granule
+  static_assert(PPR <= 64 && GR % RPI == 0, "a row is at most one instruction, a granule whole ones");
+  int lane;
+  uint32_t place;          // of the lane's piece in instruction 0, from the first row on
+
+  static __device__ __forceinline__ constexpr int swizzle(int r) {
+    return VALUES ? value_swizzle<ES, PPR>(r) : key_swizzle<PPR>(r);
+  }
+  // sub: the first row's number in its granule
+  __device__ __forceinline__ Stage(int lane_, int sub) : lane(lane_) {
+    const int r = lane / PPR;
+    place = (uint32_t)(r * RB + (((lane % PPR) ^ swizzle(r) ^ swizzle(sub)) << 4));
+  }
+  __device__ __forceinline__ void operator()(const void* cache, const Pages& pg, int key, int beg, int end,
+                                             uint32_t lds) const {
 #pragma unroll
-  for (int g = 0; g < NR / GR; ++g) {
-    const int at = key + g * 16;
-    const int row = __builtin_amdgcn_readlane(pg.row, ((at >> 4) - pg.first) & 63);
-    const bool whole = row >= 0 && at >= beg && at + GR <= end;
-    const char* base = static_cast<const char*>(cache) + ((int64_t)row + (at & 15)) * RB;
+    for (int g = 0; g < NR / GR; ++g) {
+      const int at = key + g * 16;
+      const int row = __builtin_amdgcn_readlane(pg.row, ((at >> 4) - pg.first) & 63) + (GR < 16 ? at & 15 : 0);
+      const char* base = static_cast<const char*>(cache) + (int64_t)row * RB;
+      const uint32_t to = lds + (uint32_t)(g * 16 * RB);
+      if (row >= 0 && at >= beg && at + GR <= end) {
 #pragma unroll
-    for (int n = 0; n < GR / RPI; ++n) {
-      const int r = n * RPI + lane / PPR;          // row of the granule's part
-      const int tr = (at & 15) + r + 16 * g;       // (swizzles go by the row's number modulo 16)
-      const int piece = (lane % PPR) ^ (VALUES ? value_swizzle<ES, PPR>(tr) : key_swizzle<PPR>(tr));
-      const uint32_t off = (uint32_t)(r * RB + piece * 16);
-      const uint32_t to = lds + (uint32_t)((g * 16 + n * RPI) * RB);
-      if (whole) {
-        dma16(off, base, to);
+        for (int n = 0; n < GR / RPI; ++n)
+          dma16((place ^ (uint32_t)(swizzle(n * RPI) << 4)) + n * 1024, base, to + n * 1024);
       } else {
-        const bool in = row >= 0 && at + r >= beg && at + r < end;
-        dma16(in ? static_cast<const void*>(base + off) : static_cast<const void*>(zeros16), to);
+#pragma unroll
+        for (int n = 0; n < GR / RPI; ++n) {
+          const int k = at + n * RPI + lane / PPR;
+          const char* src = base + (place ^ (uint32_t)(swizzle(n * RPI) << 4)) + n * 1024;
+          dma16(row >= 0 && k >= beg && k < end ? static_cast<const void*>(src) : static_cast<const void*>(zeros16),
+                to + n * 1024);
+        }
       }
     }
   }
-}
-
+};
 
 // A tile's rows and keys.
 template <int ROWS>
@@ -710,11 +770,19 @@ __device__ __forceinline__ void part_blocks(int n, const Piece& u, int from, int
   e = to == u.length ? n : scalar(min((int)((float)to * blocks), n));
 }
 
-// Many rows: four waves of 32 rows, the same keys.  Tiles of KT keys are double buffered; a tile's loads are issued one
-// tile ahead, and the one barrier a tile also says that nobody reads the other buffer any more.
+// Many rows: four waves of 32 rows, the same keys, in blocks of KT of them.  Keys and values have two buffers each; a
+// block's loads are issued one block ahead.  The one barrier a block says that its loads have landed and that nobody
+// reads the buffers that the next ones go to.
+//
+// Where the registers leave one wave a SIMD (D = 256, fp32 from D = 128 on), nothing fills the matrix unit while that wave
+// makes weights: keys are loaded two blocks ahead and multiplied one block ahead, in turn with the exponentials of the
+// block before (2048 new tokens over 16384 keys, 16 heads of 256, bf16: 780 -> 596 us).  With two waves or more the
+// other wave does that, and the plain order needs fewer registers (D = 128: 542 us plain, 552 in turn).  There, waves
+// that multiply go first (542 -> 522 us).
 template <typename T, int D>
 struct ManyShape {
   static constexpr int RB = D * (int)sizeof(T), KT = many_keys(RB), NS = KT / 32;
+  static constexpr bool ALONE = many_waves(RB) == 1;     // one wave a SIMD
 };
 
 template <typename T, int D>
@@ -737,56 +805,186 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
     int tb, te;
     part_blocks(t.end > t.beg ? (t.end - key_first + KT - 1) / KT : 0, u, from, to, tb, te);
     const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
-    Pages pg;
-    pg.first = -0x40000000;
-    auto stage = [&](int i, int buf) {
+    const Stage<ES, D, NR, false> stage_k(lane, wave * NR & 15);
+    const Stage<ES, D, NR, true> stage_v(lane, wave * NR & 15);
+    // keys run one block ahead of values (ALONE): a page window each
+    Pages kp, vp;
+    kp.first = vp.first = -0x40000000;
+    auto stage_keys = [&](int i) {
       const int key = key_first + i * KT;
-      if ((key >> 4) - pg.first >= 64) load_pages(a, table, head, key >> 4, lane, pg);
-      const uint32_t at = lds + (uint32_t)(buf * 2 * KT * RB + wave * NR * RB);
-      stage_rows<ES, D, NR, false>(a.k_cache, pg, key + wave * NR, t.beg, t.end, lane, at);
-      stage_rows<ES, D, NR, true>(a.v_cache, pg, key + wave * NR, t.beg, t.end, lane, at + KT * RB);
-      return (int)((pg.none >> ((key >> 4) - pg.first)) & ((1 << (KT / 16)) - 1));
+      if ((key >> 4) - kp.first >= 64) load_pages(a, table, head, key >> 4, lane, kp);
+      stage_k(a.k_cache, kp, key + wave * NR, t.beg, t.end, lds + (uint32_t)((i & 1) * KT * RB + wave * NR * RB));
+      return (int)((kp.none >> ((key >> 4) - kp.first)) & ((1 << (KT / 16)) - 1));
     };
-    lds_barrier();                                 // nobody reads the last piece's tiles any more
-    int gone = 0;
-    if (tb < te) gone = stage(tb, 0);
-    for (int i = tb; i < te; ++i) {
-      const int buf = (i - tb) & 1, key = key_first + i * KT, absent = gone;
-      wait_loads<0>();
-      lds_barrier();
-      if (i + 1 < te) gone = stage(i + 1, buf ^ 1);
-      unsigned char* K = smem + buf * 2 * KT * RB;
-      unsigned char* V = K + KT * RB;
-      f32x16 s[S::NS];
+    auto stage_values = [&](int i) {
+      const int key = key_first + i * KT;
+      if ((key >> 4) - vp.first >= 64) load_pages(a, table, head, key >> 4, lane, vp);
+      stage_v(a.v_cache, vp, key + wave * NR, t.beg, t.end, lds + (uint32_t)((2 + (i & 1)) * KT * RB + wave * NR * RB));
+    };
+    // whether some row of the tile does not see some of block i's keys
+    auto partly = [&](int i, int absent) {
+      const int key = key_first + i * KT;
+      return key + KT - 1 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
+    };
+    f32x16 s[S::NS];
+    auto mask = [&](int i, int absent) {
 #pragma unroll
-      for (int n = 0; n < S::NS; ++n) s[n] = w.scores(K, 32 * n);
-      const bool part = key + KT - 1 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
-      if (part) {
+      for (int n = 0; n < S::NS; ++n) w.mask(s[n], key_first + i * KT + 32 * n, absent >> (2 * n));
+    };
+    lds_barrier();                                 // nobody reads the last piece's blocks any more
+    auto clean = [&](int i, int absent, typename Wave<T, D>::Weights (&p)[S::NS]) {
+      unsigned char* V = smem + (2 + (i & 1)) * KT * RB;
 #pragma unroll
-        for (int n = 0; n < S::NS; ++n) w.mask(s[n], key + 32 * n, absent >> (2 * n));
+      for (int n = 0; n < S::NS; ++n) {
+        const uint32_t bad = w.not_finite(V, 32 * n);          // the same for all four waves
+        if (__builtin_expect(bad != 0, 0)) {
+          w.add_rows(V, 32 * n, p[n], bad, key_first + i * KT + 32 * n, absent >> (2 * n));
+          lds_barrier();
+          w.clear_rows(V, 32 * n, bad);                        // all waves write the same zeros
+          lds_barrier();
+        }
       }
+    };
+    auto highest = [&] {
       float top = -INFINITY;
 #pragma unroll
       for (int n = 0; n < S::NS; ++n)
 #pragma unroll
         for (int j = 0; j < 16; ++j) top = fmaxf(top, s[n][j]);
-      w.raise(top, c, slack);
+      return top;
+    };
+    if constexpr (!S::ALONE) {
+      int ahead = 0;                               // keys without a page in the next block
+      if (tb < te) {
+        ahead = stage_keys(tb);
+        stage_values(tb);
+      }
+      for (int i = tb; i < te; ++i) {
+        const int absent = ahead;
+        wait_loads<0>();
+        lds_barrier();
+        if (i + 1 < te) {
+          ahead = stage_keys(i + 1);
+          stage_values(i + 1);
+        }
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int n = 0; n < S::NS; ++n) w.weigh(s[n], c);
-      if (part) {
+        for (int n = 0; n < S::NS; ++n) s[n] = w.scores(smem + (i & 1) * KT * RB, 32 * n);
+        __builtin_amdgcn_s_setprio(0);
+        const bool part = partly(i, absent);
+        if (part) mask(i, absent);
+        w.raise(highest(), c, slack);
+        typename Wave<T, D>::Weights p[S::NS];
 #pragma unroll
         for (int n = 0; n < S::NS; ++n) {
-          const uint32_t bad = w.not_finite(V, 32 * n);          // the same for all four waves
-          if (__builtin_expect(bad != 0, 0)) {
-            w.add_rows(V, 32 * n, s[n], bad, key + 32 * n, absent >> (2 * n));
-            lds_barrier();
-            w.clear_rows(V, 32 * n, bad);                        // all waves write the same zeros
-            lds_barrier();
+          p[n] = w.weigh(s[n], c);
+          w.l += Wave<T, D>::sum(p[n]);
+        }
+        if (part) clean(i, absent, p);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int n = 0; n < S::NS; ++n) w.add_values(smem + (2 + (i & 1)) * KT * RB, 32 * n, p[n]);
+        __builtin_amdgcn_s_setprio(0);
+      }
+    } else {
+      int absent = 0, ahead = 0;                     // keys without a page in blocks i, i + 1
+      if (tb < te) {
+        absent = stage_keys(tb);
+        stage_values(tb);
+        if (tb + 1 < te) ahead = stage_keys(tb + 1);
+        wait_loads<0>();
+        lds_barrier();
+#pragma unroll
+        for (int n = 0; n < S::NS; ++n) s[n] = w.scores(smem + (tb & 1) * KT * RB, 32 * n);
+        if (partly(tb, absent)) mask(tb, absent);
+      }
+      float top = highest();
+      // Block i: its scores are there.  The next block's are computed beside its weights, and their maximum beside its
+      // products with the values, a product and a few vector operations in turn: the compiler left to itself puts all
+      // products before all exponentials, and neither unit works while the other does.
+      auto step = [&](int i, auto more) {
+        using W = Wave<T, D>;
+        constexpr int AHEAD = 3;                     // LDS reads in flight
+        unsigned char* V = smem + (2 + (i & 1)) * KT * RB;
+        const unsigned char* K = smem + ((i + 1) & 1) * KT * RB;
+        w.raise(top, c, slack);
+        f32x16 x[S::NS];
+        typename W::Weights p[S::NS];
+        if constexpr (more.value) {
+          constexpr int N = S::NS * W::QN, PAIRS = 8 * S::NS;
+          uint4 k[AHEAD + 1];
+#pragma unroll
+          for (int n = 0; n < S::NS; ++n) x[n] = W::zeros();
+#pragma unroll
+          for (int t = 0; t < AHEAD; ++t) k[t] = w.key_piece(K, 32 * (t / W::QN), t % W::QN);
+#pragma unroll
+          for (int t = 0; t < N; ++t) {
+            if (t + AHEAD < N)
+              k[(t + AHEAD) % (AHEAD + 1)] = w.key_piece(K, 32 * ((t + AHEAD) / W::QN), (t + AHEAD) % W::QN);
+            w.add_product(x[t / W::QN], k[t % (AHEAD + 1)], t % W::QN);
+#pragma unroll
+            for (int e = t * PAIRS / N; e < (t + 1) * PAIRS / N; ++e) {
+              w.weigh_two(p[e / 8], s[e / 8], e % 8 * 2, c);
+              p[e / 8].pin(e % 8 * 2);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
+        } else {
+#pragma unroll
+          for (int n = 0; n < S::NS; ++n) p[n] = w.weigh(s[n], c);
+        }
+        if (partly(i, absent)) clean(i, absent, p);
+        constexpr int N = S::NS * W::PARTS, PAIRS = 8 * S::NS;
+        typename W::Value v[AHEAD + 1];
+        float part[S::NS], high = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < S::NS; ++n) part[n] = 0.f;
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) v[t] = w.value_part(V, 32 * (t / W::PARTS), t % W::PARTS);
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+          if (t + AHEAD < N)
+            v[(t + AHEAD) % (AHEAD + 1)] = w.value_part(V, 32 * ((t + AHEAD) / W::PARTS), (t + AHEAD) % W::PARTS);
+          w.add_part(v[t % (AHEAD + 1)], p[t / W::PARTS], t % W::PARTS);
+#pragma unroll
+          for (int e = t * PAIRS / N; e < (t + 1) * PAIRS / N; ++e) {
+            part[e / 8] = W::add_two(part[e / 8], p[e / 8], e % 8 * 2);
+            if constexpr (more.value) high = fmaxf(fmaxf(high, x[e / 8][e % 8 * 2]), x[e / 8][e % 8 * 2 + 1]);
+            asm volatile("" : "+v"(part[e / 8]), "+v"(high));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int n = 0; n < S::NS; ++n) w.l += part[n];
+        if constexpr (more.value) {
+#pragma unroll
+          for (int n = 0; n < S::NS; ++n) s[n] = x[n];
+          top = high;
+        }
+      };
+      for (int i = tb; i + 1 < te; ++i) {
+        if (i > tb) {
+          wait_loads<0>();
+          lds_barrier();
+        }
+        int then = 0;
+        if (i + 2 < te) then = stage_keys(i + 2);
+        stage_values(i + 1);
+        step(i, std::true_type{});
+        absent = ahead;
+        ahead = then;
+        if (partly(i + 1, absent)) {
+          mask(i + 1, absent);
+          top = highest();
         }
       }
-#pragma unroll
-      for (int n = 0; n < S::NS; ++n) w.add_values(V, 32 * n, s[n]);
+      if (tb < te) {
+        if (tb + 1 < te) {
+          wait_loads<0>();
+          lds_barrier();
+        }
+        step(te - 1, std::false_type{});
+      }
     }
     const float l = other_half_sum(w.l);
     if (t.row0 + mine >= t.R) return;
@@ -833,6 +1031,8 @@ void cache_attention_few_kernel(AttendArgs a) {
     int tb, te;
     part_blocks(t.end > t.beg ? (t.end - key_first + 31) / 32 : 0, u, from, to, tb, te);
     const int32_t* table = a.c.table + (int64_t)u.s * a.c.max_pages;
+    const Stage<ES, D, 32, false> stage_k(lane, 0);
+    const Stage<ES, D, 32, true> stage_v(lane, 0);
     Pages pg;
     pg.first = -0x40000000;
     auto pages_for = [&](int i) {
@@ -843,8 +1043,8 @@ void cache_attention_few_kernel(AttendArgs a) {
     int i = tb + wave, gone = 0;
     if (i < te) {
       gone = pages_for(i);
-      stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, lane, ldsK);
-      stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, lane, ldsK + 32 * RB);
+      stage_k(a.k_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK);
+      stage_v(a.v_cache, pg, key_first + 32 * i, t.beg, t.end, ldsK + 32 * RB);
     }
     set_row(a, G, head, t, lane & 31, w);
     for (; i < te; i += NW) {
@@ -854,7 +1054,7 @@ void cache_attention_few_kernel(AttendArgs a) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (next < te) {
         gone = pages_for(next);
-        stage_rows<ES, D, 32, false>(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, lane, ldsK);
+        stage_k(a.k_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK);
       }
       const bool part = key + 31 > min(t.pmin, t.room - 1) || (a.window > 0 && key < t.pmax - a.window + 1) || absent;
       if (part) w.mask(s, key, absent);
@@ -862,20 +1062,21 @@ void cache_attention_few_kernel(AttendArgs a) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
       w.raise(top, c, slack);
-      w.weigh(s, c);
+      const auto p = w.weigh(s, c);
+      w.l += Wave<T, D>::sum(p);
       if (next < te) wait_loads<NI>();               // the values: the next keys were issued after them
       else wait_loads<0>();
       if (part) {
         const uint32_t bad = w.not_finite(V, 0);
         if (__builtin_expect(bad != 0, 0)) {
-          w.add_rows(V, 0, s, bad, key, absent);
+          w.add_rows(V, 0, p, bad, key, absent);
           w.clear_rows(V, 0, bad);
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
       }
-      w.add_values(V, 0, s);
+      w.add_values(V, 0, p);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (next < te) stage_rows<ES, D, 32, true>(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, lane, ldsK + 32 * RB);
+      if (next < te) stage_v(a.v_cache, pg, key_first + 32 * next, t.beg, t.end, ldsK + 32 * RB);
     }
     // join the waves: everyone's accumulators in LDS (pieces of 16 bytes at piece ^ row % 8)
     const float l = other_half_sum(w.l);

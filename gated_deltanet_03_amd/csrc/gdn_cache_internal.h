@@ -85,7 +85,7 @@ constexpr int32_t kFewRows = 32, kManyRows = 128;
 constexpr int32_t kFewKeys = 128, kManyKeys = 128, kMostShares = 1024;
 constexpr int many_keys(int rb) { return rb >= 1024 ? 32 : 64; }
 constexpr int many_lds(int rb) { return 4 * many_keys(rb) * rb; }
-constexpr int many_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : rb >= 128 ? 3 : 4; }
+constexpr int many_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : 3; }
 constexpr int few_group(int rb) { return rb >= 1024 ? 2 : 4; }
 constexpr int few_lds(int rb) { return few_group(rb) * 64 * rb; }
 constexpr int few_waves(int rb) { return rb >= 512 ? 1 : rb >= 256 ? 2 : rb >= 128 ? 3 : 4; }
