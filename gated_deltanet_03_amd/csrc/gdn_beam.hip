@@ -7,13 +7,13 @@
 // that is the order of the logits, whatever the sum turns out to be.  beam_join_kernel: a workgroup for each search
 // joins the segments' sums and selects among the K * segments * W entries that are left.
 //
-// Selection: the K-th largest of a wave's 64 lane maxima, found by bisection over the bits with ballots, is a bound
-// that at least K entries reach; the entries that reach the highest wave's bound go to a list in LDS, and an
+// Selection: the K-th largest of a wave's 64 lane maxima, found by bisection over their upper bits with ballots, is a
+// bound that at least K entries reach; the entries that reach the highest wave's bound go to a list in LDS, and an
 // entry's rank is the number of entries before it.  Lists that do not fit (very many equal entries) are taken one
 // maximum at a time.
 //
-// Sums of exponentials: 2^(t log2 e) with the product's own rounding error added back, so that what is left is the
-// rounding of v_exp_f32, which averages out over a row; terms are added in 64 bits.
+// Sums of exponentials: the difference to the maximum first, so that the exponent's rounding is small where terms are
+// large; eight terms a thread in fp32, those in 64 bits.
 #include <algorithm>
 
 #include "gdn_cache_internal.h"
@@ -39,11 +39,12 @@ __device__ __forceinline__ double unordered64(uint64_t u) {
   return __builtin_bit_cast(double, u ^ (~(uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull));
 }
 
-// The k-th largest of the lanes' values (1 <= k <= 64).
+// The upper BITS bits of the k-th largest of the lanes' values (1 <= k <= 64).
+template <int BITS>
 __device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k) {
   uint32_t t = 0;
 #pragma unroll
-  for (int b = 31; b >= 0; --b) {
+  for (int b = 31; b >= 32 - BITS; --b) {
     const uint32_t at = t | (1u << b);
     if (__popcll(__ballot(v >= at)) >= k) t = at;
   }
@@ -74,31 +75,33 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
-// exp(t), t <= 0, to the rounding of v_exp_f32; 0 from -150 (2^-216) down, -infinity among it
-__device__ __forceinline__ float exp_terms(float t) {
-  t = fmaxf(t, -150.f);
-  const float hi = t * 1.44269504f;
-  const float lo = fmaf(t, 1.44269504f, -hi) + t * 1.92596299e-8f;
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return fmaf(e, 0.693147181f * lo, e);
-}
-
 // Entries of a segment as keys: the logit's order, then the lower index first.
 __device__ __forceinline__ uint64_t entry_key(float x, int v) { return (uint64_t)ordered(x) << 32 | (uint32_t)~v; }
 
+// How many of a list's n entries come before one: larger keys, or equal ones with the larger place.
+template <bool PLACES>
+__device__ __forceinline__ int rank_of(const uint64_t* list, const uint32_t* from, int n, uint64_t k, uint32_t f) {
+  int rank = 0, o = 0;
+  for (; o + 8 <= n; o += 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += list[o + i] > k || (PLACES && list[o + i] == k && from[o + i] > f);
+  }
+  for (; o < n; ++o) rank += list[o] > k || (PLACES && list[o] == k && from[o] > f);
+  return rank;
+}
+
 // NV 16-byte vectors a thread: NV * 256 * (16 / sizeof(T)) entries a segment.
 template <typename T, int NV>
-__global__ __launch_bounds__(kThreads) void beam_part_kernel(SelectArgs p, int64_t row0) {
+__global__ __launch_bounds__(kThreads, 8) void beam_part_kernel(SelectArgs p, int64_t row0) {
   constexpr int E = Vec16<T>::N;
   __shared__ uint64_t list[kList];
   __shared__ uint32_t wave_top[4], wave_kth[4];
   __shared__ double wave_sum[4];
-  __shared__ int bad[4], count;
+  __shared__ int count;
   __shared__ uint64_t top_key[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = row0 + blockIdx.y;
   const int seg = blockIdx.x, v0 = seg * p.segment;
-  if (p.finished && p.finished[row]) return;      // the join reads nothing of it
   const T* x = static_cast<const T*>(p.x) + row * p.row_stride;
   Vec16<T> q[NV];
 #pragma unroll
@@ -111,82 +114,92 @@ __global__ __launch_bounds__(kThreads) void beam_part_kernel(SelectArgs p, int64
       for (int i = 0; i < E; ++i) q[j].e[i] = v + i < p.V ? x[v + i] : Elem<T>::from_f(-INFINITY);
     }
   }
+  if (p.finished && p.finished[row]) return;      // (asked for beside the entries) the join reads nothing of it
   if (tid == 0) count = 0;
-  float top = -INFINITY;
-  bool wrong = false;
+  // The entries stay packed: the compiler would keep them widened from one pass to the next, in twice the registers.
+  auto repack = [&] {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float f = q[j].f(i);
-      wrong |= !(f < INFINITY);                  // NaN or +infinity
-      top = fmaxf(top, f);
+    for (int j = 0; j < NV; ++j) {
+      uint4 u = __builtin_bit_cast(uint4, q[j]);
+      asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w));
+      q[j] = __builtin_bit_cast(Vec16<T>, u);
     }
-  }
+  };
+  float top = -INFINITY;                         // (NaN does not show here, but in the sum)
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < E; ++i) top = fmaxf(top, q[j].f(i));
+  repack();
   const uint32_t mine = ordered(top);
-  const uint32_t kth = kth_of_lanes(mine, p.K), wtop = wave_max(mine);
-  const bool wave_wrong = __ballot(wrong) != 0;
-  if (lane == 0) wave_top[wave] = wtop, wave_kth[wave] = kth, bad[wave] = wave_wrong;
+  const uint32_t kth = kth_of_lanes<16>(mine, p.K), wtop = wave_max(mine);
+  if (lane == 0) wave_top[wave] = wtop, wave_kth[wave] = kth;
   __syncthreads();
   uint32_t m = wave_top[0], bound = wave_kth[0];
-  bool any = bad[0];
 #pragma unroll
   for (int w = 1; w < 4; ++w) {
     m = wave_top[w] > m ? wave_top[w] : m;
     bound = wave_kth[w] > bound ? wave_kth[w] : bound;
-    any |= bad[w] != 0;
   }
   const int64_t at = row * p.segments + seg;
   const float most = unordered(m);
-  if (any || most == -INFINITY) {                // no entries; NaN tells the join that the beam is absent
-    if (tid < p.K) p.best[at * p.K + tid] = 0;
-    if (tid == 0) p.seg_max[at] = any ? NAN : -INFINITY, p.seg_sum[at] = 0.0;
-    return;
-  }
   const uint32_t void_key = ordered(-INFINITY);
   if (bound <= void_key) bound = void_key + 1;   // -infinity is no entry
+  const float least = unordered(bound);
   double sum = 0.0;
+  if (most == -INFINITY) {                       // differences would be NaN where entries are -infinity
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float f = q[j].f(i);
-      sum += (double)exp_terms(f - most);
-      if (ordered(f) >= bound) {
-        const int n = atomicAdd(&count, 1);
-        if (n < kList) list[n] = entry_key(f, v0 + (j * kThreads + tid) * E + i);
+      for (int i = 0; i < E; ++i)
+        if (q[j].f(i) != q[j].f(i)) sum = NAN;
+  } else {
+    uint32_t reach[(NV * E + 31) / 32] = {};     // which of the thread's entries reach the bound
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float f = q[j].f(i);
+        part += __builtin_amdgcn_exp2f((f - most) * 1.44269504f);
+        if (f >= least) reach[(j * E + i) / 32] |= 1u << (j * E + i) % 32;
       }
+      sum += (double)part;
     }
+#pragma unroll
+    for (int r = 0; r < (NV * E + 31) / 32; ++r)
+      for (uint32_t left = reach[r]; left != 0; left &= left - 1) {
+        const int k = r * 32 + __ffs(left) - 1, v = v0 + (k / E * kThreads + tid) * E + k % E;
+        const int n = atomicAdd(&count, 1);
+        if (n < kList) list[n] = entry_key(Elem<T>::to_f(x[v]), v);   // read again: registers cannot be indexed
+      }
   }
   sum = wave_sum64(sum);
   if (lane == 0) wave_sum[wave] = sum;
   __syncthreads();
-  if (tid == 0) {
-    p.seg_max[at] = most;
-    p.seg_sum[at] = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+  sum = (wave_sum[0] + wave_sum[1]) + (wave_sum[2] + wave_sum[3]);
+  const bool wrong = !(sum < INFINITY) || most == INFINITY;
+  if (tid == 0) {                                // NaN tells the join that the beam is absent
+    p.seg_max[at] = wrong ? NAN : most;
+    p.seg_sum[at] = sum;
   }
-  const int n = count;
+  const int n = wrong ? 0 : count;
   uint64_t* best = p.best + at * p.K;
   if (n <= kList) {
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t k = list[i];
-      int rank = 0;
-      for (int o = 0; o < n; ++o) rank += list[o] > k;
+      const int rank = rank_of<false>(list, nullptr, n, k, 0);
       if (rank < p.K) best[rank] = k;
     }
     if (tid >= n && tid < p.K) best[tid] = 0;
     return;
   }
-  uint64_t last = ~0ull;                         // one maximum below the last one at a time
+  uint64_t last = ~0ull;                         // one maximum below the last one at a time, read again
   for (int r = 0; r < p.K; ++r) {
     uint64_t k = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const uint64_t e = entry_key(q[j].f(i), v0 + (j * kThreads + tid) * E + i);
-        if (e < last && e > k && (uint32_t)(e >> 32) > void_key) k = e;
-      }
+    for (int v = v0 + tid; v < min(v0 + p.segment, p.V); v += kThreads) {
+      const uint64_t e = entry_key(Elem<T>::to_f(x[v]), v);
+      if (e < last && e > k && (uint32_t)(e >> 32) > void_key) k = e;
     }
     k = wave_max64(k);
     if (lane == 0) top_key[wave] = k;
@@ -200,22 +213,31 @@ __global__ __launch_bounds__(kThreads) void beam_part_kernel(SelectArgs p, int64
   }
 }
 
-// One workgroup a search.
-__global__ __launch_bounds__(kThreads) void beam_join_kernel(SelectArgs p) {
+// One workgroup a search.  A thread holds up to kHeld of the entries, loaded before the sums are joined; only searches
+// with more entries (very large vocabularies, many beams) read the others again from memory.
+constexpr int kJoin = 1024, kWaves = kJoin / 64, kHeld = 4;
+
+__global__ __launch_bounds__(kJoin) void beam_join_kernel(SelectArgs p) {
   __shared__ double start[64];                   // score minus log of the sum; NaN: absent
   __shared__ double high[64];                    // the maximum, apart: the log would drown in one of -1e38
   __shared__ uint8_t done[64];
   __shared__ uint64_t key[kList];
   __shared__ uint32_t from[kList];
-  __shared__ uint32_t wave_kth[4];
   __shared__ int count;
-  __shared__ uint64_t top_key[4];
-  __shared__ uint32_t top_from[4];
+  __shared__ uint64_t top_key[kWaves];
+  __shared__ uint32_t top_from[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t b = blockIdx.x;
   if (tid == 0) count = 0;
-  // sums: a group of lanes a beam
-  for (int w = wave; w < p.W; w += 4) {
+  // entry i: the (i % (K * segments))-th of beam i / (K * segments)
+  const int per = p.K * p.segments, all = per * p.W;
+  uint64_t held[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    const int i = tid + h * kJoin;
+    held[h] = i < all ? p.best[b * all + i] : 0;
+  }
+  for (int w = wave; w < p.W; w += kWaves) {     // sums: a wave a beam
     const int64_t row = b * p.W + w;
     const float score = p.scores[row];
     const bool fin = p.finished && p.finished[row];
@@ -246,48 +268,59 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(SelectArgs p) {
   }
   __syncthreads();
 
-  // candidate i: entry i % K of segment (i / K) % segments of beam i / (K * segments)
-  const int per = p.K * p.segments, all = per * p.W;
-  auto candidate = [&](int i, uint64_t& k, uint32_t& f) {
-    const int w = i / per, r = i - w * per;
+  // entry i as a score's order and a place: 0 if it is none
+  auto candidate = [&](int i, uint64_t e, uint64_t& k, uint32_t& f) {
+    const int w = i / per;
     k = 0;
     f = 0;
     const double s = start[w];
     if (s != s) return;
     if (done[w]) {
-      if (r != 0) return;
+      if (i != w * per) return;
       k = ordered64(s);
       f = (uint32_t)~((w << 24) | p.pad);
       return;
     }
-    const uint64_t e = p.best[(b * p.W + w) * per + r];
     if (e == 0) return;
     k = ordered64(s + ((double)unordered((uint32_t)(e >> 32)) - high[w]));
     f = (uint32_t)~((w << 24) | (int)~(uint32_t)e);   // token below 2^24, beam below 2^6: lower flat index, larger f
   };
-  uint32_t mine = 0;                             // upper halves: rounded down, so still in order
-  for (int i = tid; i < all; i += kThreads) {
+  // body(key, place) of every entry of this thread
+  uint64_t hk[kHeld];
+  uint32_t hf[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+    hk[h] = 0, hf[h] = 0;
+    if (tid + h * kJoin < all) candidate(tid + h * kJoin, held[h], hk[h], hf[h]);
+  }
+  auto each = [&](auto&& body) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) body(hk[h], hf[h]);
+    for (int i = tid + kHeld * kJoin; i < all; i += kJoin) {
+      uint64_t k;
+      uint32_t f;
+      candidate(i, p.best[b * all + i], k, f);
+      body(k, f);
+    }
+  };
+  // The lists are in order: the K-th largest of 64 maxima of their first entries, the same in every wave, is a bound
+  // that K entries reach (in fp32: rounding keeps the order).
+  auto coarse = [](uint64_t k) { return k ? ordered((float)unordered64(k)) : 0u; };
+  uint32_t mine = 0;
+  for (int l = lane; l < p.W * p.segments; l += 64) {
     uint64_t k;
     uint32_t f;
-    candidate(i, k, f);
-    const uint32_t h = (uint32_t)(k >> 32);
+    candidate(l * p.K, p.best[b * all + (int64_t)l * p.K], k, f);
+    const uint32_t h = coarse(k);
     mine = h > mine ? h : mine;
   }
-  const uint32_t kth = kth_of_lanes(mine, p.K);
-  if (lane == 0) wave_kth[wave] = kth;
-  __syncthreads();
-  uint32_t bound = wave_kth[0];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) bound = wave_kth[w] > bound ? wave_kth[w] : bound;
-  for (int i = tid; i < all; i += kThreads) {
-    uint64_t k;
-    uint32_t f;
-    candidate(i, k, f);
-    if (k != 0 && (uint32_t)(k >> 32) >= bound) {
+  const uint32_t bound = kth_of_lanes<32>(mine, p.K);
+  each([&](uint64_t k, uint32_t f) {
+    if (k != 0 && coarse(k) >= bound) {
       const int n = atomicAdd(&count, 1);
       if (n < kList) key[n] = k, from[n] = f;
     }
-  }
+  });
   __syncthreads();
   const int n = count;
   auto put = [&](int r, uint64_t k, uint32_t f) {
@@ -300,11 +333,10 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(SelectArgs p) {
     p.new_finished[o] = !k || done[w] || v == p.eos;
   };
   if (n <= kList) {
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t k = key[i];
-      const uint32_t f = from[i];
-      int rank = 0;
-      for (int o = 0; o < n; ++o) rank += key[o] > k || (key[o] == k && from[o] > f);
+    if (tid < n) {
+      const uint64_t k = key[tid];
+      const uint32_t f = from[tid];
+      const int rank = rank_of<true>(key, from, n, k, f);
       if (rank < p.K) put(rank, k, f);
     }
     if (tid >= n && tid < p.K) put(tid, 0, ~0u);
@@ -315,19 +347,16 @@ __global__ __launch_bounds__(kThreads) void beam_join_kernel(SelectArgs p) {
   for (int r = 0; r < p.K; ++r) {
     uint64_t k = 0;
     uint32_t f = 0;
-    for (int i = tid; i < all; i += kThreads) {
-      uint64_t ki;
-      uint32_t fi;
-      candidate(i, ki, fi);
+    each([&](uint64_t ki, uint32_t fi) {
       if ((ki < last || (ki == last && fi < last_f)) && (ki > k || (ki == k && fi > f))) k = ki, f = fi;
-    }
+    });
     const uint64_t wk = wave_max64(k);
     const uint32_t wf = wave_max(k == wk ? f : 0);
     if (lane == 0) top_key[wave] = wk, top_from[wave] = wf;
     __syncthreads();
     k = top_key[0], f = top_from[0];
 #pragma unroll
-    for (int w = 1; w < 4; ++w)
+    for (int w = 1; w < kWaves; ++w)
       if (top_key[w] > k || (top_key[w] == k && top_from[w] > f)) k = top_key[w], f = top_from[w];
     if (tid == 0) put(r, k, f);
     last = k, last_f = f;
@@ -350,7 +379,7 @@ static hipError_t launch_select_t(const SelectArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   prof_begin(K_SELECT_JOIN, s);
-  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(kJoin), 0, s, a);
   prof_end(K_SELECT_JOIN, s);
   return hipGetLastError();
 }
