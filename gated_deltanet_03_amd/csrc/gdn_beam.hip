@@ -18,6 +18,7 @@
 
 #include "gdn_cache_internal.h"
 #include "gdn_rows.h"
+#include "gdn_scan.h"
 
 namespace gdn {
 
@@ -52,12 +53,15 @@ __device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k) {
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint32_t o = __shfl_xor(v, m);
-    v = o > v ? o : v;
-  }
-  return v;
+  auto up = [&](uint32_t o) { v = o > v ? o : v; };
+  up(__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false));    // lane ^ 1
+  up(__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false));    // lane ^ 2
+  up(__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));   // the other four of 8
+  up(__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));   // the other eight of 16
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = a[0] > a[1] ? a[0] : a[1];
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return b[0] > b[1] ? b[0] : b[1];
 }
 
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
@@ -70,9 +74,9 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+  const uint64_t u = __builtin_bit_cast(uint64_t, wave_scan64(v));
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // Entries of a segment as keys: the logit's order, then the lower index first.
