@@ -817,64 +817,82 @@ def gdn_block_norm(y, *, gate=None, gate_act="silu", residual=None, residual_sca
 # ---------------------------------------------------------------------------
 # Paged cache, beams
 # ---------------------------------------------------------------------------
-def _tokens(t, name, dtype, dev, ragged, H=None, d=None):
-    """(elements between tokens, tokens, H, d) of a [T, H, d] (ragged; also [1, T, H, d]) or [B, L, H, d] tensor whose
-    tokens are evenly spaced and whole."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+# The calls below are made once a layer and token: each first asks everything at once, and looks for what is wrong, to name
+# it, only if something is.
+def _tokens(t, name, dtype, index, ragged, H, d):
+    """(elements between tokens, tokens, heads) of a [T, H, d] (ragged; also [1, T, H, d]) or [B, L, H, d] tensor whose
+    tokens are evenly spaced and whole; any number of heads if H is None."""
     shape = t.shape
-    if ragged and len(shape) == 4 and shape[0] == 1:
-        t = t[0]
-    if t.dim() != (3 if ragged else 4):
-        raise ValueError(f"{name} must be {'[T, H, d] with cu_seqlens' if ragged else '[B, L, H, d]'}, "
-                         f"got shape {tuple(shape)}")
-    h, e = t.shape[-2:]
-    if (H is not None and h != H) or (d is not None and e != d):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected heads {H} of {d}")
-    count = t.shape[0] if ragged else t.shape[0] * t.shape[1]
+    n = len(shape)
+    h, e = shape[-2:] if n > 2 else (-1, -1)
+    if t.dtype is not dtype or t.get_device() != index or e != d or (h != H and H is not None) or \
+            n != (3 if ragged else 4):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected {'cpu' if index < 0 else f'cuda:{index}'}")
+        if n == 4 and ragged and shape[0] == 1:
+            return _tokens(t[0], name, dtype, index, ragged, H, d)
+        if n != (3 if ragged else 4):
+            raise ValueError(f"{name} must be {'[T, H, d] with cu_seqlens' if ragged else '[B, L, H, d]'}, "
+                             f"got shape {tuple(shape)}")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected heads {'of' if H is None else f'{H} of'} {d}")
+    count = shape[0] if ragged else shape[0] * shape[1]
     if t.is_contiguous():
-        return h * e, count, h, e
+        return h * e, count, h
     s = t.stride()
     if (e > 1 and s[-1] != 1) or (h > 1 and s[-2] != e):
         raise ValueError(f"{name}'s heads must be contiguous within a token")
     if ragged:
         row = s[0] if count > 1 else h * e
     else:
-        B, L = t.shape[:2]
+        B, L = shape[:2]
         row = s[1] if L > 1 else (s[0] if B > 1 else h * e)
         if B > 1 and L > 1 and s[0] != L * row:
             raise ValueError(f"{name} must have evenly spaced tokens, got strides {tuple(s)}")
     if row < h * e:
         raise ValueError(f"{name}'s tokens overlap: strides {tuple(s)}")
-    return row, count, h, e
+    return row, count, h
 
 
-def _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev):
-    """Checks shared by the cache's entry points; (N, Hkv, d, page_size, num_pages, max_pages)."""
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [N, max_pages]")
-    dtype = k_cache.dtype
-    if dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {dtype}")
-    _need(k_cache, "k_cache", None, dev)
-    _need(v_cache, "v_cache", dtype, dev)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(k_cache.shape)}")
-    _need(block_table, "block_table", torch.int32, dev)
-    _need(cache_lens, "cache_lens", torch.int32, dev)
-    N, max_pages = block_table.shape
-    if cache_lens.shape != (N,):
-        raise ValueError(f"cache_lens has shape {tuple(cache_lens.shape)}, expected {(N,)}")
-    if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-        if cu_seqlens.shape != (N + 1,):
-            raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected {(N + 1,)}")
-    pages, Hkv, page_size, d = k_cache.shape
-    if Hkv < 1 or page_size < 1:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}")
-    return N, Hkv, d, page_size, pages, max_pages
+_I32 = torch.int32
+
+
+def _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens):
+    """Checks shared by the cache's entry points; (device index, dtype, its code, k_cache's shape, N, max_pages)."""
+    shape, dtype, index = k_cache.shape, k_cache.dtype, k_cache.get_device()
+    code, table = _DTYPES.get(dtype), block_table.shape
+    if code is None or len(shape) != 4 or len(table) != 2 or v_cache.shape != shape or v_cache.dtype is not dtype or \
+            v_cache.get_device() != index or not (k_cache.is_contiguous() and v_cache.is_contiguous()) or \
+            block_table.dtype is not _I32 or block_table.get_device() != index or not block_table.is_contiguous() or \
+            cache_lens.dtype is not _I32 or cache_lens.get_device() != index or not cache_lens.is_contiguous() or \
+            cache_lens.shape != table[:1] or shape[1] < 1 or shape[2] < 1:
+        if len(shape) != 4 or len(table) != 2:
+            raise ValueError("k_cache must be [num_pages, Hkv, page_size, d] and block_table [N, max_pages]")
+        if code is None:
+            raise TypeError(f"unsupported dtype {dtype}")
+        dev = k_cache.device
+        _need(k_cache, "k_cache", None, dev)
+        _need(v_cache, "v_cache", dtype, dev)
+        if v_cache.shape != shape:
+            raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, k_cache {tuple(shape)}")
+        _need(block_table, "block_table", _I32, dev)
+        _need(cache_lens, "cache_lens", _I32, dev)
+        if cache_lens.shape != table[:1]:
+            raise ValueError(f"cache_lens has shape {tuple(cache_lens.shape)}, expected {(table[0],)}")
+        raise ValueError(f"k_cache has shape {tuple(shape)}")
+    N, max_pages = table
+    if cu_seqlens is not None and (cu_seqlens.dtype is not _I32 or cu_seqlens.get_device() != index or
+                                   cu_seqlens.shape != (N + 1,) or not cu_seqlens.is_contiguous()):
+        _need(cu_seqlens, "cu_seqlens", _I32, k_cache.device)
+        raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected {(N + 1,)}")
+    return index, dtype, code, shape, N, max_pages
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape and type (a slice of wider rows may be the model)."""
+    out = torch.empty_like(t)
+    return out if out.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def gdn_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, *, cu_seqlens=None, q=None, inv_freq=None,
@@ -888,55 +906,55 @@ def gdn_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     pair).  ``interleaved`` pairs elements 2j, 2j + 1 instead of j, j + rotary / 2.  ``q_out`` may be q.
     Returns q_out (None without q)."""
     lib = load_library()
-    dev, ragged = k_cache.device, cu_seqlens is not None
-    N, Hkv, d, page_size, pages, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev)
-    dtype = k_cache.dtype
-    ks, tokens, _, _ = _tokens(k, "k", dtype, dev, ragged, Hkv, d)
-    vs, nv, _, _ = _tokens(v, "v", dtype, dev, ragged, Hkv, d)
+    ragged = cu_seqlens is not None
+    index, dtype, code, (pages, Hkv, page_size, d), N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens,
+                                                                                 cu_seqlens)
+    ks, tokens, _ = _tokens(k, "k", dtype, index, ragged, Hkv, d)
+    vs, nv, _ = _tokens(v, "v", dtype, index, ragged, Hkv, d)
     if nv != tokens or (not ragged and (k.shape[0] != N or v.shape != k.shape)):
         raise ValueError(f"k has shape {tuple(k.shape)}, v {tuple(v.shape)}, for {N} sequences")
     Hq, qs = Hkv, Hkv * d
     if q is not None:
         if inv_freq is None:
             raise ValueError("q is given without inv_freq: there is nothing to do with it")
-        qs, nq, Hq, _ = _tokens(q, "q", dtype, dev, ragged, None, d)
+        qs, nq, Hq = _tokens(q, "q", dtype, index, ragged, None, d)
         if nq != tokens or (not ragged and q.shape[:2] != k.shape[:2]):
             raise ValueError(f"q has shape {tuple(q.shape)}, k {tuple(k.shape)}")
         if Hq % Hkv != 0:
             raise ValueError(f"Hq={Hq} must be a multiple of Hkv={Hkv}")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=dev)
+            q_out = _like(q)
         else:
-            _need(q_out, "q_out", dtype, dev)
+            _need(q_out, "q_out", dtype, q.device)
             if q_out.shape != q.shape:
                 raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
     elif q_out is not None:
         raise ValueError("q_out is given without q")
     rotary, axes = 0, 1
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, dev)
         rotary = 2 * inv_freq.numel()
-        if inv_freq.dim() != 1 or rotary < 1 or rotary > d:
+        if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != index or not inv_freq.is_contiguous() or \
+                inv_freq.dim() != 1 or not 1 < rotary <= d:
+            _need(inv_freq, "inv_freq", torch.float32, k_cache.device)
             raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [rotary / 2] with rotary <= {d}")
     if positions is not None:
-        _need(positions, "positions", torch.int32, dev)
+        _need(positions, "positions", _I32, k_cache.device)
         if inv_freq is None:
             raise ValueError("positions are given without inv_freq")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
         if positions.dim() > 2 or axes < 1 or positions.shape[-1] != tokens:
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [{tokens}] or [axes, {tokens}]")
     if pair_axis is not None:
-        _need(pair_axis, "pair_axis", torch.int32, dev)
+        _need(pair_axis, "pair_axis", _I32, k_cache.device)
         _expect(pair_axis, "pair_axis", rotary // 2)
     elif axes > 1:
         raise ValueError(f"pair_axis is required with {axes} axes")
-    T = tokens if ragged else k.shape[1]
-    _, ref = _descriptor(gdn_cache_shape, (N, T, Hq, Hkv, d, _DTYPES[dtype], page_size, pages, max_pages))
-    _, how = _descriptor(gdn_append_shape, (qs, ks, vs, rotary, int(bool(interleaved)), axes))
-    stream = _on_gpu(dev)
+    _, ref = _descriptor(gdn_cache_shape, (N, tokens if ragged else k.shape[1], Hq, Hkv, d, code, page_size, pages,
+                                           max_pages))
+    _, how = _descriptor(gdn_append_shape, (qs, ks, vs, rotary, 1 if interleaved else 0, axes))
     st = lib.gdn_cache_append(ref, how, _addr(q), k.data_ptr(), v.data_ptr(), _addr(inv_freq), _addr(positions),
                               _addr(pair_axis), block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens),
-                              _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), stream)
+                              _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), _on_gpu(k_cache.device))
     if st:
         _check(st)
     return q_out
@@ -958,22 +976,23 @@ def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     i of the L of a sequence has the place cache_lens - L + i and sees the keys up to it, with ``window`` only the
     last ``window`` of them.  ``scale`` is d^-1/2 unless given.  Returns o (q's shape, contiguous)."""
     lib = load_library()
-    dev, ragged = k_cache.device, cu_seqlens is not None
-    N, Hkv, d, page_size, pages, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens, dev)
-    dtype = k_cache.dtype
-    qs, tokens, Hq, _ = _tokens(q, "q", dtype, dev, ragged, None, d)
+    ragged = cu_seqlens is not None
+    index, dtype, code, (pages, Hkv, page_size, d), N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens,
+                                                                                 cu_seqlens)
+    qs, tokens, Hq = _tokens(q, "q", dtype, index, ragged, None, d)
     if Hq < 1 or Hq % Hkv != 0:
         raise ValueError(f"Hq={Hq} must be a multiple of Hkv={Hkv}")
     if not ragged and q.shape[0] != N:
         raise ValueError(f"q has shape {tuple(q.shape)}, for {N} sequences")
     if o is None:
-        o = torch.empty(q.shape, dtype=dtype, device=dev)
+        o = _like(q)
     else:
-        _need(o, "o", dtype, dev)
+        _need(o, "o", dtype, q.device)
         if o.shape != q.shape:
             raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(q.shape)}")
-    T = tokens if ragged else q.shape[1]
-    _, ref = _descriptor(gdn_cache_shape, (N, T, Hq, Hkv, d, _DTYPES[dtype], page_size, pages, max_pages))
+    _, ref = _descriptor(gdn_cache_shape, (N, tokens if ragged else q.shape[1], Hq, Hkv, d, code, page_size, pages,
+                                           max_pages))
+    dev = k_cache.device
     stream = _on_gpu(dev)
     if workspace is None:   # an invalid shape is named by the call itself
         workspace = _scratch(lib.gdn_cache_attention_workspace_bytes(ref, ragged), dev)
@@ -982,7 +1001,7 @@ def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib.gdn_cache_attention(ref, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
                                  cache_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else float(scale),
-                                 int(window), o.data_ptr(), _addr(workspace), nbytes, stream)
+                                 window, o.data_ptr(), _addr(workspace), nbytes, stream)
     if st:
         _check(st)
     return o
@@ -1050,19 +1069,17 @@ def gdn_beam_select(logits, scores, *, beams=None, finished=None, eos_token=-1, 
             raise ValueError(f"finished has shape {tuple(finished.shape)}, expected {(B, W)}")
     if K < 1:
         raise ValueError(f"beams={K} < 1")
-    outs = []
-    for t, n, kind in ((tokens, "tokens", torch.int32), (parents, "parents", torch.int32),
-                       (new_scores, "new_scores", torch.float32), (new_finished, "new_finished", torch.bool)):
+    outs = [tokens, parents, new_scores, new_finished]
+    for i, kind in enumerate((_I32, _I32, torch.float32, torch.bool)):
+        t = outs[i]
         if t is None:
-            t = torch.empty((B, K), dtype=kind, device=dev)
-        else:
-            _need(t, n, kind, dev)
-            if t.shape != (B, K):
-                raise ValueError(f"{n} has shape {tuple(t.shape)}, expected {(B, K)}")
-        outs.append(t)
-    for name, x in (("eos_token", eos_token), ("pad_token", pad_token)):
-        if not -(1 << 31) <= x < 1 << 31:
-            raise ValueError(f"{name}={x} does not fit 32 bits")
+            outs[i] = torch.empty_like(scores, dtype=kind) if K == W else torch.empty((B, K), dtype=kind, device=dev)
+        elif t.dtype is not kind or t.device != dev or t.shape != (B, K) or not t.is_contiguous():
+            name = ("tokens", "parents", "new_scores", "new_finished")[i]
+            _need(t, name, kind, dev)
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, K)}")
+    if not (-0x80000000 <= eos_token < 0x80000000 and -0x80000000 <= pad_token < 0x80000000):
+        raise ValueError(f"eos_token={eos_token} or pad_token={pad_token} does not fit 32 bits")
     _, ref = _descriptor(gdn_beam_shape, (B, W, K, V, _DTYPES[dtype], int(eos_token), int(pad_token), row))
     stream = _on_gpu(dev)
     if workspace is None:
