@@ -209,8 +209,14 @@ struct Line {
       }
     }
     if (!none && count * 4 <= a.shares) {
+      // a sequence's tiles all count as its longest: then at most one share a tile comes on top
+      int drawn = 0;
+      for (int s = 0; s < a.N; s += 64) {
+        load(s);
+        drawn += wave_sum(tiles > 0 ? tiles * (first + step * (tiles - 1)) : 0);
+      }
       r.drawn = 1;
-      r.share = max(least, parts(all, a.shares - count));
+      r.share = max(least, parts(drawn, a.shares - count));
       r.rest = 0;
       for (int s = 0; s < a.N; s += 64) {
         load(s);
@@ -302,7 +308,7 @@ struct Cut {
 // Borders near a tile's end lie there.
 __device__ __forceinline__ int border(int x, int length, int share) {
   const int near = share >> 4;
-  return x < near ? 0 : (length - x < near ? length : x);
+  return x >= length ? length : (x < near ? 0 : (length - x < near ? length : x));
 }
 
 template <typename T> struct Op;

@@ -110,6 +110,56 @@ def test_against_the_oracle(gdn, shape, dtype):
     check(call(gdn, c), oracle(c), c, "o")
 
 
+# Prompts from one to many tiles of rows beside the card's workgroups, over themselves and over older text: the work is
+# left whole, drawn out to whole shares, cut evenly, or cut behind whole rounds of tiles.
+CUTS = [([1031], [1031], 4, 1, 64), ([520], [3000], 2, 2, 64), ([200, 900, 3], [1500, 900, 4000], 4, 1, 32),
+        ([33], [6000], 4, 1, 128), ([700, 40], [700, 2500], 2, 1, 256)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", CUTS)
+def test_cuts(gdn, new, ctx, Hq, Hkv, d, dtype):
+    c = make(61 + d, new, ctx, Hq, Hkv, d, 32, dtype)
+    say(f"cuts {dtype} {new} {ctx}")
+    check(call(gdn, c), oracle(c), c, "o")
+
+
+def plain(c):
+    """The formula in 64 bits on the GPU, for sizes that the oracle's loops take too long for."""
+    d = {n: (x.to(DEV) if torch.is_tensor(x) else x) for n, x in c.items()}
+    (N, _), ps, d_ = d["table"].shape, d["kc"].shape[2], d["kc"].shape[3]
+    Hkv, cu = d["kc"].shape[1], c["cu"].tolist()
+    G = c["q"].shape[1] // Hkv
+    out = {"o": torch.zeros(c["q"].shape, dtype=torch.float64, device=DEV)}
+    out["size"], out["score"] = torch.zeros_like(out["o"]), torch.zeros(*c["q"].shape[:2], 1, dtype=torch.float64, device=DEV)
+    for s in range(N):
+        L, n = cu[s + 1] - cu[s], int(c["lens"][s])
+        j = torch.arange(n, device=DEV)
+        page = d["table"][s].long()[j // ps]
+        hidden = j > torch.arange(n - L, n, device=DEV)[:, None]
+        for h in range(Hkv):
+            k, v = (d[x][page, h, j % ps].double() for x in ("kc", "vc"))
+            for g in range(h * G, h * G + G):
+                q = d["q"][cu[s]:cu[s + 1], g].double()
+                w = torch.softmax((c["scale"] * (q @ k.T)).masked_fill(hidden, -math.inf), -1)
+                out["o"][cu[s]:cu[s + 1], g] = w @ v
+                out["size"][cu[s]:cu[s + 1], g] = w @ v.abs()
+                out["score"][cu[s]:cu[s + 1], g] = c["scale"] * (q.abs() @ k.abs().T).amax(-1, keepdim=True)
+    return {n: f64(x) for n, x in out.items()}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", [
+    ([2048, 700, 1, 63], [9000, 5000, 3000, 1031], 16, 4, 128), ([4000], [4000], 8, 8, 64),
+    ([64, 1, 1, 1, 1, 1, 1, 1], [4096, 900, 700, 3000, 1500, 12000, 64, 129], 16, 4, 128),
+    ([513, 300, 700, 64, 1000, 128], [513, 300, 700, 64, 1000, 128], 16, 2, 256), ([1] * 70, list(range(10, 7010, 100)), 8, 4, 64),
+    ([5] * 9, [20000] + [50] * 8, 8, 2, 32)])
+def test_large(gdn, new, ctx, Hq, Hkv, d, dtype):
+    c = make(71, new, ctx, Hq, Hkv, d, 64, dtype)
+    say(f"large {dtype} {new} {ctx}")
+    check(call(gdn, c), plain(c), c, "o")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("window", [1, 5, 16, 100, 5000])
 @pytest.mark.parametrize("new,ctx", [([1, 4], [300, 90]), ([70, 3], [200, 3])])

@@ -1,0 +1,85 @@
+"""Every key counts once, however the work is cut.
+
+All scores are 0, so every weight is 1 and every sum a whole number below 2^24: exact in fp32, whatever its order.
+Column c of the value of key j is 1 where (j / 16) mod 31 = c and 0 elsewhere, column 31 is 1: o times the number of keys
+that a token sees is their count in each class, off by 3 roundings (1 / l, its product, the one here)."""
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import gated_deltanet_03_amd as m
+    m.load_library()
+    return m
+
+
+def draw(rng):
+    kind = rng.choice(["next", "drafts", "prompts", "mixed", "one"])
+    Hkv, G = rng.choice([1, 2, 3, 4, 8, 16]), rng.choice([1, 2, 3, 4, 8])
+    d, page = rng.choice([32, 64, 64, 128, 256]), rng.choice([16, 32, 48, 64, 256])
+    far = rng.choice([100, 1000, 5000, 20000])
+    if kind == "next":
+        new = [1] * rng.choice([1, 3, 17, 64, 130, 300])
+    elif kind == "drafts":
+        new = [rng.randint(0, 8) for _ in range(rng.choice([1, 5, 20, 90]))]
+    elif kind == "prompts":
+        new = [rng.randint(1, 1500) for _ in range(rng.randint(1, 5))]
+    elif kind == "one":
+        new = [rng.randint(1, 4000)]
+    else:
+        new = [rng.choice([1, 1, 1, 4, rng.randint(30, 900)]) for _ in range(rng.randint(2, 40))]
+    room = 60_000_000 // (Hkv * d)               # keys of a cache of 240 MB
+    ctx = []
+    for n in new:
+        old = rng.choice([0, rng.randint(0, far), rng.randint(0, far), rng.randint(0, 30)])
+        old = max(0, min(old, room - n))
+        room -= n + old + page
+        ctx.append(n + old if room > 0 else n)
+    return dict(new=new, ctx=ctx, Hkv=Hkv, G=G, d=d, page=page, window=rng.choice([0, 0, 0, rng.randint(1, 3000)]),
+                spare=rng.choice([0, 0, 7, 400]))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_every_key_counts_once(gdn, seed):
+    c = draw(random.Random(seed))
+    new, ctx, Hkv, G, d, page = c["new"], c["ctx"], c["Hkv"], c["G"], c["d"], c["page"]
+    say(f"cut {c}")
+    need = [-(-n // page) for n in ctx]
+    starts = np.concatenate([[0], np.cumsum(need)])
+    N, most = len(new), max(max(need), 1) + c["spare"]
+    j = torch.cat([torch.arange(n * page) for n in need] or [torch.zeros(0, dtype=torch.long)]).view(-1, page).to(DEV)
+    v = torch.zeros(len(j), 1, page, d, device=DEV)
+    v.scatter_(3, ((j >> 4) % 31)[:, None, :, None], 1.0)
+    v[..., 31] = 1.0
+    v = v.expand(-1, Hkv, -1, -1).contiguous()
+    k = torch.zeros_like(v)
+    table = np.full((N, most), -1, dtype=np.int32)
+    for s in range(N):
+        table[s, :need[s]] = np.arange(starts[s], starts[s + 1])
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.randn(int(cu[-1]), Hkv * G, d, device=DEV)
+    o = torch.full_like(q, float("nan"))
+    gdn.gdn_cache_attention(q, k, v, torch.from_numpy(table).to(DEV), torch.tensor(ctx, dtype=torch.int32, device=DEV),
+                            cu_seqlens=torch.from_numpy(cu).to(DEV), window=c["window"], o=o)
+    # what each token sees
+    hi = np.concatenate([np.arange(m - n, m) for n, m in zip(new, ctx)] or [np.zeros(0, int)]) + 1
+    lo = np.maximum(hi - c["window"], 0) if c["window"] else np.zeros_like(hi)
+    every = np.arange(max(max(ctx), 1))
+    cum = np.zeros((len(every) + 1, 32))
+    cum[1:, :31] = np.cumsum(((every >> 4) % 31)[:, None] == np.arange(31), 0)
+    cum[1:, 31] = every + 1
+    want = torch.from_numpy(cum[hi] - cum[lo]).to(DEV)[:, None]
+    n = torch.from_numpy(hi - lo).to(DEV)[:, None, None].double()
+    got = o[..., :32].double() * n
+    off = ((got - want).abs() / want.clamp(min=1)).amax() if len(q) else 0.0
+    assert not torch.isnan(o).any() and float(off) <= 3 * 2.0 ** -24, (float(off), c)
+    assert not o[..., 32:].any()
