@@ -160,7 +160,7 @@ struct Line {
       int e;
       seq_range(a.cu, a.T, a.total, s, b, e);
       L = e - b;
-      lens = min(max(a.lens[s], -(1 << 30)), 1 << 30);
+      lens = min(max(a.lens[s], 0), 1 << 30);     // (below 0 no token has a place, as with 0)
       tiles = (int)(((int64_t)L * a.G + ROWS - 1) / ROWS);
       const int old = min(max(lens - L, 0), a.room), more = ROWS / a.G + 1;
       const bool inside = a.window > 0 && a.window < old;
@@ -193,8 +193,9 @@ struct Line {
     for (int s = 0; s < a.N; s += 64) {
       load(s);
       all += wave_sum(tiles_length(first, step, tiles));
-      count += wave_sum(tiles);
+      count += wave_sum(min(tiles, a.tiles + 1));
       longest = max(longest, wave_max(tiles > 0 ? first + step * (tiles - 1) : 0));
+      if (count > a.tiles) return r;      // offsets that overlap: more tiles than the line has room for, no work at all
     }
     auto parts = [](int x, int n) { return (int)(((uint32_t)x + (uint32_t)n - 1) / (uint32_t)n); };
     const int even = parts(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
@@ -233,7 +234,6 @@ struct Line {
       }
       const int rounds = may / a.shares;
       r.whole = none || (sure == 0 && rounds >= 3) ? may : rounds * a.shares;
-      r.whole = max(min(r.whole, a.tiles), 0);     // (malformed offsets may count more tiles than there is room for)
       int before = 0;
       r.rest = 0;
       for (int s = 0; s < a.N; s += 64) {
@@ -269,7 +269,7 @@ struct Line {
         const int cut = n - lane_value(kept, j);     // tiles that are not whole
         int f = lane_value(first, j), st = lane_value(step, j), i = 0;
         if constexpr (WHOLE) {
-          i = n - 1 - rest;                          // a sequence's last tiles see the most keys: first
+          i = max(n - 1 - rest, 0);                  // a sequence's last tiles see the most keys: first
         } else {
           if (sh.drawn) f = drawn_tile(f, st, n, sh), st = 0;
           if (cut > 1) {          // f i + st i (i - 1) / 2 <= rest, nearly by the quadratic's root, then exactly
@@ -1138,8 +1138,8 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
   __shared__ float2 ml[kJoinThreads];
   __shared__ float4 sums[kJoinThreads];
   const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  if (cut.end - cut.begin < 2 || cut.end > a.shares + 1) return;
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), j = (int)(blockIdx.x / a.c.Hkv);
+  if (cut.end - cut.begin < 2) return;
   const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
   const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
   if (items <= 0) return;

@@ -457,8 +457,10 @@ gdn_status gdn_block_norm(const gdn_norm_shape* shape, const void* y, const void
  *                   cache_lens[s] - L_s + i.
  * cu_seqlens        int32 [N+1] as above (packed rows; those behind cu_seqlens[N] are
  *                   neither read nor written), or NULL: T tokens for each of N rows.
+ * Offsets that decrease or overlap leave the outputs of these rows unspecified; nothing
+ * out of range is read or written.
  * d in {32, 64, 128, 256}; page_size a multiple of 16 up to 1024; max_pages * page_size
- * up to 2^26; all pointers 16-byte aligned, token strides multiples of 16 bytes
+ * up to 2^26; N up to 2^20; Hq/Hkv up to 256; all pointers 16-byte aligned, token strides multiples of 16 bytes
  * (cu_seqlens, cache_lens, block_table, positions, pair_axis, inv_freq: 4-byte).
  */
 typedef struct {
@@ -521,7 +523,7 @@ gdn_status gdn_cache_append(const gdn_cache_shape* shape, const gdn_append_shape
  *
  * Precision: scores, the running maximum and all sums in fp32, o rounded once; for
  * 16-bit inputs the weights are rounded to the input type (against a running
- * maximum, at most 2^8) as operands of their product with v.
+ * maximum, at most 2^8) as operands of their product with v, and summed as rounded.
  *
  *  q, o       [tokens, Hq, d]; q at q_token_stride (elements), o contiguous.
  *  scale      finite and > 0.
@@ -545,7 +547,7 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* shape, const void* q, int6
  * pad_token, with its score unchanged.  The K largest in descending order, ties to
  * the lowest w, then the lowest v.
  *
- * exp in fp32 (2^-23 of a term), sums, logarithm and scores in 64 bits; new_scores
+ * exp in fp32 (2^-22 of a term near the maximum), sums, logarithm and scores in 64 bits; new_scores
  * rounded once to fp32.  Two continuations of different beams nearer than about
  * 2^-24 may change places.  Logits of -infinity are no continuations.  A beam counts
  * as absent if its score is not finite, or (unfinished) a logit is NaN or +infinity,
