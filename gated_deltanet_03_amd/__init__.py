@@ -889,6 +889,21 @@ def _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens):
     return index, dtype, code, shape, N, max_pages
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(dev, call, *args):
+    """call(*args, dev's stream): kernels start on the current device, so that is made dev where it is another."""
+    stream = _on_gpu(dev)
+    if _current_device() == dev.index:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, stream)
+    if st:
+        _check(st)
+
+
 def _like(t):
     """A new contiguous tensor of t's shape and type (a slice of wider rows may be the model)."""
     out = torch.empty_like(t)
@@ -907,8 +922,8 @@ def gdn_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     Returns q_out (None without q)."""
     lib = load_library()
     ragged = cu_seqlens is not None
-    index, dtype, code, (pages, Hkv, page_size, d), N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens,
-                                                                                 cu_seqlens)
+    index, dtype, code, shape, N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens)
+    pages, Hkv, page_size, d = shape
     ks, tokens, _ = _tokens(k, "k", dtype, index, ragged, Hkv, d)
     vs, nv, _ = _tokens(v, "v", dtype, index, ragged, Hkv, d)
     if nv != tokens or (not ragged and (k.shape[0] != N or v.shape != k.shape)):
@@ -952,11 +967,9 @@ def gdn_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     _, ref = _descriptor(gdn_cache_shape, (N, tokens if ragged else k.shape[1], Hq, Hkv, d, code, page_size, pages,
                                            max_pages))
     _, how = _descriptor(gdn_append_shape, (qs, ks, vs, rotary, 1 if interleaved else 0, axes))
-    st = lib.gdn_cache_append(ref, how, _addr(q), k.data_ptr(), v.data_ptr(), _addr(inv_freq), _addr(positions),
-                              _addr(pair_axis), block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens),
-                              _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr(), _on_gpu(k_cache.device))
-    if st:
-        _check(st)
+    _launch(k_cache.device, lib.gdn_cache_append, ref, how, _addr(q), k.data_ptr(), v.data_ptr(), _addr(inv_freq),
+            _addr(positions), _addr(pair_axis), block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens),
+            _addr(q_out), k_cache.data_ptr(), v_cache.data_ptr())
     return q_out
 
 
@@ -977,8 +990,8 @@ def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seql
     last ``window`` of them.  ``scale`` is d^-1/2 unless given.  Returns o (q's shape, contiguous)."""
     lib = load_library()
     ragged = cu_seqlens is not None
-    index, dtype, code, (pages, Hkv, page_size, d), N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens,
-                                                                                 cu_seqlens)
+    index, dtype, code, shape, N, max_pages = _cache_common(k_cache, v_cache, block_table, cache_lens, cu_seqlens)
+    pages, Hkv, page_size, d = shape
     qs, tokens, Hq = _tokens(q, "q", dtype, index, ragged, None, d)
     if Hq < 1 or Hq % Hkv != 0:
         raise ValueError(f"Hq={Hq} must be a multiple of Hkv={Hkv}")
@@ -992,18 +1005,17 @@ def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seql
             raise ValueError(f"o has shape {tuple(o.shape)}, expected {tuple(q.shape)}")
     _, ref = _descriptor(gdn_cache_shape, (N, tokens if ragged else q.shape[1], Hq, Hkv, d, code, page_size, pages,
                                            max_pages))
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window={window} must be in [0, 2^31)")
     dev = k_cache.device
-    stream = _on_gpu(dev)
     if workspace is None:   # an invalid shape is named by the call itself
         workspace = _scratch(lib.gdn_cache_attention_workspace_bytes(ref, ragged), dev)
     else:
         _need(workspace, "workspace", None, dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.gdn_cache_attention(ref, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                                 cache_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else float(scale),
-                                 window, o.data_ptr(), _addr(workspace), nbytes, stream)
-    if st:
-        _check(st)
+    _launch(dev, lib.gdn_cache_attention, ref, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else float(scale),
+            window, o.data_ptr(), _addr(workspace), nbytes)
     return o
 
 
@@ -1028,11 +1040,8 @@ def gdn_cache_copy_pages(k_cache, v_cache, src_pages, dst_pages):
         return
     row = k_cache.numel() // rows * k_cache.element_size()
     _, ref = _descriptor(gdn_reorder_shape, (2, apart, apart, rows, rows, row, 0, G, W))
-    stream = _on_gpu(dev)
-    st = lib.gdn_state_reorder(ref, k_cache.data_ptr(), k_cache.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(),
-                               stream)
-    if st:
-        _check(st)
+    _launch(dev, lib.gdn_state_reorder, ref, k_cache.data_ptr(), k_cache.data_ptr(), src_pages.data_ptr(),
+            dst_pages.data_ptr())
 
 
 def gdn_beam_workspace_bytes(shape: gdn_beam_shape) -> int:
@@ -1081,17 +1090,13 @@ def gdn_beam_select(logits, scores, *, beams=None, finished=None, eos_token=-1, 
     if not (-0x80000000 <= eos_token < 0x80000000 and -0x80000000 <= pad_token < 0x80000000):
         raise ValueError(f"eos_token={eos_token} or pad_token={pad_token} does not fit 32 bits")
     _, ref = _descriptor(gdn_beam_shape, (B, W, K, V, _DTYPES[dtype], int(eos_token), int(pad_token), row))
-    stream = _on_gpu(dev)
     if workspace is None:
         workspace = _scratch(lib.gdn_beam_workspace_bytes(ref), dev)
     else:
         _need(workspace, "workspace", None, dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib.gdn_beam_select(ref, logits.data_ptr(), scores.data_ptr(), _addr(finished), outs[0].data_ptr(),
-                             outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), _addr(workspace), nbytes,
-                             stream)
-    if st:
-        _check(st)
+    _launch(dev, lib.gdn_beam_select, ref, logits.data_ptr(), scores.data_ptr(), _addr(finished), outs[0].data_ptr(),
+            outs[1].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), _addr(workspace), nbytes)
     return tuple(outs)
 
 
@@ -1126,10 +1131,7 @@ def gdn_state_reorder(state, parents, *, axis=0, out=None):
     if row % 16 != 0:
         raise ValueError(f"a row of {row} bytes is not a multiple of 16")
     _, ref = _descriptor(gdn_reorder_shape, (layers, rows * row, B * K * row, rows, B * K, row, rows // B, B, K))
-    stream = _on_gpu(dev)
-    st = lib.gdn_state_reorder(ref, state.data_ptr(), out.data_ptr(), parents.data_ptr(), None, stream)
-    if st:
-        _check(st)
+    _launch(dev, lib.gdn_state_reorder, ref, state.data_ptr(), out.data_ptr(), parents.data_ptr(), None)
     return out
 
 

@@ -259,3 +259,32 @@ def test_binding_reorder_refusals():
                            ((c, c, p.long(), p), TypeError, "src_pages"), ((c, c.clone(), p, p), ValueError, "GPU")):
         with pytest.raises(error, match=word):
             gdn.gdn_cache_copy_pages(*a)
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 31, 1 << 40])
+def test_binding_window(window):
+    with pytest.raises(ValueError, match="window"):
+        call_attend(tensors(), window=window)
+
+
+def test_launches_on_the_tensors_device(monkeypatch):
+    """A kernel starts on the current device; tensors of another one make that current for the call."""
+    seen, entered = [], []
+
+    class Device:
+        def __init__(self, dev):
+            entered.append(dev)
+
+        def __enter__(self):
+            seen.append("in")
+
+        def __exit__(self, *a):
+            seen.append("out")
+    monkeypatch.setattr(gdn, "_on_gpu", lambda dev: 1000 + dev.index)
+    monkeypatch.setattr(gdn, "_current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for index in (1, 0):
+        gdn._launch(torch.device("cuda", index), lambda *a: seen.append(a), "x")
+    assert seen == [("x", 1001), "in", ("x", 1000), "out"] and entered == [torch.device("cuda", 0)]
+    with pytest.raises(gdn.GdnError):
+        gdn._launch(torch.device("cuda", 0), lambda *a: gdn.GDN_ERR_INVALID_ARG)
