@@ -82,6 +82,13 @@ __device__ __forceinline__ constexpr int value_swizzle(int r) {
 __device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
 __device__ __forceinline__ int lane_value(int x, int lane) { return __builtin_amdgcn_readlane(x, lane); }
 
+// x / n and its ceiling where that is below 2^20: the reciprocal's product is less than one off.
+__device__ __forceinline__ int quotient(int x, int n) {
+  const int q = (int)((float)x * __builtin_amdgcn_rcpf((float)n)), r = x - q * n;
+  return q + (r >= n) - (r < 0);
+}
+__device__ __forceinline__ int quotient_up(int x, int n) { return quotient(x + n - 1, n); }
+
 // Inclusive prefix sum over the wave's lanes.
 __device__ __forceinline__ int wave_scan(int x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);   // row_shr:1
@@ -92,10 +99,14 @@ __device__ __forceinline__ int wave_scan(int x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
   return x;
 }
-__device__ __forceinline__ int wave_max(int x) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) x = max(x, __shfl_xor(x, m));
-  return scalar(x);
+__device__ __forceinline__ int wave_max(int x) {   // of numbers that are not negative
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return lane_value(x, 63);
 }
 __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x), 63); }
 
@@ -118,7 +129,9 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 // outlast all others.
 //
 // Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one
-// piece, and a second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.
+// piece, and a second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.  A share is
+// a multiple `run` of the step there, so that tile i has ceil((ceil(first / step) + i) / run) of them, whose sum and its inverse
+// have a closed form.
 //
 // Borders between shares that come within a 16th of a share of a tile's end are moved there.
 struct Piece {
@@ -131,7 +144,7 @@ struct Shares {
   int longest;             // of the tiles that may stay whole
   int whole;               // tiles that stay whole
   int rest, share;         // length of the line that is left, and of a share of it
-  int drawn;               // tiles are whole numbers of shares
+  int drawn;               // tiles are whole numbers of shares: of how many steps a share is, 0: they are not
 };
 
 // What the work is laid out from.
@@ -175,12 +188,44 @@ struct Line {
   }
   // The lane's sequence without its last `kept` tiles.
   __device__ __forceinline__ int length(int kept, const Shares& sh) const {
-    if (sh.drawn) return tiles * drawn_tile(first, step, tiles, sh);
+    if (sh.drawn) {
+      if (__ballot(tiles > 1) == 0) return tiles * Drawn(first, step, sh).q * sh.share;
+      return tiles > 0 ? Drawn(first, step, sh).shares(tiles) * sh.share : 0;
+    }
     return tiles_length(first, step, tiles - kept);
   }
-  static __device__ __forceinline__ int drawn_tile(int first, int step, int tiles, const Shares& sh) {
-    return tiles > 0 ? (int)((float)(first + step * (tiles - 1)) / (float)sh.share + 0.999f) * sh.share : 0;
-  }
+
+  // Drawn out: tile i of a sequence has q + floor((i + r) / run) shares.
+  struct Drawn {
+    int run, q, r;
+    __device__ __forceinline__ Drawn(int first, int step, const Shares& sh) : run(1 << 30), r(0) {
+      if (step != 0) {
+        const int a = up(first, step) + sh.drawn - 1;
+        run = sh.drawn, q = quotient(a, run), r = a - q * run;
+      } else {
+        q = quotient_up(first, sh.share);
+      }
+    }
+    // The shares of i tiles; g(r + i) of them lie in whole runs.
+    __device__ __forceinline__ int shares(int i) const {
+      const int g = quotient(r + i, run);
+      return i * q + run * (g * (g - 1) / 2) + (r + i - g * run) * g;
+    }
+    // The tile in which share x lies: of those from tile run * g - r on with q + g shares each, g nearly by the
+    // quadratic's root, then exactly.
+    __device__ __forceinline__ int tile(int x) const {
+      auto before = [&](int g) { return (run * g - r) * q + run * (g * (g - 1) / 2); };
+      int g = 0;
+      if (run < 1 << 30) {
+        const float v = (float)q - 0.5f, w = 2.f * (float)(r * q + x) * __builtin_amdgcn_rcpf((float)run);
+        g = max((int)(__builtin_amdgcn_sqrtf(v * v + w) - v), 0);
+        while (g > 0 && before(g) > x) --g;
+        while (before(g + 1) <= x) ++g;
+      }
+      return run * g - r + quotient(x - before(g), q + g);
+    }
+  };
+  static __device__ __forceinline__ int up(int x, int n) { return (int)(((uint32_t)x + (uint32_t)n - 1) / (uint32_t)n); }
 
   // How many of the lane's tiles may stay whole, however many others do.
   __device__ __forceinline__ int may_be_whole(int longest) const {
@@ -197,8 +242,7 @@ struct Line {
       longest = max(longest, wave_max(tiles > 0 ? first + step * (tiles - 1) : 0));
       if (count > a.tiles) return r;      // offsets that overlap: more tiles than the line has room for, no work at all
     }
-    auto parts = [](int x, int n) { return (int)(((uint32_t)x + (uint32_t)n - 1) / (uint32_t)n); };
-    const int even = parts(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
+    const int even = up(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
     r.rest = all;
     r.share = max(least, even);
     const bool none = count <= a.shares ? longest <= r.share + a.extra : !FEW && longest / 2 <= a.extra;
@@ -210,14 +254,10 @@ struct Line {
       }
     }
     if (!none && count * 4 <= a.shares) {
-      // a sequence's tiles all count as its longest: then at most one share a tile comes on top
-      int drawn = 0;
-      for (int s = 0; s < a.N; s += 64) {
-        load(s);
-        drawn += wave_sum(tiles > 0 ? tiles * (first + step * (tiles - 1)) : 0);
-      }
-      r.drawn = 1;
-      r.share = max(least, parts(drawn, a.shares - count));
+      // a tile has at most (its length + a step) / share + 1 shares
+      const int steps = max((ROWS / a.G + 1) >> a.unit, 1);
+      r.drawn = up(max(least, up(all + count * steps, a.shares - count)), steps);
+      r.share = r.drawn * steps;
       r.rest = 0;
       for (int s = 0; s < a.N; s += 64) {
         load(s);
@@ -242,7 +282,7 @@ struct Line {
         r.rest += wave_sum(length(min(max(r.whole - (upto - mine), 0), mine), r));
         before = lane_value(upto, 63);
       }
-      r.share = max(least, parts(r.rest, a.shares));
+      r.share = max(least, up(r.rest, a.shares));
     }
     return r;
   }
@@ -267,20 +307,32 @@ struct Line {
         const int j = __ffsll((unsigned long long)__ballot(pos < upto)) - 1;
         const int rest = pos - lane_value(upto - mine, j), n = lane_value(tiles, j);
         const int cut = n - lane_value(kept, j);     // tiles that are not whole
-        int f = lane_value(first, j), st = lane_value(step, j), i = 0;
+        const int f = lane_value(first, j), st = lane_value(step, j);
+        int i = 0, at = 0, length = 1;
         if constexpr (WHOLE) {
           i = max(n - 1 - rest, 0);                  // a sequence's last tiles see the most keys: first
         } else {
-          if (sh.drawn) f = drawn_tile(f, st, n, sh), st = 0;
-          if (cut > 1) {          // f i + st i (i - 1) / 2 <= rest, nearly by the quadratic's root, then exactly
-            float x = (float)rest / (float)f;
-            if (st != 0) {
-              const float v = (float)f / (float)st - 0.5f;
-              x = sqrtf(v * v + 2.f * (float)rest / (float)st) - v;
+          if (sh.drawn) {
+            const Drawn x(f, st, sh);
+            length = x.q * sh.share;
+            if (n > 1) {
+              i = x.tile(quotient(rest, sh.share));
+              at = x.shares(i) * sh.share;
+              length = x.shares(i + 1) * sh.share - at;
             }
-            i = min(max((int)x, 0), cut - 1);
-            while (i > 0 && tiles_length(f, st, i) > rest) --i;
-            while (i + 1 < cut && tiles_length(f, st, i + 1) <= rest) ++i;
+          } else {
+            if (cut > 1) {        // f i + st i (i - 1) / 2 <= rest, nearly by the quadratic's root, then exactly
+              float x = (float)rest * __builtin_amdgcn_rcpf((float)f);
+              if (st != 0) {
+                const float s = __builtin_amdgcn_rcpf((float)st), v = (float)f * s - 0.5f;
+                x = __builtin_amdgcn_sqrtf(v * v + 2.f * (float)rest * s) - v;
+              }
+              i = min(max((int)x, 0), cut - 1);
+              while (i > 0 && tiles_length(f, st, i) > rest) --i;
+              while (i + 1 < cut && tiles_length(f, st, i + 1) <= rest) ++i;
+            }
+            at = tiles_length(f, st, i);
+            length = f + st * i;
           }
         }
         p.s = s0 + j;
@@ -288,8 +340,8 @@ struct Line {
         p.L = lane_value(L, j);
         p.lens = lane_value(lens, j);
         p.tile = i;
-        p.at = WHOLE ? pos : pos - rest + tiles_length(f, st, i);
-        p.length = WHOLE ? 1 : f + st * i;
+        p.at = pos - rest + at;
+        p.length = length;
         return true;
       }
       before = total;
@@ -501,6 +553,29 @@ struct Wave {
     for (int k = 0; k < PARTS; ++k) add_part(value_part(V, r0, k), p, k);
   }
 
+  // Whether 32 rows of values hold no infinity or NaN: the largest of all without signs.
+  __device__ __forceinline__ bool finite(const unsigned char* V, int r0) const {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    uint32_t top = 0;
+#pragma unroll 8
+    for (int n = 0; n < RB / 32; ++n) {
+      const uint4 x = *reinterpret_cast<const uint4*>(V + r0 * RB + n * 1024 + lane * 16);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+          top = max(top, w[i] & 0x7fffffffu);
+        } else {
+          top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, top),
+                                                                       __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu)));
+        }
+      }
+    }
+    constexpr uint32_t X = __is_same(T, _Float16) ? 0x7c00u : 0x7f80u;
+    const bool bad = F32 ? top >= 0x7f800000u : (top & 0xffffu) >= X || top >> 16 >= X;
+    return __ballot(bad) == 0;
+  }
+
   // Which of 32 rows of values hold an infinity or NaN.
   __device__ __forceinline__ uint32_t not_finite(const unsigned char* V, int r0) const {
     constexpr int LANES = PPR < 64 ? PPR : 64, PER = 64 / LANES;   // lanes of a row, rows at once
@@ -682,20 +757,28 @@ struct Next {
 enum { kNone, kTile, kPart };
 
 // Finds workgroup j's first piece (first), or the one after the last.  Not inlined: the kernels' registers are full, and
-// what this computes would be kept in them over the pieces.  Every wave has a Next of its own.
+// what this computes would be kept in them over the pieces.
 template <bool FEW>
-__device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
+__device__ __attribute__((noinline)) void plan_piece(Work w, int j, bool first,
                                                      __attribute__((address_space(3))) Next* k) {
+  // arguments come in vector registers: as scalars again, branches on them are branches
+  const uint64_t cu = (uint64_t)w.cu, lens = (uint64_t)w.lens;
+  auto address = [](uint64_t x) {
+    return reinterpret_cast<const int32_t*>((uint64_t)(uint32_t)scalar((int)(x >> 32)) << 32 | (uint32_t)scalar((int)x));
+  };
+  const Work a{address(cu), address(lens), scalar(w.N), scalar(w.T), scalar(w.total), scalar(w.G), scalar(w.room),
+               scalar(w.window), scalar(w.tiles), scalar(w.shares), scalar(w.unit), scalar(w.extra)};
+  j = scalar(j);
+  first = scalar(first) != 0;
   Line<FEW> line(a);
   Shares sh{0, 0, 0, 1, 0};
   int pos = 0, end = 0;
   bool tile = a.shares == 0;
   if (!first) {
-    sh.longest = k->sh.longest, sh.whole = k->sh.whole, sh.rest = k->sh.rest, sh.share = k->sh.share;
-    sh.drawn = k->sh.drawn;
-    pos = k->pos;
-    end = k->end;
-    j = k->j;
+    sh = Shares{scalar(k->sh.longest), scalar(k->sh.whole), scalar(k->sh.rest), scalar(k->sh.share), scalar(k->sh.drawn)};
+    pos = scalar(k->pos);
+    end = scalar(k->end);
+    j = scalar(k->j);
   } else if (!tile) {
     sh = line.share_out();
     if (j >= sh.whole + a.shares) {                  // the grid has room for more whole tiles
@@ -723,11 +806,9 @@ __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
       slot = 2 * j + (from == 0);
       if (first && from > 0 && u.at >= pos - sh.share) {
         const int last = u.at + u.length;
-        int n = max((int)((float)last / (float)sh.share), j);      // the share that ends the tile
-        while (n > j && (int64_t)n * sh.share >= last) --n;
-        while ((int64_t)(n + 1) * sh.share < last) ++n;
+        const int n = quotient(last - 1, sh.share);                // the share that ends the tile
         const int begin = border(from, u.length, sh.share) == 0;
-        const int over = border((int)((int64_t)n * sh.share - u.at), u.length, sh.share) == u.length;
+        const int over = border(n * sh.share - u.at, u.length, sh.share) == u.length;
         cut = Cut{u.b, u.L, u.tile, (short)begin, (short)(n - j + 2 - over)};
       }
       first = false;
@@ -753,12 +834,15 @@ __device__ __attribute__((noinline)) void plan_piece(Work a, int j, bool first,
 // workgroup has a tile.
 template <bool FEW, typename B>
 __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j, B&& body) {
-  __shared__ Next next[4];
-  Next& k = next[threadIdx.x >> 6];
+  __shared__ Next k;
+  const int wave = scalar(threadIdx.x >> 6);
   const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares,
                   a.unit, a.extra};
   for (bool first = true;; first = false) {
-    plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
+    // One wave for all: the others would only get in its way.  (k may be written: all have read the last one's before
+    // a barrier in body.)
+    if (wave == 0) plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
+    lds_barrier();
     const int state = scalar(k.state), share = scalar(k.j);
     if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)share * a.c.Hkv + head] = k.cut;
     if (state == kNone) return;
@@ -842,8 +926,8 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
       unsigned char* V = smem + (2 + (i & 1)) * KT * RB;
 #pragma unroll
       for (int n = 0; n < S::NS; ++n) {
-        const uint32_t bad = w.not_finite(V, 32 * n);          // the same for all four waves
-        if (__builtin_expect(bad != 0, 0)) {
+        if (__builtin_expect(!w.finite(V, 32 * n), 0)) {       // the same for all four waves
+          const uint32_t bad = w.not_finite(V, 32 * n);
           w.add_rows(V, 32 * n, p[n], bad, key_first + i * KT + 32 * n, absent >> (2 * n));
           lds_barrier();
           w.clear_rows(V, 32 * n, bad);                        // all waves write the same zeros
@@ -1072,13 +1156,11 @@ void cache_attention_few_kernel(AttendArgs a) {
       w.l += Wave<T, D>::sum(p);
       if (next < te) wait_loads<NI>();               // the values: the next keys were issued after them
       else wait_loads<0>();
-      if (part) {
+      if (part && __builtin_expect(!w.finite(V, 0), 0)) {
         const uint32_t bad = w.not_finite(V, 0);
-        if (__builtin_expect(bad != 0, 0)) {
-          w.add_rows(V, 0, p, bad, key, absent);
-          w.clear_rows(V, 0, bad);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        }
+        w.add_rows(V, 0, p, bad, key, absent);
+        w.clear_rows(V, 0, bad);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       }
       w.add_values(V, 0, p);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
