@@ -844,7 +844,7 @@ __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j
     if (wave == 0) plan_piece<FEW>(work, j, first, (__attribute__((address_space(3))) Next*)&k);
     lds_barrier();
     const int state = scalar(k.state), share = scalar(k.j);
-    if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[(int64_t)share * a.c.Hkv + head] = k.cut;
+    if (first && share >= 0 && threadIdx.x == 0) static_cast<Cut*>(a.cuts)[head * a.shares + share] = k.cut;
     if (state == kNone) return;
     const Piece u{scalar(k.u.s), scalar(k.u.b), scalar(k.u.L), scalar(k.u.lens), scalar(k.u.tile), 0, scalar(k.u.length)};
     const int from = scalar(k.from), to = scalar(k.to);
@@ -1209,19 +1209,38 @@ void cache_attention_few_kernel(AttendArgs a) {
   });
 }
 
-// Joins the pieces of tiles that lie in several shares.  Its rows go round among gridDim.y workgroups; a thread has 4
-// columns of a row and every few pieces of it (a running maximum and sum over them), the groups of pieces are joined in
-// LDS, in their order.
+// Joins the pieces of tiles that lie in several shares.  Bound by latency: workgroups x / Hkv, of as many as there are
+// tiles at most, find their cut among those of all shares by one load a thread (a workgroup for each share instead, most
+// of them with nothing to do: 8.4 us for 13 tiles, 8 heads and 96 shares, so 4.5).  A tile's rows go round among gridDim.y
+// workgroups; a thread has 4 columns of a row and every few pieces of it (a running maximum and sum over them), the
+// groups of pieces are joined in LDS, in their order.
 constexpr int kJoinThreads = 1024;
+static_assert(kJoinThreads >= kMostShares, "a thread for each share");
 
 template <typename T, int D, int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(AttendArgs a) {
   constexpr int COLS = D / 4, AT_ONCE = 8;
   __shared__ float2 ml[kJoinThreads];
   __shared__ float4 sums[kJoinThreads];
-  const Cut cut = static_cast<const Cut*>(a.cuts)[blockIdx.x];
-  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), j = (int)(blockIdx.x / a.c.Hkv);
-  if (cut.end - cut.begin < 2) return;
+  __shared__ int cuts[kJoinThreads / 64], found;
+  const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv), mine_of_all = (int)(blockIdx.x / a.c.Hkv);
+  const Cut* all = static_cast<const Cut*>(a.cuts) + head * a.shares;
+  {
+    const int s = threadIdx.x, lane = s & 63, wave = s >> 6;
+    bool cut = false;
+    if (s < a.shares) cut = all[s].end - all[s].begin >= 2;
+    const uint64_t b = __ballot(cut);
+    if (lane == 0) cuts[wave] = __popcll(b);
+    if (s == 0) found = -1;
+    __syncthreads();
+    int rank = mine_of_all - __popcll(b & ((1ull << lane) - 1));
+    for (int w = 0; w < wave; ++w) rank -= cuts[w];
+    if (cut && rank == 0) found = s;
+    __syncthreads();
+  }
+  const int j = scalar(found);
+  if (j < 0) return;
+  const Cut cut = all[j];
   const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
   const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
   if (items <= 0) return;
@@ -1316,8 +1335,10 @@ static hipError_t launch_attend_d(const AttendArgs& a, hipStream_t s) {
   prof_end(K_ATTEND, s);
   if ((e = hipGetLastError()) != hipSuccess || a.shares < 2) return e;
   prof_begin(K_ATTEND_JOIN, s);
-  if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), dim3(shares, 4), dim3(kJoinThreads), 0, s, a);
-  else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), dim3(shares, 4), dim3(kJoinThreads), 0, s, a);
+  const unsigned cuts = std::min(shares, tiles);
+  const dim3 grid(cuts, std::max(1u, std::min(8u, 256 / cuts)));       // one workgroup a CU
+  if (a.few) hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kFewRows>), grid, dim3(kJoinThreads), 0, s, a);
+  else hipLaunchKernelGGL((cache_attention_join_kernel<T, D, kManyRows>), grid, dim3(kJoinThreads), 0, s, a);
   prof_end(K_ATTEND_JOIN, s);
   return hipGetLastError();
 }

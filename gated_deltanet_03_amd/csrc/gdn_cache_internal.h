@@ -48,7 +48,7 @@ struct AttendArgs {
   int32_t extra;         // what cutting tiles costs, in units of work
   float* part_o;         // [2 shares, Hkv, rows of a tile, d]
   float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
-  void* cuts;            // [shares, Hkv] of 16 bytes
+  void* cuts;            // [Hkv, shares] of 16 bytes
 };
 
 struct SelectArgs {
