@@ -82,6 +82,26 @@ __device__ __forceinline__ double wave_sum64(double v) {
 // Entries of a segment as keys: the logit's order, then the lower index first.
 __device__ __forceinline__ uint64_t entry_key(float x, int v) { return (uint64_t)ordered(x) << 32 | (uint32_t)~v; }
 
+__device__ __forceinline__ uint64_t lane_value64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// Entries of a list of n <= 64, by rank: body(rank, key, place) for the wave's share of them, every `waves`-th, a ballot
+// each (a loop over the list in every thread: 2.9 us for 30 entries, so 0.6).
+template <typename B>
+__device__ __forceinline__ void by_rank(const uint64_t* list, const uint32_t* from, int n, int wave, int waves, B&& body) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t k = lane < n ? list[lane] : 0;
+  const uint32_t f = from && lane < n ? from[lane] : 0;
+  for (int i = wave; i < n; i += waves) {
+    const uint64_t ki = lane_value64(k, i);
+    const uint32_t fi = (uint32_t)__builtin_amdgcn_readlane((int)f, i);
+    const int rank = __popcll(__ballot(k > ki || (k == ki && f > fi)));
+    if (lane == 0) body(rank, ki, fi);
+  }
+}
+
 // How many of a list's n entries come before one: larger keys, or equal ones with the larger place.
 template <bool PLACES>
 __device__ __forceinline__ int rank_of(const uint64_t* list, const uint32_t* from, int n, uint64_t k, uint32_t f) {
@@ -189,13 +209,19 @@ __global__ __launch_bounds__(kThreads, 8) void beam_part_kernel(SelectArgs p, in
   }
   const int n = wrong ? 0 : count;
   uint64_t* best = p.best + at * p.K;
+  if (n <= 64) {
+    by_rank(list, nullptr, n, wave, 4, [&](int rank, uint64_t k, uint32_t) {
+      if (rank < p.K) best[rank] = k;
+    });
+    if (tid >= n && tid < p.K) best[tid] = 0;
+    return;
+  }
   if (n <= kList) {
     for (int i = tid; i < n; i += kThreads) {
       const uint64_t k = list[i];
       const int rank = rank_of<false>(list, nullptr, n, k, 0);
       if (rank < p.K) best[rank] = k;
     }
-    if (tid >= n && tid < p.K) best[tid] = 0;
     return;
   }
   uint64_t last = ~0ull;                         // one maximum below the last one at a time, read again
@@ -289,7 +315,6 @@ __global__ __launch_bounds__(kJoin) void beam_join_kernel(SelectArgs p) {
     k = ordered64(s + ((double)unordered((uint32_t)(e >> 32)) - high[w]));
     f = (uint32_t)~((w << 24) | (int)~(uint32_t)e);   // token below 2^24, beam below 2^6: lower flat index, larger f
   };
-  // body(key, place) of every entry of this thread
   uint64_t hk[kHeld];
   uint32_t hf[kHeld];
 #pragma unroll
@@ -297,6 +322,7 @@ __global__ __launch_bounds__(kJoin) void beam_join_kernel(SelectArgs p) {
     hk[h] = 0, hf[h] = 0;
     if (tid + h * kJoin < all) candidate(tid + h * kJoin, held[h], hk[h], hf[h]);
   }
+  // body(key, place) of every entry of this thread
   auto each = [&](auto&& body) {
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) body(hk[h], hf[h]);
@@ -336,6 +362,13 @@ __global__ __launch_bounds__(kJoin) void beam_join_kernel(SelectArgs p) {
     p.new_scores[o] = k ? (float)unordered64(k) : -INFINITY;
     p.new_finished[o] = !k || done[w] || v == p.eos;
   };
+  if (n <= 64) {
+    by_rank(key, from, n, wave, kWaves, [&](int rank, uint64_t k, uint32_t f) {
+      if (rank < p.K) put(rank, k, f);
+    });
+    if (tid >= n && tid < p.K) put(tid, 0, ~0u);
+    return;
+  }
   if (n <= kList) {
     if (tid < n) {
       const uint64_t k = key[tid];
@@ -343,7 +376,6 @@ __global__ __launch_bounds__(kJoin) void beam_join_kernel(SelectArgs p) {
       const int rank = rank_of<true>(key, from, n, k, f);
       if (rank < p.K) put(rank, k, f);
     }
-    if (tid >= n && tid < p.K) put(tid, 0, ~0u);
     return;
   }
   uint64_t last = ~0ull;
