@@ -114,7 +114,10 @@ struct Plan {
   int64_t tiles;
 };
 
-// As many workgroups as the card holds at once share the work evenly; sequences that are sure to be short are not cut.
+// As many workgroups as the card holds at once share the work evenly.  Tables too narrow for sequences whose cutting
+// pays are not cut: then there is no join to launch (2.7 us, also where the kernel finds nothing to cut).  One token, 8
+// heads, whole and cut: fp32 of 64 200 keys 11.1 and 14.0 us, 300 keys 13.9 and 14.0, 500 keys 16.3 and 14.0; bf16 of 128
+// 300 keys 10.1 and 12.8, 500 keys 11.3 and 12.9, 1000 keys 16.8 and 13.2.
 Plan attention_plan(const gdn_cache_shape* sh, int64_t tokens, bool ragged) {
   const int64_t G = sh->Hq / sh->Hkv, rows = tokens * G;
   Plan p{};
@@ -122,7 +125,9 @@ Plan attention_plan(const gdn_cache_shape* sh, int64_t tokens, bool ragged) {
   p.rows = p.few ? kFewRows : kManyRows;
   p.tiles = ragged ? rows / p.rows + sh->N : sh->N * (((int64_t)sh->T * G + p.rows - 1) / p.rows);
   const int rb = sh->d * (int)elem_size(sh->dtype), at_once = 256 * (p.few ? few_waves(rb) : many_waves(rb));
-  if ((int64_t)sh->max_pages * sh->page_size > (p.few ? kFewKeys : kManyKeys))
+  const bool f32 = sh->dtype == GDN_F32;
+  if ((int64_t)sh->max_pages * sh->page_size > (p.few ? kFewKeys + (f32 ? 16384 : 49152) / sh->d
+                                                      : kManyKeys + (f32 ? 16384 : 81920) / sh->d))
     p.shares = std::max(1, std::min(kMostShares, at_once / sh->Hkv));
   // all tiles with all keys, twice that where they are drawn out, stay below 2^30 units
   const int64_t keys = (int64_t)sh->max_pages * sh->page_size + 64 + p.rows;
@@ -241,9 +246,9 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;
   a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles; a.unit = plan.unit;
-  // 16 us of many rows' keys, or 5 us of few rows' (a workgroup's rates beside the others')
-  const int32_t keys = (plan.few ? 1 : 2) * (sh->dtype == GDN_F32 ? 8192 : 40960) / sh->d;
-  a.extra = keys >> plan.unit;
+  // 16 us of many rows' keys, or 3 us of few rows' (a workgroup's rates beside the others')
+  const bool f32 = sh->dtype == GDN_F32;
+  a.extra = ((plan.few ? (f32 ? 8192 : 28672) : (f32 ? 16384 : 81920)) / sh->d) >> plan.unit;
   if (need > 0) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + part_rows(sh, plan) * sh->d;

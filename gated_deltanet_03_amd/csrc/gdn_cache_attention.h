@@ -120,7 +120,7 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 //
 // Nothing is cut where that would end no later: the longest tile, and with more tiles than shares half of it above an even
 // share, against an even share and `extra`, what the pieces and their join cost (measured with 512 tiles of 128 rows or
-// fewer: about 16 us with many rows, 5 us with few).
+// fewer: about 16 us with many rows, 3 us with few).
 //
 // Many rows: workgroups that walk one head's keys side by side read them from the cache they share, and pieces that
 // begin anywhere do not (16384 keys of 8 heads, 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole
