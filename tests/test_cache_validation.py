@@ -97,10 +97,13 @@ def test_attention_refusals(lib):
                      (dict(stride=512), "stride"), (dict(q=NULL), "q is NULL"), (dict(o=NULL), "o is NULL"),
                      (dict(kc=NULL), "k_cache"), (dict(table=NULL), "block_table"), (dict(lens=NULL), "cache_lens"),
                      (dict(o=ctypes.c_void_p(0x200000008)), "aligned"), (dict(o=at(0)), "overlaps"),
-                     (dict(o=at(8)), "overlaps"), (dict(ws=NULL), "workspace"), (dict(n=64), "workspace"),
-                     (dict(ws=ctypes.c_void_p(0x200000008)), "aligned"), (dict(ws=at(7)), "overlaps"),
-                     (dict(ws=at(6)), "overlaps")):
+                     (dict(o=at(8)), "overlaps")):
         assert attend(lib, **kw) == INVALID and word in last(lib), (kw, last(lib))
+    wide = cache(max_pages=100)               # sequences that may be cut: a workspace
+    assert gdn.gdn_cache_attention_workspace_bytes(wide, False) > 64
+    for kw, word in ((dict(ws=NULL), "workspace"), (dict(n=64), "workspace"), (dict(ws=at(6)), "overlaps"),
+                     (dict(ws=ctypes.c_void_p(0x200000008)), "aligned"), (dict(ws=at(7)), "overlaps")):
+        assert attend(lib, wide, **kw) == INVALID and word in last(lib), (kw, last(lib))
     assert attend(lib, cache(N=0)) == OK and attend(lib, cache(T=0)) == OK
     assert gdn.gdn_cache_attention_workspace_bytes(cache(N=0), False) == 0
     assert gdn.gdn_cache_attention_workspace_bytes(cache(max_pages=1), False) == 0      # one page: nothing to split
