@@ -1014,8 +1014,8 @@ def gdn_cache_attention(q, k_cache, v_cache, block_table, cache_lens, *, cu_seql
         _need(workspace, "workspace", None, dev)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch(dev, lib.gdn_cache_attention, ref, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
-            block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else float(scale),
-            window, o.data_ptr(), _addr(workspace), nbytes)
+            block_table.data_ptr(), cache_lens.data_ptr(), _addr(cu_seqlens),
+            d ** -0.5 if scale is None else float(scale), window, o.data_ptr(), _addr(workspace), nbytes)
     return o
 
 

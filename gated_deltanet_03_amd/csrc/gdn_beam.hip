@@ -12,6 +12,9 @@
 // entry's rank is the number of entries before it.  Lists that do not fit (very many equal entries) are taken one
 // maximum at a time.
 //
+// 16 searches of 8 beams over 131072 tokens, bf16: 16.2 us (the logits alone 6.6 us; by count vector operations, 10 an
+// entry, are as long again) and 6.9 us for the join, a chain of latencies; 4 beams over 32003, fp32: 3.8 and 5.1 us.
+//
 // Sums of exponentials: the difference to the maximum first, so that the exponent's rounding is small where terms are
 // large; eight terms a thread in fp32, those in 64 bits.
 #include <algorithm>
@@ -75,8 +78,8 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 
 __device__ __forceinline__ double wave_sum64(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, wave_scan64(v));
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(u >> 32), 63);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 | lo);
 }
 
 // Entries of a segment as keys: the logit's order, then the lower index first.
@@ -90,7 +93,8 @@ __device__ __forceinline__ uint64_t lane_value64(uint64_t v, int lane) {
 // Entries of a list of n <= 64, by rank: body(rank, key, place) for the wave's share of them, every `waves`-th, a ballot
 // each (a loop over the list in every thread: 2.9 us for 30 entries, so 0.6).
 template <typename B>
-__device__ __forceinline__ void by_rank(const uint64_t* list, const uint32_t* from, int n, int wave, int waves, B&& body) {
+__device__ __forceinline__ void by_rank(const uint64_t* list, const uint32_t* from, int n, int wave, int waves,
+                                        B&& body) {
   const int lane = threadIdx.x & 63;
   const uint64_t k = lane < n ? list[lane] : 0;
   const uint32_t f = from && lane < n ? from[lane] : 0;

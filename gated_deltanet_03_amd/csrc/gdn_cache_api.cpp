@@ -59,7 +59,8 @@ gdn_status check_cache(const gdn_cache_shape* sh, bool ragged, int64_t* tokens) 
     return fail(GDN_ERR_UNSUPPORTED, "N=%d exceeds 2^20, Hq=%d 65535 or Hq/Hkv 256", sh->N, sh->Hq);
   *tokens = ragged ? (int64_t)sh->T : (int64_t)sh->N * sh->T;
   if (*tokens > (1LL << 30) || *tokens * sh->Hq > 0x7fffffffLL)
-    return fail(GDN_ERR_UNSUPPORTED, "%lld tokens of %d heads exceed 2^30 tokens or 2^31-1 rows", (long long)*tokens, sh->Hq);
+    return fail(GDN_ERR_UNSUPPORTED, "%lld tokens of %d heads exceed 2^30 tokens or 2^31-1 rows", (long long)*tokens,
+                sh->Hq);
   return GDN_OK;
 }
 

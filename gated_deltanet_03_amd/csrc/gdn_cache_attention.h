@@ -112,26 +112,26 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 
 // How the work of one head is laid out.
 //
-// The tiles of all sequences lie on one line, a tile about as long as the keys it sees and what starting one costs, in
-// units of 2^unit keys that the host chooses so that the line is shorter than 2^30: v_i = first + step * i for tile i
-// of a sequence.  The first workgroups take whole tiles, one each; what is left of the line is cut into `shares` even
-// pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one more.  Pieces that
-// are not whole tiles go to the workspace and are joined.
+// The tiles of all sequences lie on one line, a tile about as long as the keys it sees and what starting one costs,
+// in units of 2^unit keys that the host chooses so that the line is shorter than 2^30: v_i = first + step * i for
+// tile i of a sequence. The first workgroups take whole tiles, one each; what is left of the line is cut into
+// `shares` even pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one
+// more. Pieces that are not whole tiles go to the workspace and are joined.
 //
-// Nothing is cut where that would end no later: the longest tile, and with more tiles than shares half of it above an even
-// share, against an even share and `extra`, what the pieces and their join cost (measured with 512 tiles of 128 rows or
-// fewer: about 16 us with many rows, 3 us with few).
+// Nothing is cut where that would end no later: the longest tile, and with more tiles than shares half of it above an
+// even share, against an even share and `extra`, what the pieces and their join cost (measured with 512 tiles of 128
+// rows or fewer: about 16 us with many rows, 3 us with few).
 //
 // Many rows: workgroups that walk one head's keys side by side read them from the cache they share, and pieces that
-// begin anywhere do not (16384 keys of 8 heads, 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole).  So whole
-// rounds of `shares` tiles stay whole, the last ones of a sequence, which see the most keys, first; with three rounds or
-// more nothing is cut.  Tiles longer than 5/4 of an even share are always cut, so that one long sequence does not
+// begin anywhere do not (16384 keys of 8 heads, 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole). So whole
+// rounds of `shares` tiles stay whole, the last ones of a sequence, which see the most keys, first; with three rounds
+// or more nothing is cut. Tiles longer than 5/4 of an even share are always cut, so that one long sequence does not
 // outlast all others.
 //
-// Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one
-// piece, and a second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares.  A share is
-// a multiple `run` of the step there, so that tile i has ceil((ceil(first / step) + i) / run) of them, whose sum and its inverse
-// have a closed form.
+// Where shares are many times the tiles, tiles are drawn out to whole numbers of shares: a share is then one piece,
+// and a second one's start (plan, page numbers, first loads: 6 us) costs more than the longer shares. A share is a
+// multiple `run` of the step there, so that tile i has ceil((ceil(first / step) + i) / run) of them, whose sum and
+// its inverse have a closed form.
 //
 // Borders between shares that come within a 16th of a share of a tile's end are moved there.
 struct Piece {
@@ -642,8 +642,8 @@ struct Pages {
   uint64_t none;  // lanes without a page
 };
 
-template <typename A>
-__device__ __forceinline__ void load_pages(const A& a, const int32_t* __restrict__ table, int head, int g0, int lane, Pages& p) {
+__device__ __forceinline__ void load_pages(const AttendArgs& a, const int32_t* __restrict__ table, int head, int g0,
+                                           int lane, Pages& p) {
   const int g = g0 + lane;
   // g * (ceil(2^32 / n)) >> 32 = g / n: the error g (n - 1) / (n 2^32) is below 1 / n for g < 2^32 / n
   const int page = (int)(((uint64_t)(uint32_t)g * a.granule_magic) >> 32), sub = g - page * a.granules;
@@ -863,6 +863,11 @@ __device__ __forceinline__ void part_blocks(int n, const Piece& u, int from, int
 // Many rows: four waves of 32 rows, the same keys, in blocks of KT of them.  Keys and values have two buffers each; a
 // block's loads are issued one block ahead.  The one barrier a block says that its loads have landed and that nobody
 // reads the buffers that the next ones go to.
+//
+// Bound by the matrix unit and the vector unit's exponentials in turn: 44 and 42% busy with heads of 128, LDS 22% and
+// free of conflicts.  2048 new tokens over 16384 keys, bf16: 32 heads of 128 522 us (987 TFLOP/s; a large matrix product
+// has 1221), of 64 352 us (730, as many exponentials for half the products), 16 heads of 256 580 us (888); 1024 over
+// 4096 fp32, 32 heads of 128 556 us (108 of 138).
 //
 // Where the registers leave one wave a SIMD (D = 256, fp32 from D = 128 on), nothing fills the matrix unit while that wave
 // makes weights: keys are loaded two blocks ahead and multiplied one block ahead, in turn with the exponentials of the
@@ -1099,7 +1104,9 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
 }
 
 // Few rows: one tile of 32 rows, each wave on its own 32 keys at a time with its own piece of LDS and no barrier: once
-// a tile's keys have been read the next ones are on their way, once its values have been read the next values.
+// a tile's keys have been read the next ones are on their way, once its values have been read the next values.  Bound by
+// reading the cache: one token over 131001 keys of 2 heads of 256, bf16, 54 us (4.9 TB/s), 32 tokens over 600 to 32011
+// keys of 8 heads of 128 98 us (5.2).  Short ones by latency: 3 us until the work is found, 3 us to the first keys.
 template <typename T, int D>
 __global__ __launch_bounds__((64 * few_group(D * (int)sizeof(T))), (few_waves(D * (int)sizeof(T))))
 void cache_attention_few_kernel(AttendArgs a) {
@@ -1211,9 +1218,9 @@ void cache_attention_few_kernel(AttendArgs a) {
 
 // Joins the pieces of tiles that lie in several shares.  Bound by latency: workgroups x / Hkv, of as many as there are
 // tiles at most, find their cut among those of all shares by one load a thread (a workgroup for each share instead, most
-// of them with nothing to do: 8.4 us for 13 tiles, 8 heads and 96 shares, so 4.5).  A tile's rows go round among gridDim.y
-// workgroups; a thread has 4 columns of a row and every few pieces of it (a running maximum and sum over them), the
-// groups of pieces are joined in LDS, in their order.
+// of them with nothing to do: 8.4 us for 13 tiles, 8 heads and 96 shares, so 4.5).  A tile's rows go round among
+// gridDim.y workgroups; a thread has 4 columns of a row and every few pieces of it (a running maximum and sum over them),
+// the groups of pieces are joined in LDS, in their order.  2 tiles of 128 pieces of 8 rows of 256: 6.4 us.
 constexpr int kJoinThreads = 1024;
 static_assert(kJoinThreads >= kMostShares, "a thread for each share");
 
@@ -1244,7 +1251,8 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
   const int row0 = cut.tile * ROWS, rows = min(ROWS, cut.L * G - row0), turn = (int)gridDim.y;
   const int mine = (rows - (int)blockIdx.y + turn - 1) / turn, items = mine * COLS;
   if (items <= 0) return;
-  const int groups = max(1, min(kJoinThreads / items, (cut.end - cut.begin + AT_ONCE - 1) / AT_ONCE)), group = threadIdx.x / items;
+  const int groups = max(1, min(kJoinThreads / items, (cut.end - cut.begin + AT_ONCE - 1) / AT_ONCE));
+  const int group = threadIdx.x / items;
   for (int base = 0; base < items; base += kJoinThreads) {      // more than once only with one group
     const int item = base + (groups > 1 ? (int)threadIdx.x - group * items : (int)threadIdx.x);
     const bool on = groups > 1 ? group < groups : item < items;

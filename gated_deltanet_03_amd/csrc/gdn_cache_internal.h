@@ -79,8 +79,8 @@ struct ReorderArgs {
 };
 
 // Sizes that the host's plan and the attention's kernels share: rows of a tile, the fewest keys of a share of few and of
-// many rows, and by the
-// bytes of one key (rb) the keys of a tile, waves of a workgroup, LDS and waves a SIMD (one workgroup each).
+// many rows, the most shares, and by the bytes of one key (rb) the keys of a block, LDS, waves of a workgroup and waves
+// a SIMD, which is workgroups a CU.
 constexpr int32_t kFewRows = 32, kManyRows = 128;
 constexpr int32_t kFewKeys = 128, kManyKeys = 128, kMostShares = 1024;
 constexpr int many_keys(int rb) { return rb >= 1024 ? 32 : 64; }
