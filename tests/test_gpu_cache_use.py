@@ -185,3 +185,39 @@ def test_profile_names(gdn):
     assert {k: n for k, (n, _) in gdn.gdn_profile_collect().items()} == {
         "cache_append_kernel": 1, "cache_attention_kernel": 2, "cache_attention_join_kernel": 2, "beam_part_kernel": 1,
         "beam_join_kernel": 1, "state_reorder_kernel": 2}
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_nothing_there(gdn, new):
+    """Tables without columns, caches without pages, no sequences, no tokens."""
+    q, k = torch.randn(2, new, 4, 64, device=DEV), torch.randn(2, new, 2, 64, device=DEV)
+    kc, none = torch.randn(3, 2, 16, 64, device=DEV), torch.empty(0, 2, 16, 64, device=DEV)
+    lens, inv = torch.tensor([new, new + 5], dtype=I32, device=DEV), torch.ones(32, device=DEV)
+    tables = torch.empty(2, 0, dtype=I32, device=DEV), torch.zeros(2, 30, dtype=I32, device=DEV)
+    for cache, table in ((kc, tables[0]), (none, tables[0]), (none, tables[1])):
+        other, was = cache.clone(), cache.clone()
+        turned = gdn.gdn_cache_append(k, k, cache, other, table, lens, q=q, inv_freq=inv)
+        assert not torch.equal(turned[1], q[1])                    # queries are turned all the same
+        assert torch.equal(cache, was) and torch.equal(other, was)
+        o = gdn.gdn_cache_attention(q, cache, other, table, lens)
+        assert not o.any()
+    for N, L in ((0, 3), (2, 0)):
+        t, n = torch.zeros(N, 4, dtype=I32, device=DEV), torch.ones(N, dtype=I32, device=DEV)
+        x, y = torch.empty(N, L, 4, 64, device=DEV), torch.empty(N, L, 2, 64, device=DEV)
+        assert gdn.gdn_cache_attention(x, kc, kc.clone(), t, n).shape == x.shape
+        assert gdn.gdn_cache_append(y, y, kc, kc.clone(), t, n, q=x, inv_freq=inv).shape == x.shape
+    one, ones = torch.ones(0, 3, device=DEV), torch.ones(0, 3, 10, device=DEV)
+    assert [t.shape for t in gdn.gdn_beam_select(ones, one, beams=5)] == [(0, 5)] * 4
+    assert gdn.gdn_state_reorder(torch.ones(0, 8, device=DEV), torch.zeros(0, 4, dtype=I32, device=DEV)).shape == (0, 8)
+
+
+def test_pages_of_caches_in_either_order(gdn):
+    both = torch.randn(2, 9, 2, 16, 64, device=DEV)
+    src = torch.tensor([[0, 0, 1], [4, -1, 3]], dtype=I32, device=DEV)
+    dst = torch.tensor([[1, 2, 0], [5, 6, 4]], dtype=I32, device=DEV)
+    want = both.clone()
+    want[:, [1, 2, 0, 5, 4]] = both[:, [0, 0, 1, 4, 3]]
+    for a, b in ((0, 1), (1, 0)):
+        moved = both.clone()
+        gdn.gdn_cache_copy_pages(moved[a], moved[b], src, dst)
+        assert torch.equal(moved, want)
