@@ -50,7 +50,21 @@ def draw(rng):
 
 @pytest.mark.parametrize("seed", range(60))
 def test_every_key_counts_once(gdn, seed):
-    c = draw(random.Random(seed))
+    count(gdn, draw(random.Random(seed)))
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_tables_of_the_widest(gdn, seed):
+    """Tables for 2^26 keys a sequence: work is cut in units of many keys, so that its sum stays below 2^30."""
+    rng = random.Random(1000 + seed)
+    c = draw(rng)
+    while c["Hkv"] * c["d"] > 1024:
+        c["Hkv"], c["d"] = max(c["Hkv"] // 2, 1), max(c["d"] // 2, 32)
+    most = rng.choice([1, 3, 40])
+    count(gdn, dict(c, new=c["new"][:most], ctx=[min(n, 9000) for n in c["ctx"][:most]], page=1024, spare=65536 - 9))
+
+
+def count(gdn, c):
     new, ctx, Hkv, G, d, page = c["new"], c["ctx"], c["Hkv"], c["G"], c["d"], c["page"]
     say(f"cut {c}")
     need = [-(-n // page) for n in ctx]
