@@ -247,9 +247,11 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;
   a.few = plan.few; a.shares = plan.shares; a.tiles = (int32_t)plan.tiles; a.unit = plan.unit;
-  // 16 us of many rows' keys, or 3 us of few rows' (a workgroup's rates beside the others')
+  // at a workgroup's rates beside the others': 3 us of few rows' keys; 16 us of many rows' keys, or 40 us where most tiles
+  // are cut and written in pieces
   const bool f32 = sh->dtype == GDN_F32;
-  a.extra = ((plan.few ? (f32 ? 8192 : 28672) : (f32 ? 16384 : 81920)) / sh->d) >> plan.unit;
+  a.extra_drawn = ((plan.few ? (f32 ? 8192 : 28672) : (f32 ? 16384 : 81920)) / sh->d) >> plan.unit;
+  a.extra_even = plan.few ? a.extra_drawn : (f32 ? 256 : sh->d <= 64 ? 1920 : 1280) >> plan.unit;
   if (need > 0) {
     a.part_o = static_cast<float*>(ws);
     a.part_ml = a.part_o + part_rows(sh, plan) * sh->d;

@@ -118,9 +118,13 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 // `shares` even pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one
 // more. Pieces that are not whole tiles go to the workspace and are joined.
 //
-// Nothing is cut where that would end no later: the longest tile, and with more tiles than shares half of it above an
-// even share, against an even share and `extra`, what the pieces and their join cost (measured with 512 tiles of 128
-// rows or fewer: about 16 us with many rows, 3 us with few).
+// Nothing is cut where that would end no later.  Whole tiles end with the longest one, or with as many rounds as
+// there are tiles for a share, of average ones; cut ones with an even share and what the pieces and their join cost:
+// 3 us with few rows, 16 us with many where a share is one piece, else 40 us (128 rows of 128 in fp32 are 64 KB,
+// written and read again by every share).  Few rows wait for memory, which fewer workgroups than fit keep busy too:
+// there only the longest tile counts (256 tokens over 100 to 1103 keys of 8 heads of 128, bf16: 145 us cut, 121
+// whole).  A prompt of 2000 tokens, 32 on 8 heads of 128, bf16: 94 us cut, 68 whole; 1000 tokens over 4000 keys: 94
+// us cut, 108 whole; 4000 over 8000: 432 cut, 408 whole.
 //
 // Many rows: workgroups that walk one head's keys side by side read them from the cache they share, and pieces that
 // begin anywhere do not (16384 keys of 8 heads, 512 tiles of 128 rows, bf16: 677 us cut evenly, 563 whole). So whole
@@ -151,7 +155,7 @@ struct Shares {
 struct Work {
   const int32_t* cu;
   const int32_t* lens;
-  int N, T, total, G, room, window, tiles, shares, unit, extra;
+  int N, T, total, G, room, window, tiles, shares, unit, extra_drawn, extra_even;
 };
 
 template <bool FEW>
@@ -245,7 +249,22 @@ struct Line {
     const int even = up(all, a.shares), least = max((FEW ? kFewKeys : kManyKeys) >> a.unit, 1);
     r.rest = all;
     r.share = max(least, even);
-    const bool none = count <= a.shares ? longest <= r.share + a.extra : !FEW && longest / 2 <= a.extra;
+    const bool drawn = count * 4 <= a.shares;
+    const int extra = drawn ? a.extra_drawn : a.extra_even;
+    bool none = longest <= r.share + extra;
+    if constexpr (!FEW) {
+      if (none && count > a.shares) {       // whole tiles take rounds of average ones, or end with short ones
+        const int rounds = quotient_up(count, a.shares);
+        if (up(all, count) * rounds > even + extra) {
+          int brief = 0;
+          for (int s = 0; s < a.N; s += 64) {
+            load(s);
+            brief += wave_sum(first > extra ? 0 : step > 0 ? min((extra - first) / step + 1, tiles) : tiles);
+          }
+          none = brief >= count - (rounds - 1) * a.shares;
+        }
+      }
+    }
     if constexpr (FEW) {
       if (none) {
         r.longest = longest;
@@ -253,7 +272,7 @@ struct Line {
         r.rest = 0;
       }
     }
-    if (!none && count * 4 <= a.shares) {
+    if (!none && drawn) {
       // a tile has at most (its length + a step) / share + 1 shares
       const int steps = max((ROWS / a.G + 1) >> a.unit, 1);
       r.drawn = up(max(least, up(all + count * steps, a.shares - count)), steps);
@@ -767,7 +786,8 @@ __device__ __attribute__((noinline)) void plan_piece(Work w, int j, bool first,
     return reinterpret_cast<const int32_t*>((uint64_t)(uint32_t)scalar((int)(x >> 32)) << 32 | (uint32_t)scalar((int)x));
   };
   const Work a{address(cu), address(lens), scalar(w.N), scalar(w.T), scalar(w.total), scalar(w.G), scalar(w.room),
-               scalar(w.window), scalar(w.tiles), scalar(w.shares), scalar(w.unit), scalar(w.extra)};
+               scalar(w.window), scalar(w.tiles), scalar(w.shares), scalar(w.unit), scalar(w.extra_drawn),
+               scalar(w.extra_even)};
   j = scalar(j);
   first = scalar(first) != 0;
   Line<FEW> line(a);
@@ -797,8 +817,8 @@ __device__ __attribute__((noinline)) void plan_piece(Work w, int j, bool first,
   Cut cut{0, 0, 0, 0, 0};
   if (tile) {
     if (line.template find<true>(sh, j, u)) state = kTile;
-    // of few rows there are no workgroups behind the shares: the cuts of the last ones, none, are written here
-    j = FEW && a.shares ? a.shares - sh.whole + j : -1;
+    // where there are no workgroups behind the shares, the cuts of the last ones, none, are written here
+    j = FEW && a.tiles <= a.shares ? a.shares - sh.whole + j : -1;
   } else {
     while (pos < end && line.template find<false>(sh, pos, u)) {
       from = pos - u.at;
@@ -837,7 +857,7 @@ __device__ __forceinline__ void walk(const AttendArgs& a, int G, int head, int j
   __shared__ Next k;
   const int wave = scalar(threadIdx.x >> 6);
   const Work work{a.c.cu, a.c.lens, a.c.N, a.c.T, a.c.total, G, a.c.max_pages * a.c.page_size, a.window, a.tiles, a.shares,
-                  a.unit, a.extra};
+                  a.unit, a.extra_drawn, a.extra_even};
   for (bool first = true;; first = false) {
     // One wave for all: the others would only get in its way.  (k may be written: all have read the last one's before
     // a barrier in body.)
@@ -1326,9 +1346,9 @@ static hipError_t allow_lds(K kernel, int bytes) {
 template <typename T, int D>
 static hipError_t launch_attend_d(const AttendArgs& a, hipStream_t s) {
   constexpr int RB = D * (int)sizeof(T);
-  // few rows: shares alone; many rows: some tiles are taken whole before them
+  // few rows and no more tiles: shares alone; else some tiles or all are taken whole before them
   const unsigned shares = (unsigned)((int64_t)a.shares * a.c.Hkv), tiles = (unsigned)((int64_t)a.tiles * a.c.Hkv);
-  const unsigned wgs = a.shares && a.few ? shares : tiles + shares;
+  const unsigned wgs = a.few && a.tiles <= a.shares ? shares : tiles + shares;
   prof_begin(K_ATTEND, s);
   hipError_t e;
   if (a.few) {

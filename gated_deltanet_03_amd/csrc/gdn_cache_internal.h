@@ -45,7 +45,8 @@ struct AttendArgs {
   int32_t shares;        // even shares of a head's work, 0: a tile for each workgroup
   int32_t tiles;         // upper bound on a head's tiles
   int32_t unit;          // log2 of the keys of a unit of work
-  int32_t extra;         // what cutting tiles costs, in units of work
+  int32_t extra_drawn;   // what cutting costs, in units of work: where a share is one piece,
+  int32_t extra_even;    // and where it is the end of one tile and the beginning of another
   float* part_o;         // [2 shares, Hkv, rows of a tile, d]
   float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
   void* cuts;            // [Hkv, shares] of 16 bytes
