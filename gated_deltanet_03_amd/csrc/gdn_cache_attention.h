@@ -467,20 +467,25 @@ struct Wave {
     }
   }
 
-  // The running maximum takes `top` (of this lane's keys) in.
+  // The running maximum takes `top` (of this lane's keys) in.  Weights are taken against m * scale as rounded, so the
+  // factors between maxima are too (contracted, or of (m - n) * scale, they would be off by 2^-24 of the maximum itself).
   __device__ __forceinline__ void raise(float top, float c, float slack) {
+#pragma clang fp contract(off)
     top = other_half_max(top);
     if (__ballot(top > m + slack || (m == -INFINITY && top > m)) == 0) return;
-    const float n = fmaxf(m, top);
-    const float f = n == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - n) * c);
+    const float n = fmaxf(m, top), nc = n * c;
+    const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mc - nc);
     m = n;
-    mc = n == -INFINITY ? 0.f : n * c;
+    mc = n == -INFINITY ? 0.f : nc;
     l *= f;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[t][i] *= f;
   }
+
+  // What the weights were taken against, -infinity without a key.
+  __device__ __forceinline__ float against() const { return m == -INFINITY ? -INFINITY : mc; }
 
   // Weights of 32 keys as operands: fp32, or rounded to T.
   struct Weights {
@@ -1118,7 +1123,7 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           store4<float>(o + 32 * k + 8 * j + 4 * h, w.o[k][4 * j], w.o[k][4 * j + 1], w.o[k][4 * j + 2], w.o[k][4 * j + 3]);
-      if (h == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(w.m, l);
+      if (h == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(w.against(), l);
     }
   });
 }
@@ -1196,7 +1201,7 @@ void cache_attention_few_kernel(AttendArgs a) {
     // join the waves: everyone's accumulators in LDS (pieces of 16 bytes at piece ^ row % 8)
     const float l = other_half_sum(w.l);
     const int h = lane >> 5, row = lane & 31;
-    if (h == 0) ml[wave][row] = make_float2(w.m, l);
+    if (h == 0) ml[wave][row] = make_float2(w.against(), l);
     __syncthreads();                                 // and nobody reads keys or values any more
     float4* O = reinterpret_cast<float4*>(smem);
 #pragma unroll
@@ -1218,7 +1223,7 @@ void cache_attention_few_kernel(AttendArgs a) {
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
         const float2 x = ml[v][r];
-        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * c);
+        const float f = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - m);
         const float4 p = O[(v * 32 + r) * (D / 4) + (piece ^ (r & 7))];
         sum.x += f * p.x, sum.y += f * p.y, sum.z += f * p.z, sum.w += f * p.w;
         tot += f * x.y;
@@ -1300,13 +1305,13 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) top = fmaxf(top, x[i].x);
-        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale_log2);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
         sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
         l *= f;
         m = top;
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-          const float w = x[i].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x[i].x - m) * a.scale_log2);
+          const float w = x[i].x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x[i].x - m);
           sum.x += w * p[i].x, sum.y += w * p[i].y, sum.z += w * p[i].z, sum.w += w * p[i].w;
           l += w * x[i].y;
         }
@@ -1323,7 +1328,7 @@ __global__ __launch_bounds__(kJoinThreads) void cache_attention_join_kernel(Atte
       for (int g = 0; g < groups; ++g) {
         const float2 x = ml[g * items + item];
         const float4 p = sums[g * items + item];
-        const float w = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * a.scale_log2);
+        const float w = x.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(x.x - m);
         sum.x += w * p.x, sum.y += w * p.y, sum.z += w * p.z, sum.w += w * p.w;
         l += w * x.y;
       }

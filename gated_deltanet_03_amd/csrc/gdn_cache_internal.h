@@ -48,7 +48,7 @@ struct AttendArgs {
   int32_t extra_drawn;   // what cutting costs, in units of work: where a share is one piece,
   int32_t extra_even;    // and where it is the end of one tile and the beginning of another
   float* part_o;         // [2 shares, Hkv, rows of a tile, d]
-  float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]
+  float* part_ml;        // [2 shares, Hkv, rows of a tile, 2]: what the weights were taken against, their sum
   void* cuts;            // [Hkv, shares] of 16 bytes
 };
 
