@@ -1094,10 +1094,8 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
         }
       };
       for (int i = tb; i + 1 < te; ++i) {
-        if (i > tb) {
-          wait_loads<0>();
-          lds_barrier();
-        }
+        if (i > tb) wait_loads<0>();
+        lds_barrier();                               // (at first: all have read block tb's keys, the next go there)
         int then = 0;
         if (i + 2 < te) then = stage_keys(i + 2);
         stage_values(i + 1);
