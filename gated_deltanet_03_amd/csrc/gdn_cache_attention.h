@@ -718,10 +718,12 @@ struct Stage {
 #pragma unroll
     for (int g = 0; g < NR / GR; ++g) {
       const int at = key + g * 16;
-      const int row = __builtin_amdgcn_readlane(pg.row, ((at >> 4) - pg.first) & 63) + (GR < 16 ? at & 15 : 0);
+      const int granule = __builtin_amdgcn_readlane(pg.row, ((at >> 4) - pg.first) & 63);
+      const bool there = granule >= 0;
+      const int row = granule + (GR < 16 ? at & 15 : 0);     // (of no page: no row, whatever is added)
       const char* base = static_cast<const char*>(cache) + (int64_t)row * RB;
       const uint32_t to = lds + (uint32_t)(g * 16 * RB);
-      if (row >= 0 && at >= beg && at + GR <= end) {
+      if (there && at >= beg && at + GR <= end) {
 #pragma unroll
         for (int n = 0; n < GR / RPI; ++n)
           dma16((place ^ (uint32_t)(swizzle(n * RPI) << 4)) + n * 1024, base, to + n * 1024);
@@ -730,7 +732,7 @@ struct Stage {
         for (int n = 0; n < GR / RPI; ++n) {
           const int k = at + n * RPI + lane / PPR;
           const char* src = base + (place ^ (uint32_t)(swizzle(n * RPI) << 4)) + n * 1024;
-          dma16(row >= 0 && k >= beg && k < end ? static_cast<const void*>(src) : static_cast<const void*>(zeros16),
+          dma16(there && k >= beg && k < end ? static_cast<const void*>(src) : static_cast<const void*>(zeros16),
                 to + n * 1024);
         }
       }

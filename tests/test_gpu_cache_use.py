@@ -221,3 +221,19 @@ def test_pages_of_caches_in_either_order(gdn):
         moved = both.clone()
         gdn.gdn_cache_copy_pages(moved[a], moved[b], src, dst)
         assert torch.equal(moved, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("new", [1, 60, 300])
+def test_keys_on_no_page_are_not_read(gdn, new, d, dtype):
+    """Keys that the lengths promise, in a cache without pages and on numbers that are no page: no memory is behind them."""
+    q = torch.randn(2, new, 4, d, device=DEV).to(dtype)
+    lens = torch.tensor([new + 500, 900], dtype=I32, device=DEV)
+    none, other = torch.empty(0, 2, 16, d, dtype=dtype, device=DEV), torch.empty(0, 2, 16, d, dtype=dtype, device=DEV)
+    for number in (0, -1, 7):
+        table = torch.full((2, 60), number, dtype=I32, device=DEV)
+        assert not gdn.gdn_cache_attention(q, none, other, table, lens).any()
+    bad = torch.full((1, 2, 16, d), float("nan"), dtype=dtype, device=DEV)
+    table = torch.full((2, 60), -1, dtype=I32, device=DEV)
+    assert not gdn.gdn_cache_attention(q, bad, bad.clone(), table, lens).any()
