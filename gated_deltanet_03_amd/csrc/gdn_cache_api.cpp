@@ -130,7 +130,7 @@ Plan attention_plan(const gdn_cache_shape* sh, int64_t tokens, bool ragged) {
   if ((int64_t)sh->max_pages * sh->page_size > (p.few ? kFewKeys + (f32 ? 16384 : 49152) / sh->d
                                                       : kManyKeys + (f32 ? 16384 : 81920) / sh->d))
     p.shares = std::max(1, std::min(kMostShares, at_once / sh->Hkv));
-  // all tiles with all keys, twice that where they are drawn out, stay below 2^30 units
+  // all tiles with twice the table's keys, and twice that where they are drawn out, stay below 2^30 units
   const int64_t keys = (int64_t)sh->max_pages * sh->page_size + 64 + p.rows;
   while (((p.tiles + sh->N) * ((keys >> p.unit) + 2)) > (1LL << 28)) ++p.unit;
   return p;

@@ -114,7 +114,7 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 //
 // The tiles of all sequences lie on one line, a tile about as long as the keys it sees and what starting one costs,
 // in units of 2^unit keys that the host chooses so that the line is shorter than 2^30: v_i = first + step * i for
-// tile i of a sequence. The first workgroups take whole tiles, one each; what is left of the line is cut into
+// tile i of a sequence, never more than twice the table's keys. The first workgroups take whole tiles, one each; what is left of the line is cut into
 // `shares` even pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one
 // more. Pieces that are not whole tiles go to the workspace and are joined.
 //
@@ -183,6 +183,10 @@ struct Line {
       const bool inside = a.window > 0 && a.window < old;
       first = (((inside ? a.window : old) + 64 + more) >> a.unit) + 1;
       step = inside ? 0 : more >> a.unit;
+      // No tile sees more keys than the table has; `step`, rounded up, goes beyond that by itself (at most twice as far
+      // in 128 rows), and new tokens behind the table's end without a limit: then all tiles count as the table.
+      const int most = ((a.room + 64 + more) >> a.unit) + 1;
+      if (first + (int64_t)step * (tiles - 1) > 2 * most) first = most, step = 0;
     }
   }
 

@@ -97,3 +97,34 @@ def count(gdn, c):
     off = ((got - want).abs() / want.clamp(min=1)).amax() if len(q) else 0.0
     assert not torch.isnan(o).any() and float(off) <= 3 * 2.0 ** -24, (float(off), c)
     assert not o[..., 32:].any()
+
+
+@pytest.mark.parametrize("new,cols,G,dtype", [
+    ([1_050_000], 64, 1, torch.float32), ([360_000], 64, 8, torch.bfloat16), ([108_000], 96, 64, torch.bfloat16),
+    ([40] * 1000 + [900_000, 3], 128, 2, torch.float16), ([5, 2_000_000, 0, 70], 3, 1, torch.bfloat16)])
+def test_far_more_new_tokens_than_the_table_has_keys(gdn, new, cols, G, dtype):
+    """Rows behind the table's end see all of its keys, each of them once, and every row is written.
+
+    All sequences share the table's pages; the value of key j is 1 in column (j / 16) mod 31 and in column 31.  A weight
+    is 1, o a count over a count: off by 3 roundings of 2^-24 and its own to the type."""
+    u = {torch.float32: 0.0, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}[dtype]
+    room, d, N, T = cols * 16, 32, len(new), sum(new)
+    say(f"behind the table: {N} sequences, {T} tokens, {room} keys")
+    every = torch.arange(room, device=DEV)
+    v = torch.zeros(room, d, device=DEV, dtype=dtype)
+    v[every, (every >> 4) % 31] = 1.0
+    v[:, 31] = 1.0
+    kv = v.view(cols, 1, 16, d).contiguous()
+    table = torch.arange(cols, dtype=torch.int32, device=DEV).repeat(N, 1)
+    lens = torch.tensor(new, dtype=torch.int32, device=DEV)
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).to(DEV)
+    o = torch.full((T, G, d), float("nan"), device=DEV, dtype=dtype)
+    gdn.gdn_cache_attention(torch.zeros_like(o), kv, kv.clone(), table, lens, cu_seqlens=cu, o=o)
+    place = torch.arange(T, device=DEV) - torch.repeat_interleave(cu[:-1].long(), lens.long(), output_size=T)
+    seen = place.clamp(max=room - 1) + 1
+    want = torch.zeros(room + 1, d, dtype=torch.float64, device=DEV)
+    want[1:] = v.double().cumsum(0) / (every + 1.0)[:, None].double()
+    for t in range(0, T, 100_000):
+        w, got = want[seen[t:t + 100_000]][:, None], o[t:t + 100_000].double()
+        off = ((got - w).abs() / ((3 * 2.0 ** -24 + u) * w).clamp(min=1e-300)).amax()
+        assert float(off) <= 1.0, (t, float(off))
