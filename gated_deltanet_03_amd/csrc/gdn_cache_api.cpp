@@ -214,7 +214,9 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   int64_t tokens = 0;
   gdn_status st = check_cache(sh, cu != nullptr, &tokens);
   if (st != GDN_OK) return st;
-  if (!(scale > 0.f) || scale == INFINITY) return fail(GDN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);     // weights are powers of two
+  if (!(scale > 0.f) || !(scale_log2 < INFINITY))
+    return fail(GDN_ERR_INVALID_ARG, "scale=%g must be > 0 and, times log2(e), finite", (double)scale);
   if (window < 0) return fail(GDN_ERR_INVALID_ARG, "window=%d < 0", window);
   if (tokens == 0 || sh->N == 0) return GDN_OK;
   Buf ins[6];
@@ -242,7 +244,7 @@ gdn_status gdn_cache_attention(const gdn_cache_shape* sh, const void* q, int64_t
   AttendArgs a{};
   a.c = cache_args(sh, table, lens, cu, tokens);
   a.q = q; a.q_stride = q_stride; a.k_cache = kc; a.v_cache = vc; a.o = o;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.window = std::min(window, 1 << 30);
   a.granules = sh->page_size / 16;
   a.granule_magic = ((1ull << 32) + a.granules - 1) / a.granules;

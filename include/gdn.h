@@ -526,7 +526,7 @@ gdn_status gdn_cache_append(const gdn_cache_shape* shape, const gdn_append_shape
  * maximum, at most 2^8) as operands of their product with v, and summed as rounded.
  *
  *  q, o       [tokens, Hq, d]; q at q_token_stride (elements), o contiguous.
- *  scale      finite and > 0.
+ *  scale      > 0; scale * log2(e) finite.
  *  workspace  gdn_cache_attention_workspace_bytes() bytes, 16-byte aligned, contents
  *             on entry ignored; may be NULL where that is 0.  Long sequences are split
  *             over their keys; the parts are joined in a fixed order.

@@ -291,3 +291,12 @@ def test_launches_on_the_tensors_device(monkeypatch):
     assert seen == [("x", 1001), "in", ("x", 1000), "out"] and entered == [torch.device("cuda", 0)]
     with pytest.raises(gdn.GdnError):
         gdn._launch(torch.device("cuda", 0), lambda *a: gdn.GDN_ERR_INVALID_ARG)
+
+
+def test_scales_beyond_the_largest_float(lib):
+    """scale is applied times log2(e) in fp32, which has to be finite too; the largest and smallest that are pass."""
+    top = 2.0 ** 128 * (1 - 2.0 ** -24)
+    for scale in (top, 0.99 * top, top / 1.44):
+        assert attend(lib, scale=scale) == INVALID and "scale" in last(lib), scale
+    for scale in (top / 1.4427, 1e-45):
+        assert attend(lib, scale=scale, q=NULL) == INVALID and "q is NULL" in last(lib), scale
