@@ -15,8 +15,11 @@
 // Keys and values come from global memory to LDS without passing registers (16 bytes a lane).  What is absent (keys
 // past the sequence's or the tile's end or before its window, numbers that are no page) is loaded from a block of zeros.
 //
-// m follows the maximum only when that has grown by more than 2^8: exp(s - m) is then at most 2^8, which 16-bit
-// operands hold, and most tiles leave the output accumulators alone.
+// m follows the maximum only when that has grown by more than 2^8 (fp16: 2^6): exp(s - m) is then at most that, which
+// 16-bit operands hold, and most tiles leave the output accumulators alone.  In fp16 weights are taken 2^7 times as
+// large, so up to 2^13 of 2^16: its numbers end at 2^-24, and many keys with small weights may outweigh the largest
+// (131072 keys of 2^-25 of it hold 2^-8 of the sum, and were 0); so the smallest is 2^-31 of the maximum's weight.
+// 2048 tokens over 16384 keys, 32 heads of 64: 358 us without, 360 so, 361 with growth of 2^4 and weights 2^8 times.
 #pragma once
 
 #include <algorithm>
@@ -407,9 +410,12 @@ struct Wave {
   static constexpr bool F32 = ES == 4;
   static constexpr int QN = D / (2 * E);            // 16-byte pieces of a query a lane holds
   static constexpr int DT = D / 32;
+  // How far scores may grow above m, and what weights are more than exp(s - m), as powers of two.
+  static constexpr bool F16 = __is_same(T, _Float16);
+  static constexpr float SLACK = F16 ? 6.f : 8.f, MORE = F16 ? 7.f : 0.f;
   uint4 q[QN];
   f32x16 o[DT];
-  float m, mc, l;      // m in score units, mc = m * scale (0 while m = -infinity), l of this lane's keys
+  float m, mc, l;      // m in score units, mc = m * scale - MORE (0 while m = -infinity), l of this lane's keys
   int lo, hi;          // the keys this lane's query sees: lo <= key <= hi
   int lane;
 
@@ -482,13 +488,13 @@ struct Wave {
     }
   }
 
-  // The running maximum takes `top` (of this lane's keys) in.  Weights are taken against m * scale as rounded, so the
-  // factors between maxima are too (contracted, or of (m - n) * scale, they would be off by 2^-24 of the maximum itself).
+  // The running maximum takes `top` (of this lane's keys) in.  Weights are taken against mc as rounded, so the factors
+  // between maxima are too (contracted, or of (m - n) * scale, they would be off by 2^-24 of the maximum itself).
   __device__ __forceinline__ void raise(float top, float c, float slack) {
 #pragma clang fp contract(off)
     top = other_half_max(top);
     if (__ballot(top > m + slack || (m == -INFINITY && top > m)) == 0) return;
-    const float n = fmaxf(m, top), nc = n * c;
+    const float n = fmaxf(m, top), nc = n * c - MORE;
     const float f = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mc - nc);
     m = n;
     mc = n == -INFINITY ? 0.f : nc;
@@ -929,7 +935,7 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
   extern __shared__ __align__(16) unsigned char smem[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
-  const float c = a.scale_log2, slack = 8.f / c;
+  const float c = a.scale_log2, slack = Wave<T, D>::SLACK / c;
   const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem;
   walk<false>(a, G, head, (int)(blockIdx.x / a.c.Hkv), [&](const Piece& u, int from, int to, bool whole, int slot) {
     const int lane = fresh_lane(), h = lane >> 5;
@@ -1155,7 +1161,7 @@ void cache_attention_few_kernel(AttendArgs a) {
   __shared__ float2 ml[NW][32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int G = a.c.Hq / a.c.Hkv, head = (int)(blockIdx.x % a.c.Hkv);
-  const float c = a.scale_log2, slack = 8.f / c;
+  const float c = a.scale_log2, slack = Wave<T, D>::SLACK / c;
   unsigned char* K = smem + wave * 64 * RB;
   unsigned char* V = K + 32 * RB;
   const uint32_t ldsK = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)smem + wave * 64 * RB;

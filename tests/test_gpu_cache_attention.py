@@ -336,3 +336,33 @@ def test_offsets_beyond_32_bits(gdn):
     c = dict(q=q.cpu(), kc=small[0], vc=small[1], table=torch.tensor([[0, 1, 2]], dtype=torch.int32),
              lens=torch.tensor([2100]), cu=torch.tensor([0, 1]), scale=d ** -0.5, dtype="bf16")
     check(o[0], oracle(c), c, "o")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("octaves", [24, 25, 26])
+def test_one_key_above_a_hundred_thousand(gdn, octaves, new, dtype):
+    """Weights of 2^-24 to 2^-26 of the largest: 2^-7 to 2^-9 of the sum together.
+
+    Bound: o's and the weights' rounding, u each; below fp16's normal numbers 2^-32 of the largest weight a key, above and
+    below; the score of the large key, 26 octaves, through its factor and the exponential 64 e; and sums: 16 keys go into
+    one addition to an accumulator (in fp32 two, but one sequence of so many keys is cut into far more than eight parts),
+    so n / 16 + 64 roundings of it, above and below."""
+    d, n = 32, 131072
+    c = make(67, [new], [n], 1, 1, d, 1024, dtype)
+    c["q"][:] = 0
+    c["q"][..., 0] = 8.0
+    c["kc"][:] = 0.0
+    where = c["table"][0, 3]
+    c["kc"][where, 0, 5, 0] = octaves * math.log(2.0) / (8.0 * c["scale"])
+    c["vc"][:] = 1.0
+    c["vc"][where, 0, 5] = -1.0
+    gap = float(c["kc"][where, 0, 5, 0]) * 8.0 * c["scale"]                # as rounded to the type
+    rest = (n - 1 - torch.arange(new - 1, -1, -1, dtype=torch.float64)) * math.exp(-gap)
+    want = ((rest - 1) / (rest + 1))[:, None, None].expand(-1, 1, d).numpy()
+    u = {"f32": E, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    share = float(rest.max())                                              # of the sum, where weights are rounded
+    bound = u * np.abs(want) + 2 * (share * u + n * 2.0 ** -32 * (dtype == "f16") + 64 * E * share + (n / 16 + 64) * E)
+    err = np.abs(f64(call(gdn, c)) - want)
+    say(f"  2^-{octaves} {dtype} {new}: {err.max():.2e}, bound {bound.max():.2e}, share {share:.2e}")
+    assert (err <= bound).all()
