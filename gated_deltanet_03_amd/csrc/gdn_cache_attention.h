@@ -459,21 +459,28 @@ struct Wave {
 
   // Scores of 32 keys.  fp32 adds two products at a time, d / 2 roundings in a row: four sums instead of one bring the
   // error of o against 64 bits from 4.6e-7 to 2.8e-7 (d = 64) and 9.0e-7 to 3.7e-7 (256), for 1% of the time.
+  // Where they are made in turn with exponentials, two: 8.4e-7 to 5.2e-7 (300 tokens over 700 keys, d = 256) for 0.3 to
+  // 0.9% of the time; four would bring 3.9e-7, but cost 2 to 4% in vector operations there.
+  template <int N>
+  struct Sums {
+    f32x16 s[N];
+    __device__ __forceinline__ Sums() {
+#pragma unroll
+      for (int n = 0; n < N; ++n) s[n] = zeros();
+    }
+    __device__ __forceinline__ void join(int i) {      // key i's, left in s[0]
+      if constexpr (N > 1) s[0][i] += s[1][i];
+      if constexpr (N > 2) s[0][i] += s[2][i] + s[3][i];
+    }
+  };
   __device__ __forceinline__ f32x16 scores(const unsigned char* K, int r0) const {
     constexpr int SUMS = !F32 ? 1 : D <= 32 ? 2 : 4;
-    f32x16 s[SUMS];
+    Sums<SUMS> x;
 #pragma unroll
-    for (int n = 0; n < SUMS; ++n) s[n] = zeros();
+    for (int t = 0; t < QN; ++t) add_product(x.s[t % SUMS], key_piece(K, r0, t), t);
 #pragma unroll
-    for (int t = 0; t < QN; ++t) add_product(s[t % SUMS], key_piece(K, r0, t), t);
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[0][i] += s[1][i];
-        if constexpr (SUMS > 2) s[0][i] += s[2][i] + s[3][i];
-      }
-    }
-    return s[0];
+    for (int i = 0; i < 16; ++i) x.join(i);
+    return x.s[0];
   }
 
   // -infinity where the query does not see the key; key0: key of row 0, gone: bit g set where 16 rows have no page.
@@ -1048,23 +1055,22 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
       auto step = [&](int i, auto more) {
         using W = Wave<T, D>;
         constexpr int AHEAD = 3;                     // LDS reads in flight
+        constexpr int SUMS = W::F32 ? 2 : 1;
         unsigned char* V = smem + (2 + (i & 1)) * KT * RB;
         const unsigned char* K = smem + ((i + 1) & 1) * KT * RB;
         w.raise(top, c, slack);
-        f32x16 x[S::NS];
+        typename W::template Sums<SUMS> x[S::NS];
         typename W::Weights p[S::NS];
         if constexpr (more.value) {
           constexpr int N = S::NS * W::QN, PAIRS = 8 * S::NS;
           uint4 k[AHEAD + 1];
-#pragma unroll
-          for (int n = 0; n < S::NS; ++n) x[n] = W::zeros();
 #pragma unroll
           for (int t = 0; t < AHEAD; ++t) k[t] = w.key_piece(K, 32 * (t / W::QN), t % W::QN);
 #pragma unroll
           for (int t = 0; t < N; ++t) {
             if (t + AHEAD < N)
               k[(t + AHEAD) % (AHEAD + 1)] = w.key_piece(K, 32 * ((t + AHEAD) / W::QN), (t + AHEAD) % W::QN);
-            w.add_product(x[t / W::QN], k[t % (AHEAD + 1)], t % W::QN);
+            w.add_product(x[t / W::QN].s[t % SUMS], k[t % (AHEAD + 1)], t % W::QN);
 #pragma unroll
             for (int e = t * PAIRS / N; e < (t + 1) * PAIRS / N; ++e) {
               w.weigh_two(p[e / 8], s[e / 8], e % 8 * 2, c);
@@ -1092,7 +1098,11 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
 #pragma unroll
           for (int e = t * PAIRS / N; e < (t + 1) * PAIRS / N; ++e) {
             part[e / 8] = W::add_two(part[e / 8], p[e / 8], e % 8 * 2);
-            if constexpr (more.value) high = fmaxf(fmaxf(high, x[e / 8][e % 8 * 2]), x[e / 8][e % 8 * 2 + 1]);
+            if constexpr (more.value) {
+              x[e / 8].join(e % 8 * 2);
+              x[e / 8].join(e % 8 * 2 + 1);
+              high = fmaxf(fmaxf(high, x[e / 8].s[0][e % 8 * 2]), x[e / 8].s[0][e % 8 * 2 + 1]);
+            }
             asm volatile("" : "+v"(part[e / 8]), "+v"(high));
           }
           __builtin_amdgcn_sched_barrier(0);
@@ -1101,7 +1111,7 @@ __global__ __launch_bounds__(256, (many_waves(D * (int)sizeof(T)))) void cache_a
         for (int n = 0; n < S::NS; ++n) w.l += part[n];
         if constexpr (more.value) {
 #pragma unroll
-          for (int n = 0; n < S::NS; ++n) s[n] = x[n];
+          for (int n = 0; n < S::NS; ++n) s[n] = x[n].s[0];
           top = high;
         }
       };

@@ -366,3 +366,23 @@ def test_one_key_above_a_hundred_thousand(gdn, octaves, new, dtype):
     err = np.abs(f64(call(gdn, c)) - want)
     say(f"  2^-{octaves} {dtype} {new}: {err.max():.2e}, bound {bound.max():.2e}, share {share:.2e}")
     assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("d", [32, 64, 128, 256])
+@pytest.mark.parametrize("new", [1, 60])
+def test_fp32_is_as_near_as_its_sums(gdn, new, d):
+    """The error of o in fp32 as a whole, as roundings that are independent of each other add up (a third of e^2 each).
+
+    A score of n sums (four; two for heads of 32, and where 128-row tiles are computed by one wave a SIMD, heads of 128 and
+    more) has m = d / 2n roundings in each.  Scores are normal with s = 1.5, the squares of the weights lie about 2 s^2:
+    the m partial sums add s^2 m / 2 by chance and (2 s^2)^2 m / 3n by their drift.  Sums over K keys, two at a time: K / 4.
+    The exponential, its argument, the factor 1 / l and o's own rounding: 27."""
+    ctx = [200] * 16
+    c = make(73 + d, [new] * 16, ctx, 8, 2, d, 16, "f32")
+    want = plain(c)["o"]
+    n = 2 if d == 32 or (new > 1 and d >= 128) else 4
+    m = d / (2 * n)
+    bound = E * math.sqrt((1.5 ** 2 * m / 2 + 4.5 ** 2 * m / (3 * n) + ctx[0] / 4 + 27) / 3)
+    err = np.linalg.norm(f64(call(gdn, c)) - want) / np.linalg.norm(want)
+    say(f"  {new} tokens, d = {d}: {err:.2e} of {bound:.2e}")
+    assert err <= bound
