@@ -195,3 +195,23 @@ def test_copy_pages_beyond_32_bits(gdn):
     gdn.gdn_cache_copy_pages(big, other, torch.tensor([1190], dtype=torch.int32, device=DEV),
                              torch.tensor([2], dtype=torch.int32, device=DEV))
     assert (big[2] == 3.0).all() and (other[2] == 4.0).all() and not big[:2].any() and not big[3:1190].any()
+
+
+def test_the_largest_vocabulary_and_beams(gdn):
+    """2^24 tokens: more entries are left for the join than its threads hold; the best ones spread over all of it."""
+    V, W, K = 1 << 24, 3, 64
+    x = torch.zeros(1, W, V, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    at = torch.randperm(V, generator=g, device=DEV)[:100]
+    x[0, 0, at[:50]], x[0, 2, at[50:]] = 8.0, 9.0
+    x[0, 1, V - 1], x[0, 1, 0] = 16.0, 15.5
+    s = torch.tensor([[-1.0, -3.0, -2.0]], device=DEV)
+    tokens, parents, best, done = gdn.gdn_beam_select(x, s, beams=K, eos_token=V - 1)
+    ls = [math.log(V - 50 + 50 * math.exp(8.0)), math.log(V - 2 + math.exp(16.0) + math.exp(15.5)),
+          math.log(V - 50 + 50 * math.exp(9.0))]
+    every = [(-(-1.0 - ls[0] + 8.0), 0, t) for t in at[:50].tolist()] + [(-(-2.0 - ls[2] + 9.0), 2, t) for t in at[50:].tolist()]
+    every += [(-(-3.0 - ls[1] + 16.0), 1, V - 1), (-(-3.0 - ls[1] + 15.5), 1, 0)]
+    every = sorted(every)[:K]
+    assert tokens[0].tolist() == [t for _, _, t in every] and parents[0].tolist() == [w for _, w, _ in every]
+    assert np.abs(f64(best)[0] + np.array([c for c, _, _ in every])).max() <= 2.0 ** -24 * 20 + 2.0 ** -22
+    assert done[0].tolist() == [t == V - 1 for _, _, t in every]

@@ -386,3 +386,14 @@ def test_fp32_is_as_near_as_its_sums(gdn, new, d):
     err = np.linalg.norm(f64(call(gdn, c)) - want) / np.linalg.norm(want)
     say(f"  {new} tokens, d = {d}: {err:.2e} of {bound:.2e}")
     assert err <= bound
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", [
+    ([1], [700], 256, 1, 32), ([1, 3], [40, 900], 256, 1, 128), ([9], [400], 510, 2, 64), ([1, 1], [600, 77], 1000, 1000, 32),
+    ([37, 40], [600, 40], 800, 800, 32), ([2], [300], 1537, 1537, 256)])
+def test_very_many_heads(gdn, new, ctx, Hq, Hkv, d, dtype):
+    """The most query heads a key head can have (more than a tile of rows), and more key heads than the card has workgroups."""
+    c = make(79 + Hq, new, ctx, Hq, Hkv, d, 16, dtype)
+    say(f"heads {dtype} {Hq} on {Hkv} of {d}, {new} {ctx}")
+    check(call(gdn, c), oracle(c), c, "o")
