@@ -110,6 +110,12 @@ CacheArgs cache_args(const gdn_cache_shape* sh, const int32_t* table, const int3
 }
 
 // How the attention of a call is cut: rows of a tile, shares of a head's work (0: a tile each).
+//
+// Few rows or many is one choice for a call, by its rows a sequence on average: the host does not know the lengths.
+// Tiles of 32 and of 128 rows, 32 on 8 heads of 128, bf16: 16 sequences over 4096 keys with 8 tokens 54 and 67 us, 16
+// tokens 55 and 71, 24 tokens 135 and 76; 64 over 1000 keys with 8 tokens 51 and 55, 10 tokens 57 and 55.  Single tokens
+// beside a chunk: where the rule takes 32 rows, 64 over 2048 keys and 440 tokens 115 and 126 us, 32 over 4000 and 200 over
+// 2000 115 and 127; where it takes 128, 32 over 4000 and 300 over 2000 119 and 131, and 1000 over 4000 190 and 162.
 struct Plan {
   int32_t few, shares, rows, unit;
   int64_t tiles;

@@ -3,8 +3,9 @@
 // A copy, bound by memory.  A thread holds one 16-byte column of all rows of one group: it loads the group's rows
 // before it stores any of them, so a group may be permuted in place without a second buffer, and entries that stay
 // where they are cost nothing.  Groups of more than 16 rows take narrower columns, so that the rows of one column
-// still fit the registers.  4 layers of 32 states of 2 MB, 4 a group, random parents, in place: 54 us; pages of 128 KB of
-// keys and of values, 8 a group, 16 groups: 11 us.
+// still fit the registers.  4 layers of 32 states of 2 MB, 4 a group, parents at random but in order (221 MB
+// to read and write), in place: 54 us, 4.1 TB/s where a copy has 5.1; pages of 128 KB of keys and of values, 8 a group, 16
+// groups (35 MB): 11 us.
 #include <algorithm>
 
 #include "gdn_cache_internal.h"

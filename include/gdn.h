@@ -523,9 +523,12 @@ gdn_status gdn_cache_append(const gdn_cache_shape* shape, const gdn_append_shape
  *
  * Precision: scores, the running maximum and all sums in fp32, o rounded once; for
  * 16-bit inputs the weights are rounded to the input type (against a running
- * maximum, at most 2^8) as operands of their product with v, and summed as rounded.
+ * maximum, at most 2^8) as operands of their product with v, and summed as rounded,
+ * two at a time in steps that were seen to be off by at most 1.4 units of fp32's last
+ * place (or 2^-37; the largest weight is at least 1).
  * fp16 keeps weights down to 2^-31 of the row's largest, each off by 2^-32 of that at
- * most where it is below 2^-21 of it.
+ * most where it is below 2^-21 of it.  Scores times log2(e) beyond 2^24, where fp32 has
+ * no fractions for them, may give NaN.
  *
  *  q, o       [tokens, Hq, d]; q at q_token_stride (elements), o contiguous.
  *  scale      > 0; scale * log2(e) finite.

@@ -397,3 +397,25 @@ def test_very_many_heads(gdn, new, ctx, Hq, Hkv, d, dtype):
     c = make(79 + Hq, new, ctx, Hq, Hkv, d, 16, dtype)
     say(f"heads {dtype} {Hq} on {Hkv} of {d}, {new} {ctx}")
     check(call(gdn, c), oracle(c), c, "o")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_scores_of_millions(gdn, new, dtype):
+    """Whole scores up to 2^23, 2^15 apart: o is the best key's value, off by the roundings of its weight, their sum, the
+    factor, the product and o itself."""
+    n, d = 250, 32
+    c = make(83, [new], [n], 2, 1, d, 16, dtype)
+    rank = np.random.default_rng(83).permutation(n)
+    c["q"][:] = 0.0
+    c["q"][..., 0] = 4096.0
+    for j in range(n):
+        c["kc"][c["table"][0, j // 16], 0, j % 16] = 0.0
+        c["kc"][c["table"][0, j // 16], 0, j % 16, 0] = 8.0 * (rank[j] + 1)
+    c["scale"] = 1.0
+    o = f64(call(gdn, c))
+    u = {"f32": E, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    for t in range(new):
+        best = int(np.argmax(rank[:n - new + t + 1]))
+        v = f64(c["vc"][c["table"][0, best // 16], 0, best % 16])
+        assert (np.abs(o[t] - v) <= (u + 4 * E) * np.abs(v)).all(), (t, best)
