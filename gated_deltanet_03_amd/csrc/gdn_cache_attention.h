@@ -117,9 +117,9 @@ __device__ __forceinline__ int wave_sum(int x) { return lane_value(wave_scan(x),
 //
 // The tiles of all sequences lie on one line, a tile about as long as the keys it sees and what starting one costs,
 // in units of 2^unit keys that the host chooses so that the line is shorter than 2^30: v_i = first + step * i for
-// tile i of a sequence, never more than twice the table's keys. The first workgroups take whole tiles, one each; what is left of the line is cut into
-// `shares` even pieces, whatever the sequences' lengths are: the rest of one tile, whole tiles, the beginning of one
-// more. Pieces that are not whole tiles go to the workspace and are joined.
+// tile i of a sequence, never more than twice the table's keys. The first workgroups take whole tiles, one each; what
+// is left of the line is cut into `shares` even pieces, whatever the sequences' lengths are: the rest of one tile, whole
+// tiles, the beginning of one more. Pieces that are not whole tiles go to the workspace and are joined.
 //
 // Nothing is cut where that would end no later.  Whole tiles end with the longest one, or with as many rounds as
 // there are tiles for a share, of average ones; cut ones with an even share and what the pieces and their join cost:
